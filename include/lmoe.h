@@ -357,6 +357,135 @@ int latent_moe_forward_mxfp4(const lmoe_dims* dims, const lmoe_weights* weights,
 /* Kernel launches of latent_moe_forward_mxfp4 (0 on invalid dims).         */
 int latent_moe_launch_count_mxfp4(const lmoe_dims* dims, int has_shared_expert);
 
+/* ------------------------------------------------------------------------ */
+/* 8-bit (e4m3) products with a scale per block of 128.                      */
+/*                                                                            */
+/* A matrix [rows, K] is held as codes, one OCP E4M3 byte an element (4      */
+/* exponent bits with bias 7, 3 mantissa bits, no infinities, largest value  */
+/* 448, 0x7F / 0xFF NaN), and fp32 scales: for token rows one per row and 128 */
+/* columns, [rows, ceil(K/128)]; for weights one per 128 x 128 block,         */
+/* [ceil(rows/128), ceil(K/128)]; value = code * scale.  A last block may be */
+/* partial in either direction.                                              */
+/*                                                                            */
+/* lmoe_quantize_fp8: bf16 x [rows, K] -> codes and scales.  block_rows = 1   */
+/* (token rows) or 128 (weights).  For every block, in fp32, each operation  */
+/* rounded once:                                                              */
+/*   a = max(max |x| over the block, 2^-100)                                 */
+/*   scale = a / 448;   code = e4m3(x * (448 / a))   (to nearest, ties even)  */
+/* A block of zeros gets codes 0.  A block that holds a NaN or an infinity   */
+/* has that for its scale (its values are lost).                             */
+/* Requires K % 16 == 0, rows >= 0 and at most 2^31 - 1 row blocks of 128    */
+/* columns (rows * ceil(K/128)).                                              */
+/* ------------------------------------------------------------------------ */
+int lmoe_quantize_fp8(const lmoe_bf16* x, uint8_t* codes, float* scales, int64_t rows, int K,
+                      int block_rows, void* stream);
+
+/* out[t, n] = bf16( sum_kb xs[t, kb] * ws[n/128, kb] * P_kb[t, n] (+ add[t, n]) ) */
+/*   P_kb[t, n] = sum of x[t, c] * w[n, c] over the 128 columns c of block kb */
+/* x [T, K] codes with xs [T, ceil(K/128)]; w [N, K] codes with ws            */
+/* [ceil(N/128), ceil(K/128)] (PyTorch Linear layout); add [T, N] bf16 or     */
+/* NULL; out [T, N] bf16.  Block sums on the tensor cores with fp32          */
+/* accumulation, their scaled sum and the addend in fp32, one rounding.      */
+/* Requires K % 16 == 0, N % 8 == 0, T >= 0.  No workspace.  Repeated calls   */
+/* give the same bits.  Unlike lmoe_linear's, the weights are read in stream */
+/* order: a preceding call on `stream` may write them.                       */
+int lmoe_linear_fp8(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws,
+                    const lmoe_bf16* add, lmoe_bf16* out, int T, int N, int K, void* stream);
+
+/* Routed experts in e4m3 (row order as lmoe_weights.w13 / w2).              */
+typedef struct lmoe_fp8_experts {
+  const uint8_t* w13_codes;  /* [E, 2d, L]                                   */
+  const float* w13_scales;   /* [E, 2d/128, L/128]                           */
+  const uint8_t* w2_codes;   /* [E, L, d]                                    */
+  const float* w2_scales;    /* [E, L/128, d/128]                            */
+} lmoe_fp8_experts;
+
+/* The routed experts on token rows grouped by expert: expert e owns rows     */
+/* expert_offsets[e] .. expert_offsets[e+1] - 1 of x, and for each of them   */
+/*   h   = x W13_e^T                     (block-scaled, fp32)                 */
+/*   act = SituGLU(h), as e4m3 with one scale per row and 128 features       */
+/*         (the rule of lmoe_quantize_fp8 on the fp32 values; SituGLU's tanh */
+/*         factors come from the hardware tanh, about 2^-16 relative)         */
+/*   y   = bf16(act W2_e^T)              (block-scaled, fp32 sum)             */
+/* x [rows, latent] codes with xs [rows, latent/128]; expert_offsets [E+1]   */
+/* int32 on the device, ascending, within [0, rows] (entries outside are     */
+/* clamped on the device; a row that no expert owns is left untouched);      */
+/* y [rows, latent] bf16.  Requires 1 <= E <= 1024, latent % 128 == 0,         */
+/* inter % 128 == 0, latent and inter <= 8192, 0 <= rows <= 2^27.             */
+/* The workspace (lmoe_experts_fp8_workspace_bytes, 256-byte aligned) holds  */
+/* act.                                                                       */
+size_t lmoe_experts_fp8_workspace_bytes(int64_t rows, int E, int latent, int inter);
+int lmoe_experts_fp8(const lmoe_fp8_experts* experts, const uint8_t* x, const float* xs,
+                     const int32_t* expert_offsets, lmoe_bf16* y, int64_t rows, int E, int latent,
+                     int inter, float beta, float linear_beta, void* workspace,
+                     size_t workspace_bytes, void* stream);
+
+/* The layer forward with e4m3 routed experts: latent_moe_forward with        */
+/* weights->w13 and weights->w2 unused (may be NULL), the expert-major rows   */
+/* of Z quantised per 128 columns and the experts run as lmoe_experts_fp8.   */
+/* Everything else, the workspace offsets among it, is latent_moe_forward's  */
+/* (entries A, G and act of the workspace hold no data above 128 tokens).    */
+/* Limits: those of latent_moe_forward, inter % 128 == 0, inter <= 8192 and   */
+/* T * topk <= 2^27.  The four expert pointers are required (LMOE_ERR_NULL),  */
+/* 16-byte aligned (LMOE_ERR_ALIGN) device memory (LMOE_ERR_DEVICE).         */
+size_t latent_moe_workspace_bytes_fp8(const lmoe_dims* dims);
+int latent_moe_forward_fp8(const lmoe_dims* dims, const lmoe_weights* weights,
+                           const lmoe_fp8_experts* experts, const lmoe_bf16* hidden,
+                           const float* router_logits, lmoe_bf16* out, void* workspace,
+                           size_t workspace_bytes, const lmoe_debug* dbg, void* stream);
+
+/* Kernel launches of latent_moe_forward_fp8 (0 on invalid dims).            */
+int latent_moe_launch_count_fp8(const lmoe_dims* dims, int has_shared_expert);
+
+/* ------------------------------------------------------------------------ */
+/* Training of the router: its balance loss and the gradient of its logits.  */
+/*                                                                            */
+/*   s[t,e] = sigmoid(router_logits[t,e]);   q[t,e] = s[t,e] / sum_e s[t,e]   */
+/*   c[b,e] = how often the valid tokens of sequence b chose expert e        */
+/*   n_b    = valid tokens of sequence b                                      */
+/*   f[b,e] = E / (topk * n_b) * c[b,e];   P[b,e] = mean of q[t,e] over them  */
+/*   loss   = alpha * (1/S) sum_b sum_e f[b,e] P[b,e]                        */
+/* (a sequence without valid tokens adds 0; S counts it).                    */
+/* router_logits [T, E] fp32; topk_ids [T, topk] int32 as moe_route writes    */
+/* them (an id outside [0, E) is a dropped choice: not counted);              */
+/* token_mask [T] bytes or NULL: 0 marks a token that does not count          */
+/* (padding); seq_offsets [S+1] int32 on the device, ascending from 0 to T,   */
+/* or NULL with S = 1: sequence b is the tokens seq_offsets[b] ..             */
+/* seq_offsets[b+1] - 1 (a token outside all of them does not count).        */
+/* Outputs: loss [1] fp32, expert_counts [S, E] int32 (c), seq_tokens [S]     */
+/* int32 (n_b).  Logits of -infinity are experts of score 0; where all of a  */
+/* row are, the token adds 0.  NaN logits give a NaN loss.  Sums are fp32 in a */
+/* fixed order: repeated calls give the same bits.                           */
+/* Limits: those of moe_route on E and topk, T * topk <= 2^31 - 1,            */
+/* 1 <= S <= 65536, alpha finite.  T == 0 writes nothing.                     */
+/* ------------------------------------------------------------------------ */
+size_t moe_balance_loss_workspace_bytes(int T, int E, int S);
+int moe_balance_loss(const float* router_logits, const int32_t* topk_ids,
+                     const uint8_t* token_mask, const int32_t* seq_offsets, int T, int E, int topk,
+                     int S, float alpha, float* loss, int32_t* expert_counts, int32_t* seq_tokens,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* grad_logits[t, e] (every element written) = the sum of                     */
+/*  - with grad_topk_weights [T, topk] fp32 (else NULL): the gradient through  */
+/*    moe_route's weights, at the chosen experts i = topk_ids[t, j], with      */
+/*    p_j = s_j / (sum of the token's chosen s):                              */
+/*      rsf * (g_j - sum_m g_m p_m) * p_j * (1 - s_j)    renormalize != 0     */
+/*      rsf * g_j * s_j * (1 - s_j)                      renormalize == 0     */
+/*    (the ids of a token must be distinct; dropped choices take no part; the */
+/*    selection itself has no gradient; every token takes part, masked or not) */
+/*  - with grad_loss [1] fp32 on the device (else NULL): grad_loss * the       */
+/*    gradient of moe_balance_loss, the counts taken as constants:            */
+/*      alpha / (S n_b) * (f[b,e] - sum_e' f[b,e'] q[t,e']) * q[t,e] * (1 - s) */
+/*    from the expert_counts and seq_tokens that moe_balance_loss wrote for    */
+/*    the same arguments (required then; unused otherwise).                  */
+/* At least one of the two gradients is required (LMOE_ERR_NULL).            */
+int moe_router_backward(const float* router_logits, const int32_t* topk_ids,
+                        const float* grad_topk_weights, int renormalize,
+                        float routed_scaling_factor, const float* grad_loss,
+                        const int32_t* expert_counts, const int32_t* seq_tokens, float alpha,
+                        const uint8_t* token_mask, const int32_t* seq_offsets, int T, int E,
+                        int topk, int S, float* grad_logits, void* stream);
+
 /* The layer forward without a caller workspace.  The pages have no          */
 /* counterpart to this entry point; it exists for callers that cannot         */
 /* allocate device memory: a plugin that an inference runtime calls with only */

@@ -12,4 +12,8 @@ from ._binding import (  # noqa: F401
     lmoe_router_logits, lmoe_router_logits_workspace_bytes, latent_moe_forward_router,
     latent_moe_launch_count_router, LmoeMxfp4Experts, lmoe_dequant_mxfp4, make_mxfp4_experts,
     latent_moe_workspace_bytes_mxfp4, latent_moe_forward_mxfp4, latent_moe_launch_count_mxfp4,
+    LmoeFp8Experts, make_fp8_experts, lmoe_quantize_fp8, lmoe_linear_fp8, lmoe_experts_fp8,
+    lmoe_experts_fp8_workspace_bytes, latent_moe_workspace_bytes_fp8, latent_moe_forward_fp8,
+    latent_moe_launch_count_fp8, moe_balance_loss, moe_balance_loss_workspace_bytes,
+    moe_router_backward,
 )

@@ -33,7 +33,11 @@ ABI_FUNCTIONS = ("moe_route", "situ_and_mul", "masked_situ_and_mul", "latent_moe
                  "lmoe_router_logits", "lmoe_router_logits_workspace_bytes",
                  "latent_moe_forward_router", "latent_moe_launch_count_router",
                  "lmoe_dequant_mxfp4", "latent_moe_workspace_bytes_mxfp4",
-                 "latent_moe_forward_mxfp4", "latent_moe_launch_count_mxfp4")
+                 "latent_moe_forward_mxfp4", "latent_moe_launch_count_mxfp4",
+                 "lmoe_quantize_fp8", "lmoe_linear_fp8", "lmoe_experts_fp8",
+                 "lmoe_experts_fp8_workspace_bytes", "latent_moe_workspace_bytes_fp8",
+                 "latent_moe_forward_fp8", "latent_moe_launch_count_fp8",
+                 "moe_balance_loss", "moe_balance_loss_workspace_bytes", "moe_router_backward")
 
 
 class LmoeError(RuntimeError):
@@ -58,6 +62,11 @@ class LmoeWeights(ctypes.Structure):
 
 
 class LmoeMxfp4Experts(ctypes.Structure):
+    _fields_ = [("w13_codes", ctypes.c_void_p), ("w13_scales", ctypes.c_void_p),
+                ("w2_codes", ctypes.c_void_p), ("w2_scales", ctypes.c_void_p)]
+
+
+class LmoeFp8Experts(ctypes.Structure):
     _fields_ = [("w13_codes", ctypes.c_void_p), ("w13_scales", ctypes.c_void_p),
                 ("w2_codes", ctypes.c_void_p), ("w2_scales", ctypes.c_void_p)]
 
@@ -141,6 +150,31 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.latent_moe_forward_mxfp4.restype = i32
     lib.latent_moe_launch_count_mxfp4.argtypes = [ctypes.POINTER(LmoeDims), i32]
     lib.latent_moe_launch_count_mxfp4.restype = i32
+    lib.lmoe_quantize_fp8.argtypes = [vp, vp, vp, i64, i32, i32, vp]
+    lib.lmoe_quantize_fp8.restype = i32
+    lib.lmoe_linear_fp8.argtypes = [vp, vp, vp, vp, vp, vp, i32, i32, i32, vp]
+    lib.lmoe_linear_fp8.restype = i32
+    lib.lmoe_experts_fp8_workspace_bytes.argtypes = [i64, i32, i32, i32]
+    lib.lmoe_experts_fp8_workspace_bytes.restype = ctypes.c_size_t
+    lib.lmoe_experts_fp8.argtypes = [ctypes.POINTER(LmoeFp8Experts), vp, vp, vp, vp, i64, i32, i32,
+                                     i32, f32, f32, vp, ctypes.c_size_t, vp]
+    lib.lmoe_experts_fp8.restype = i32
+    lib.latent_moe_workspace_bytes_fp8.argtypes = [ctypes.POINTER(LmoeDims)]
+    lib.latent_moe_workspace_bytes_fp8.restype = ctypes.c_size_t
+    lib.latent_moe_forward_fp8.argtypes = [ctypes.POINTER(LmoeDims), ctypes.POINTER(LmoeWeights),
+                                           ctypes.POINTER(LmoeFp8Experts), vp, vp, vp, vp,
+                                           ctypes.c_size_t, ctypes.POINTER(LmoeDebug), vp]
+    lib.latent_moe_forward_fp8.restype = i32
+    lib.latent_moe_launch_count_fp8.argtypes = [ctypes.POINTER(LmoeDims), i32]
+    lib.latent_moe_launch_count_fp8.restype = i32
+    lib.moe_balance_loss_workspace_bytes.argtypes = [i32, i32, i32]
+    lib.moe_balance_loss_workspace_bytes.restype = ctypes.c_size_t
+    lib.moe_balance_loss.argtypes = [vp, vp, vp, vp, i32, i32, i32, i32, f32, vp, vp, vp, vp,
+                                     ctypes.c_size_t, vp]
+    lib.moe_balance_loss.restype = i32
+    lib.moe_router_backward.argtypes = [vp, vp, vp, i32, f32, vp, vp, vp, f32, vp, vp, i32, i32,
+                                        i32, i32, vp, vp]
+    lib.moe_router_backward.restype = i32
     _lib = lib
     return lib
 
@@ -510,3 +544,173 @@ def latent_moe_launch_count_mxfp4(dims, has_shared_expert: bool = True) -> int:
     dd = dims if isinstance(dims, LmoeDims) else make_dims(dims)
     return int(load_library().latent_moe_launch_count_mxfp4(ctypes.byref(dd),
                                                              1 if has_shared_expert else 0))
+
+
+# --- 8-bit (e4m3) block-scaled products ------------------------------------------
+
+_E4M3 = (torch.uint8, torch.float8_e4m3fn)   # e4m3 codes, as bytes or as torch's type
+
+
+def _blocks(n: int) -> int:
+    return -(-n // 128)
+
+
+def lmoe_quantize_fp8(x, codes, scales, block_rows: int = 1, stream=None, rows: int | None = None,
+                      K: int | None = None):
+    """codes [rows, K] e4m3 and scales [ceil(rows/block_rows), ceil(K/128)] fp32 of a
+    bf16 x [rows, K]; block_rows 1 (token rows) or 128 (weights)."""
+    if rows is None:
+        K = x.shape[-1]
+        rows = x.numel() // K
+    rows, K, b = int(rows), int(K), int(block_rows)
+    st = load_library().lmoe_quantize_fp8(
+        _dev(x, "x", _BF16, rows * K), _dev(codes, "codes", _E4M3, rows * K),
+        _dev(scales, "scales", torch.float32, -(-rows // max(b, 1)) * _blocks(K)), rows, K, b,
+        _stream(stream))
+    _check(st, "lmoe_quantize_fp8")
+
+
+def lmoe_linear_fp8(x, xs, w, ws, out, add=None, stream=None, T: int | None = None,
+                    N: int | None = None, K: int | None = None):
+    """out [T,N] = bf16(x @ w^T (+ add)) for e4m3 x [T,K] with scales xs
+    [T, ceil(K/128)] and w [N,K] with scales ws [ceil(N/128), ceil(K/128)]."""
+    if T is None:
+        T, K = x.shape
+        N = w.shape[0]
+    T, N, K = int(T), int(N), int(K)
+    st = load_library().lmoe_linear_fp8(
+        _dev(x, "x", _E4M3, T * K), _dev(xs, "xs", torch.float32, T * _blocks(K)),
+        _dev(w, "w", _E4M3, N * K), _dev(ws, "ws", torch.float32, _blocks(N) * _blocks(K)),
+        _dev(add, "add", _BF16, T * N), _dev(out, "out", _BF16, T * N), T, N, K, _stream(stream))
+    _check(st, "lmoe_linear_fp8")
+
+
+def make_fp8_experts(q: dict, dims=None, E: int | None = None, latent: int | None = None,
+                     inter: int | None = None) -> LmoeFp8Experts:
+    """LmoeFp8Experts from a dict with w13_q, w13_s, w2_q, w2_s (e4m3 codes and fp32
+    scales); with `dims` (or E, latent and inter) each is checked against its size."""
+    names = ("w13_q", "w13_s", "w2_q", "w2_s")
+    if dims is not None:
+        E, latent, inter = dims.num_experts, dims.latent, dims.inter
+    if E is None:
+        return LmoeFp8Experts(*[_ptr(q.get(n)) for n in names])
+    E, L, d = int(E), int(latent), int(inter)
+    need = (E * 2 * d * L, E * _blocks(2 * d) * _blocks(L), E * L * d, E * _blocks(L) * _blocks(d))
+    return LmoeFp8Experts(*[_dev(q.get(n), n, torch.float32 if n.endswith("_s") else _E4M3, c)
+                            for n, c in zip(names, need)])
+
+
+def lmoe_experts_fp8_workspace_bytes(rows: int, E: int, latent: int, inter: int) -> int:
+    return int(load_library().lmoe_experts_fp8_workspace_bytes(int(rows), int(E), int(latent),
+                                                               int(inter)))
+
+
+def lmoe_experts_fp8(experts, x, xs, expert_offsets, y, workspace, inter: int, beta: float,
+                     linear_beta: float, stream=None, rows: int | None = None,
+                     latent: int | None = None, E: int | None = None):
+    """The routed experts on rows grouped by expert (expert e: rows
+    expert_offsets[e] .. expert_offsets[e+1]): y [rows, latent] bf16 of e4m3
+    x [rows, latent] with scales xs, through SituGLU."""
+    if rows is None:
+        rows, latent = x.shape
+    if E is None:
+        E = expert_offsets.numel() - 1
+    rows, L, E, d = int(rows), int(latent), int(E), int(inter)
+    qq = experts if isinstance(experts, LmoeFp8Experts) else make_fp8_experts(
+        experts, E=E, latent=L, inter=d)
+    wsp, wsn = _workspace(workspace, None)
+    st = load_library().lmoe_experts_fp8(
+        ctypes.byref(qq), _dev(x, "x", _E4M3, rows * L),
+        _dev(xs, "xs", torch.float32, rows * _blocks(L)),
+        _dev(expert_offsets, "expert_offsets", torch.int32, E + 1), _dev(y, "y", _BF16, rows * L),
+        rows, E, L, d, float(beta), float(linear_beta), wsp, wsn, _stream(stream))
+    _check(st, "lmoe_experts_fp8")
+
+
+def latent_moe_workspace_bytes_fp8(dims) -> int:
+    dd = dims if isinstance(dims, LmoeDims) else make_dims(dims)
+    return int(load_library().latent_moe_workspace_bytes_fp8(ctypes.byref(dd)))
+
+
+def latent_moe_forward_fp8(dims, weights, experts, hidden, router_logits, out, workspace,
+                           workspace_bytes: int | None = None, debug: dict | None = None,
+                           stream=None):
+    """The layer forward with e4m3 routed experts (weights' w13 / w2 unused)."""
+    dd = dims if isinstance(dims, LmoeDims) else make_dims(dims)
+    if isinstance(weights, LmoeWeights):
+        ww = weights
+    else:
+        ww = make_weights(dict(weights, w13=None, w2=None), dd)
+    qq = experts if isinstance(experts, LmoeFp8Experts) else make_fp8_experts(experts, dd)
+    T, H, E = int(dd.T), int(dd.hidden), int(dd.num_experts)
+    wsp, wsn = _workspace(workspace, workspace_bytes)
+    dbg, keep = _debug_struct(debug, dd)
+    st = load_library().latent_moe_forward_fp8(
+        ctypes.byref(dd), ctypes.byref(ww), ctypes.byref(qq), _dev(hidden, "hidden", _BF16, T * H),
+        _dev(router_logits, "router_logits", torch.float32, T * E),
+        _dev(out, "out", _BF16, T * H), wsp, wsn,
+        ctypes.byref(dbg) if dbg is not None else None, _stream(stream))
+    _check(st, "latent_moe_forward_fp8")
+
+
+def latent_moe_launch_count_fp8(dims, has_shared_expert: bool = True) -> int:
+    dd = dims if isinstance(dims, LmoeDims) else make_dims(dims)
+    return int(load_library().latent_moe_launch_count_fp8(ctypes.byref(dd),
+                                                           1 if has_shared_expert else 0))
+
+
+# --- training of the router --------------------------------------------------------
+
+
+def _router_batch(router_logits, topk_ids, token_mask, seq_offsets, shape):
+    """(T, E, topk, S) and the addresses of the batch, checked against them."""
+    if shape is not None:
+        T, E, k, S = (int(v) for v in shape)
+    else:
+        T, E = (int(v) for v in router_logits.shape)
+        k = int(topk_ids.shape[-1])
+        S = 1 if seq_offsets is None else int(seq_offsets.numel()) - 1
+    ptrs = (_dev(router_logits, "router_logits", torch.float32, T * E),
+            _dev(topk_ids, "topk_ids", torch.int32, T * k),
+            _dev(token_mask, "token_mask", (torch.uint8, torch.bool), T),
+            _dev(seq_offsets, "seq_offsets", torch.int32, S + 1))
+    return T, E, k, S, ptrs
+
+
+def moe_balance_loss_workspace_bytes(T: int, E: int, S: int = 1) -> int:
+    return int(load_library().moe_balance_loss_workspace_bytes(int(T), int(E), int(S)))
+
+
+def moe_balance_loss(router_logits, topk_ids, alpha: float, loss, expert_counts, seq_tokens,
+                     workspace, token_mask=None, seq_offsets=None, stream=None,
+                     shape: tuple | None = None):
+    """The router's balance loss: writes loss [1] fp32, expert_counts [S, E] and
+    seq_tokens [S] int32.  seq_offsets [S+1] int32 (None: one sequence), token_mask
+    [T] (None: every token counts); shape (T, E, topk, S) for raw addresses."""
+    T, E, k, S, (lg, ids, mask, seq) = _router_batch(router_logits, topk_ids, token_mask,
+                                                     seq_offsets, shape)
+    wsp, wsn = _workspace(workspace, None)
+    st = load_library().moe_balance_loss(
+        lg, ids, mask, seq, T, E, k, S, float(alpha), _dev(loss, "loss", torch.float32, 1),
+        _dev(expert_counts, "expert_counts", torch.int32, S * E),
+        _dev(seq_tokens, "seq_tokens", torch.int32, S), wsp, wsn, _stream(stream))
+    _check(st, "moe_balance_loss")
+
+
+def moe_router_backward(router_logits, topk_ids, grad_logits, grad_topk_weights=None,
+                        routed_scaling_factor: float = 1.0, renormalize: int = 1, grad_loss=None,
+                        expert_counts=None, seq_tokens=None, alpha: float = 0.0, token_mask=None,
+                        seq_offsets=None, stream=None, shape: tuple | None = None):
+    """grad_logits [T, E] fp32: the gradient through moe_route's weights
+    (grad_topk_weights [T, topk]) plus that of moe_balance_loss (grad_loss [1] with
+    the expert_counts and seq_tokens it wrote); either may be None."""
+    T, E, k, S, (lg, ids, mask, seq) = _router_batch(router_logits, topk_ids, token_mask,
+                                                     seq_offsets, shape)
+    st = load_library().moe_router_backward(
+        lg, ids, _dev(grad_topk_weights, "grad_topk_weights", torch.float32, T * k),
+        int(renormalize), float(routed_scaling_factor),
+        _dev(grad_loss, "grad_loss", torch.float32, 1),
+        _dev(expert_counts, "expert_counts", torch.int32, S * E),
+        _dev(seq_tokens, "seq_tokens", torch.int32, S), float(alpha), mask, seq, T, E, k, S,
+        _dev(grad_logits, "grad_logits", torch.float32, T * E), _stream(stream))
+    _check(st, "moe_router_backward")

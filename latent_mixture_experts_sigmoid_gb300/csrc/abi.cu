@@ -38,10 +38,12 @@
 #include <mutex>
 #include <vector>
 
+#include "fp8.cuh"
 #include "gemm_tc.cuh"
 #include "lmoe_internal.cuh"
 #include "moe_data.cuh"
 #include "mxfp4.cuh"
+#include "router_train.cuh"
 
 namespace lmoe {
 
@@ -137,7 +139,13 @@ struct Ws {
   // MXFP4 forward at decode sizes with heavy slots: the light experts' list
   // and count, the heavy slots' group tables
   int32_t *light, *n_light, *h_expert, *h_count, *h_offset, *h_prefix;
+  // e4m3 forward: expert-major rows and activations, codes and scales
+  uint8_t *A8, *act8;
+  float *A8s, *act8s;
 };
+
+// Which form the routed experts' weights have.
+enum class Experts { kBf16, kMxfp4, kFp8 };
 
 // Heavy-expert slots of the MXFP4 forward: an upper bound on the experts with
 // more than kFp4HeavyTokens of the T*k (token, slot) pairs (0 when no expert
@@ -161,7 +169,8 @@ bool fp4_direct(const lmoe_dims& d) {
 // Router logits rows are padded to whole 128-row weight tiles of the router GEMM.
 size_t padded_experts(int E) { return (size_t)round_up(E, 128); }
 
-size_t carve(const lmoe_dims& d, char* base, Ws* ws, bool mxfp4 = false) {
+size_t carve(const lmoe_dims& d, char* base, Ws* ws, Experts form = Experts::kBf16) {
+  const bool mxfp4 = form == Experts::kMxfp4;
   Carver c;
   c.base = base;
   const size_t T = d.T, k = d.topk, E = d.num_experts, L = d.latent, H = d.hidden;
@@ -213,6 +222,12 @@ size_t carve(const lmoe_dims& d, char* base, Ws* ws, bool mxfp4 = false) {
     w.h_prefix = c.take<int32_t>(Hs + 1);
   } else {
     w.Wd13 = w.Wd2 = nullptr;
+  }
+  if (form == Experts::kFp8) {
+    w.A8 = c.take<uint8_t>(T * k * L);
+    w.A8s = c.take<float>(T * k * (L / kFp8Block));
+    w.act8 = c.take<uint8_t>(T * k * dI);
+    w.act8s = c.take<float>(T * k * (dI / kFp8Block));
   }
   if (ws) *ws = w;
   return (c.off + 255) & ~size_t(255);
@@ -342,7 +357,8 @@ Plan make_plan(const lmoe_dims& d, int nsm, bool router = false) {
   return p;
 }
 
-int plan_launches(const Plan& p, bool shared, bool mxfp4 = false) {
+int plan_launches(const Plan& p, bool shared, Experts form = Experts::kBf16) {
+  const bool mxfp4 = form == Experts::kMxfp4;
   // one permutation kernel for T <= 256; at decode sizes it also does the scatter
   const int perm = p.T <= 256 ? 1 : 3;
   // GEMM1 (+ SituGLU unless fused), GEMM2; MXFP4 experts: one kernel per
@@ -351,6 +367,9 @@ int plan_launches(const Plan& p, bool shared, bool mxfp4 = false) {
   // without the 4-bit kernels, one dequantization kernel first
   int experts = p.fuse_g1 ? 2 : 3;
   if (mxfp4) experts = p.fp4_direct ? 2 + (p.fp4_heavy > 0 ? 3 : 0) : experts + 1;
+  // e4m3: one kernel per stage, and at decode sizes the quantisation of the
+  // scattered rows (above, the scatter quantises)
+  if (form == Experts::kFp8) experts = 2 + (p.decode ? 1 : 0);
   // route, down, permute, scatter (fused into the permutation at decode sizes),
   // experts, combine
   int n = 1 + 1 + perm + (p.decode ? 0 : 1) + experts + 1;
@@ -442,6 +461,68 @@ bool on_current_device(std::initializer_list<const void*> ptrs) {
     if (a.type != cudaMemoryTypeDevice || a.device != dev) return false;
   }
   return true;
+}
+
+constexpr long long kMaxFp8Rows = 1ll << 27;   // the grouped kernel's tile arithmetic is 32-bit
+constexpr int kMaxFp8Dim = 8192;
+
+int validate_dims_fp8(const lmoe_dims* d) {
+  const int v = validate_dims(d);
+  if (v != LMOE_OK) return v;
+  if (d->inter % kFp8Block || d->inter > kMaxFp8Dim || (long long)d->T * d->topk > kMaxFp8Rows)
+    return LMOE_ERR_DIM;
+  return LMOE_OK;
+}
+
+int check_fp8_experts(const lmoe_fp8_experts& w) {
+  if (!w.w13_codes || !w.w13_scales || !w.w2_codes || !w.w2_scales) return LMOE_ERR_NULL;
+  if (!aligned16(w.w13_codes) || !aligned16(w.w13_scales) || !aligned16(w.w2_codes) ||
+      !aligned16(w.w2_scales))
+    return LMOE_ERR_ALIGN;
+  return LMOE_OK;
+}
+
+// One stage of the e4m3 experts: 1 = act from x (product and SituGLU), 2 = y from act.
+cudaError_t experts_fp8(const lmoe_fp8_experts& w, const uint8_t* x, const float* xs,
+                        const int32_t* offsets, uint8_t* act, float* act_s, uint16_t* y,
+                        long long rows, int E, int L, int d, float beta, float linear_beta,
+                        int stage, cudaStream_t s) {
+  Fp8Gemm g{};
+  g.rows = rows;
+  g.groups = E;
+  g.offsets = offsets;
+  if (stage == 1) {
+    g.X = x;
+    g.xs = xs;
+    g.W = w.w13_codes;
+    g.ws = w.w13_scales;
+    g.feat = 2 * d;
+    g.K = L;
+    g.act = act;
+    g.act_s = act_s;
+    g.beta = beta;
+    g.linear_beta = linear_beta;
+  } else {
+    g.X = act;
+    g.xs = act_s;
+    g.W = w.w2_codes;
+    g.ws = w.w2_scales;
+    g.feat = L;
+    g.K = d;
+    g.out = y;
+  }
+  return launch_fp8_gemm(g, s);
+}
+
+// Workspace of lmoe_experts_fp8: the activations' codes, then their scales.
+size_t fp8_act_bytes(long long rows, int d) { return ((size_t)rows * d + 255) & ~size_t(255); }
+
+// The checks of the router's training entry points that need no pointer.
+int validate_router(int T, int E, int topk, int S, float alpha) {
+  if (T < 0 || E < 1 || E > 1024 || topk < 1 || topk > E || topk > 32) return LMOE_ERR_DIM;
+  if ((long long)T * topk > 2147483647ll || S < 1 || S > 65536 || !isfinite(alpha))
+    return LMOE_ERR_DIM;
+  return LMOE_OK;
 }
 
 #define LMOE_TRY(x)                                  \
@@ -569,8 +650,9 @@ static int forward_impl(const lmoe_dims* dims, const lmoe_weights* wt, const lmo
                         const float* router_logits, const int32_t* pre_ids, const float* pre_w,
                         const lmoe_bf16* w_router, lmoe_bf16* out, void* workspace,
                         size_t workspace_bytes, const lmoe_debug* dbg, void* stream,
-                        bool own_workspace, const lmoe_mxfp4_experts* fq = nullptr) {
-  const int v = validate_dims(dims);
+                        bool own_workspace, const lmoe_mxfp4_experts* fq = nullptr,
+                        const lmoe_fp8_experts* e8 = nullptr) {
+  const int v = e8 ? validate_dims_fp8(dims) : validate_dims(dims);
   if (v != LMOE_OK) return v;
   if (!wt) return LMOE_ERR_NULL;
   const lmoe_dims d = *dims;
@@ -581,8 +663,12 @@ static int forward_impl(const lmoe_dims* dims, const lmoe_weights* wt, const lmo
   const bool pre_routed = !router && router_logits == nullptr;
   if (!hidden || (pre_routed && (!pre_ids || !pre_w)) || !out || !wt->w_down || !wt->w_up)
     return LMOE_ERR_NULL;
-  // routed experts: bf16 (w13, w2) or MXFP4 (fq)
-  if (fq) {
+  // routed experts: bf16 (w13, w2), MXFP4 (fq) or e4m3 (e8)
+  const bool bf16_experts = !fq && !e8;
+  if (e8) {
+    const int r = check_fp8_experts(*e8);
+    if (r != LMOE_OK) return r;
+  } else if (fq) {
     if (!fq->w13_codes || !fq->w13_scales || !fq->w2_codes || !fq->w2_scales) return LMOE_ERR_NULL;
     if (d.inter > 4096 || d.latent > 4096) return LMOE_ERR_DIM;
     if (!aligned16(fq->w13_codes) || !aligned16(fq->w2_codes) || !aligned16(fq->w13_scales) ||
@@ -595,13 +681,14 @@ static int forward_impl(const lmoe_dims* dims, const lmoe_weights* wt, const lmo
   if (shared != (wt->ws2 != nullptr)) return LMOE_ERR_NULL;
   if (shared && d.shared_inter <= 0) return LMOE_ERR_DIM;
   const void* ptrs[] = {hidden, router_logits, pre_ids, pre_w, out, wt->w_down,
-                        fq ? nullptr : wt->w13, fq ? nullptr : wt->w2, wt->w_up, wt->ws13,
+                        bf16_experts ? wt->w13 : nullptr, bf16_experts ? wt->w2 : nullptr, wt->w_up, wt->ws13,
                         wt->ws2, wt->norm_w, wt->e_score_correction_bias, w_router};
   for (const void* p : ptrs)
     if (p && !aligned16(p)) return LMOE_ERR_ALIGN;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u)) return LMOE_ERR_WORKSPACE;
   Ws ws;
-  const size_t need = carve(d, static_cast<char*>(workspace), &ws, fq != nullptr);
+  const size_t need = carve(d, static_cast<char*>(workspace), &ws,
+                            e8 ? Experts::kFp8 : fq ? Experts::kMxfp4 : Experts::kBf16);
   if (workspace_bytes < need) return LMOE_ERR_WORKSPACE;
   if (dbg) {
     const void* dp[] = {dbg->topk_ids, dbg->topk_weights, dbg->expert_num_tokens,
@@ -610,11 +697,13 @@ static int forward_impl(const lmoe_dims* dims, const lmoe_weights* wt, const lmo
       if (p && !aligned16(p)) return LMOE_ERR_ALIGN;
   }
   if (!on_current_device({hidden, router_logits, pre_ids, pre_w, out, wt->w_down,
-                          fq ? nullptr : wt->w13, fq ? nullptr : wt->w2, wt->w_up, wt->ws13,
+                          bf16_experts ? wt->w13 : nullptr, bf16_experts ? wt->w2 : nullptr, wt->w_up, wt->ws13,
                           wt->ws2, wt->norm_w, wt->e_score_correction_bias, w_router,
                           own_workspace ? nullptr : workspace}))
     return LMOE_ERR_DEVICE;
   if (fq && !on_current_device({fq->w13_codes, fq->w13_scales, fq->w2_codes, fq->w2_scales}))
+    return LMOE_ERR_DEVICE;
+  if (e8 && !on_current_device({e8->w13_codes, e8->w13_scales, e8->w2_codes, e8->w2_scales}))
     return LMOE_ERR_DEVICE;
   if (dbg && !on_current_device({dbg->topk_ids, dbg->topk_weights, dbg->expert_num_tokens,
                                  dbg->expert_offsets, dbg->row_of}))
@@ -799,8 +888,13 @@ static int forward_impl(const lmoe_dims* dims, const lmoe_weights* wt, const lmo
     if (st != LMOE_OK) return st;
   }
   if (!mark(LMOE_STAGE_PERMUTE + 1)) return LMOE_ERR_CUDA;
-  // 4. routed input into the expert-major rows
-  if (!fused_scatter)
+  // 4. routed input into the expert-major rows (e4m3 experts: as codes and
+  // scales; above decode sizes a token's row is quantised once and scattered)
+  if (e8 && fused_scatter)
+    LMOE_TRY(launch_quantize_fp8(ws.A, ws.A8, ws.A8s, rows, L, 1, s));
+  else if (e8)
+    LMOE_TRY(launch_quantize_scatter_fp8(ws.Z, T, L, k, ws.row_of, ws.A8, ws.A8s, s));
+  else if (!fused_scatter)
     LMOE_TRY(launch_scatter_rows(down_split ? nullptr : ws.Z, down_split ? ws.Pa : nullptr,
                                  cdown.splits, down_stride, ldz, T, L, k, ws.row_of, ws.A, s));
   if (!mark(LMOE_STAGE_SCATTER + 1)) return LMOE_ERR_CUDA;
@@ -811,7 +905,16 @@ static int forward_impl(const lmoe_dims* dims, const lmoe_weights* wt, const lmo
   // 5-7. experts
   const uint16_t* W13 = wt->w13;
   const uint16_t* W2 = wt->w2;
-  if (fq && pl.fp4_direct) {
+  if (e8) {
+    LMOE_TRY(experts_fp8(*e8, ws.A8, ws.A8s, ws.offsets, ws.act8, ws.act8s, ws.Y, rows, E, L, dI,
+                         d.beta, d.linear_beta, 1, s));
+    if (!mark(LMOE_STAGE_GEMM1 + 1) || !mark(LMOE_STAGE_SITU + 1)) return LMOE_ERR_CUDA;
+    st = fork_shared_late();
+    if (st != LMOE_OK) return st;
+    LMOE_TRY(experts_fp8(*e8, ws.A8, ws.A8s, ws.offsets, ws.act8, ws.act8s, ws.Y, rows, E, L, dI,
+                         d.beta, d.linear_beta, 2, s));
+    if (!mark(LMOE_STAGE_GEMM2 + 1)) return LMOE_ERR_CUDA;
+  } else if (fq && pl.fp4_direct) {
     // MXFP4: GEMM1 + SituGLU and GEMM2 straight from the 4-bit weights, one
     // block per (active expert, column strip).  With heavy
     // slots (T > kFp4HeavyTokens) the permutation has split the active experts
@@ -1004,7 +1107,7 @@ int lmoe_dequant_mxfp4(const uint8_t* codes, const uint8_t* scales, lmoe_bf16* o
 
 size_t latent_moe_workspace_bytes_mxfp4(const lmoe_dims* dims) {
   if (validate_dims(dims) != LMOE_OK || dims->inter > 4096 || dims->latent > 4096) return 0;
-  return carve(*dims, nullptr, nullptr, true);
+  return carve(*dims, nullptr, nullptr, Experts::kMxfp4);
 }
 
 int latent_moe_forward_mxfp4(const lmoe_dims* dims, const lmoe_weights* wt,
@@ -1020,7 +1123,159 @@ int latent_moe_forward_mxfp4(const lmoe_dims* dims, const lmoe_weights* wt,
 int latent_moe_launch_count_mxfp4(const lmoe_dims* dims, int has_shared_expert) {
   if (validate_dims(dims) != LMOE_OK || dims->inter > 4096 || dims->latent > 4096) return 0;
   if (dims->T == 0) return 0;
-  return plan_launches(make_plan(*dims, num_sms()), has_shared_expert != 0, true);
+  return plan_launches(make_plan(*dims, num_sms()), has_shared_expert != 0, Experts::kMxfp4);
+}
+
+int lmoe_quantize_fp8(const lmoe_bf16* x, uint8_t* codes, float* scales, int64_t rows, int K,
+                      int block_rows, void* stream) {
+  if (rows < 0 || K <= 0 || K % 16 || (block_rows != 1 && block_rows != kFp8Block))
+    return LMOE_ERR_DIM;
+  if (rows > 2147483647ll / fp8_blocks(K)) return LMOE_ERR_DIM;
+  if (rows == 0) return LMOE_OK;
+  if (!x || !codes || !scales) return LMOE_ERR_NULL;
+  if (!aligned16(x) || !aligned16(codes) || !aligned16(scales)) return LMOE_ERR_ALIGN;
+  if (!on_current_device({x, codes, scales})) return LMOE_ERR_DEVICE;
+  LMOE_TRY(launch_quantize_fp8(x, codes, scales, rows, K, block_rows, (cudaStream_t)stream));
+  return LMOE_OK;
+}
+
+int lmoe_linear_fp8(const uint8_t* x, const float* xs, const uint8_t* w, const float* ws,
+                    const lmoe_bf16* add, lmoe_bf16* out, int T, int N, int K, void* stream) {
+  if (T < 0 || N <= 0 || N % 8 || K <= 0 || K % 16) return LMOE_ERR_DIM;
+  // tiles are counted in 32 bits
+  if (((long long)T + 127) / 128 * (((long long)N + 127) / 128) > 2147483647ll) return LMOE_ERR_DIM;
+  if (T == 0) return LMOE_OK;
+  if (!x || !xs || !w || !ws || !out) return LMOE_ERR_NULL;
+  if (!aligned16(x) || !aligned16(xs) || !aligned16(w) || !aligned16(ws) || !aligned16(out) ||
+      (add && !aligned16(add)))
+    return LMOE_ERR_ALIGN;
+  if (!on_current_device({x, xs, w, ws, add, out})) return LMOE_ERR_DEVICE;
+  Fp8Gemm g{};
+  g.X = x;
+  g.xs = xs;
+  g.W = w;
+  g.ws = ws;
+  g.rows = T;
+  g.groups = 1;
+  g.feat = N;
+  g.K = K;
+  g.add = add;
+  g.out = out;
+  LMOE_TRY(launch_fp8_gemm(g, (cudaStream_t)stream));
+  return LMOE_OK;
+}
+
+size_t lmoe_experts_fp8_workspace_bytes(int64_t rows, int E, int latent, int inter) {
+  if (rows < 0 || rows > kMaxFp8Rows || E < 1 || E > 1024 || latent <= 0 || latent % kFp8Block ||
+      latent > kMaxFp8Dim || inter <= 0 || inter % kFp8Block || inter > kMaxFp8Dim)
+    return 0;
+  return fp8_act_bytes(rows, inter) + fp8_act_bytes(rows, inter / kFp8Block * 4) + 256;
+}
+
+int lmoe_experts_fp8(const lmoe_fp8_experts* experts, const uint8_t* x, const float* xs,
+                     const int32_t* expert_offsets, lmoe_bf16* y, int64_t rows, int E, int latent,
+                     int inter, float beta, float linear_beta, void* workspace,
+                     size_t workspace_bytes, void* stream) {
+  const size_t need = lmoe_experts_fp8_workspace_bytes(rows, E, latent, inter);
+  if (need == 0) return LMOE_ERR_DIM;
+  if (!finite_pos(beta)) return LMOE_ERR_BETA;
+  if (!isfinite(linear_beta)) return LMOE_ERR_DIM;
+  if (rows == 0) return LMOE_OK;
+  if (!experts || !x || !xs || !expert_offsets || !y) return LMOE_ERR_NULL;
+  const int v = check_fp8_experts(*experts);
+  if (v != LMOE_OK) return v;
+  if (!aligned16(x) || !aligned16(xs) || !aligned16(expert_offsets) || !aligned16(y))
+    return LMOE_ERR_ALIGN;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) || workspace_bytes < need)
+    return LMOE_ERR_WORKSPACE;
+  if (!on_current_device({experts->w13_codes, experts->w13_scales, experts->w2_codes,
+                          experts->w2_scales, x, xs, expert_offsets, y, workspace}))
+    return LMOE_ERR_DEVICE;
+  uint8_t* act = static_cast<uint8_t*>(workspace);
+  float* act_s = reinterpret_cast<float*>(act + fp8_act_bytes(rows, inter));
+  for (int stage = 1; stage <= 2; ++stage)
+    LMOE_TRY(experts_fp8(*experts, x, xs, expert_offsets, act, act_s, y, rows, E, latent, inter,
+                         beta, linear_beta, stage, (cudaStream_t)stream));
+  return LMOE_OK;
+}
+
+size_t latent_moe_workspace_bytes_fp8(const lmoe_dims* dims) {
+  if (validate_dims_fp8(dims) != LMOE_OK) return 0;
+  return carve(*dims, nullptr, nullptr, Experts::kFp8);
+}
+
+int latent_moe_forward_fp8(const lmoe_dims* dims, const lmoe_weights* wt,
+                           const lmoe_fp8_experts* experts, const lmoe_bf16* hidden,
+                           const float* router_logits, lmoe_bf16* out, void* workspace,
+                           size_t workspace_bytes, const lmoe_debug* dbg, void* stream) {
+  if (dims && dims->T != 0 && (!experts || !router_logits)) return LMOE_ERR_NULL;
+  lmoe_fp8_experts none{};
+  return forward_impl(dims, wt, hidden, router_logits, nullptr, nullptr, nullptr, out, workspace,
+                      workspace_bytes, dbg, stream, false, nullptr, experts ? experts : &none);
+}
+
+int latent_moe_launch_count_fp8(const lmoe_dims* dims, int has_shared_expert) {
+  if (validate_dims_fp8(dims) != LMOE_OK || dims->T == 0) return 0;
+  return plan_launches(make_plan(*dims, num_sms()), has_shared_expert != 0, Experts::kFp8);
+}
+
+size_t moe_balance_loss_workspace_bytes(int T, int E, int S) {
+  if (validate_router(T, E, 1, S, 0.0f) != LMOE_OK) return 0;
+  return balance_workspace_bytes(T);
+}
+
+int moe_balance_loss(const float* router_logits, const int32_t* topk_ids,
+                     const uint8_t* token_mask, const int32_t* seq_offsets, int T, int E, int topk,
+                     int S, float alpha, float* loss, int32_t* expert_counts, int32_t* seq_tokens,
+                     void* workspace, size_t workspace_bytes, void* stream) {
+  const int v = validate_router(T, E, topk, S, alpha);
+  if (v != LMOE_OK) return v;
+  if (T == 0) return LMOE_OK;
+  if (!router_logits || !topk_ids || !loss || !expert_counts || !seq_tokens ||
+      (!seq_offsets && S != 1))
+    return LMOE_ERR_NULL;
+  const void* ptrs[] = {router_logits, topk_ids, token_mask, seq_offsets, loss, expert_counts,
+                        seq_tokens};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return LMOE_ERR_ALIGN;
+  if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+      workspace_bytes < balance_workspace_bytes(T))
+    return LMOE_ERR_WORKSPACE;
+  if (!on_current_device({router_logits, topk_ids, token_mask, seq_offsets, loss, expert_counts,
+                          seq_tokens, workspace}))
+    return LMOE_ERR_DEVICE;
+  const RouterBatch b{router_logits, topk_ids, token_mask, seq_offsets, T, E, topk, S};
+  LMOE_TRY(launch_balance_loss(b, alpha, loss, expert_counts, seq_tokens, workspace,
+                               (cudaStream_t)stream));
+  return LMOE_OK;
+}
+
+int moe_router_backward(const float* router_logits, const int32_t* topk_ids,
+                        const float* grad_topk_weights, int renormalize,
+                        float routed_scaling_factor, const float* grad_loss,
+                        const int32_t* expert_counts, const int32_t* seq_tokens, float alpha,
+                        const uint8_t* token_mask, const int32_t* seq_offsets, int T, int E,
+                        int topk, int S, float* grad_logits, void* stream) {
+  const int v = validate_router(T, E, topk, S, alpha);
+  if (v != LMOE_OK) return v;
+  if (!isfinite(routed_scaling_factor)) return LMOE_ERR_DIM;
+  if (T == 0) return LMOE_OK;
+  if (!router_logits || !grad_logits || (!grad_topk_weights && !grad_loss) ||
+      (grad_topk_weights && !topk_ids) || (!seq_offsets && S != 1) ||
+      (grad_loss && (!expert_counts || !seq_tokens)))
+    return LMOE_ERR_NULL;
+  const void* ptrs[] = {router_logits, topk_ids, grad_topk_weights, grad_loss, expert_counts,
+                        seq_tokens, token_mask, seq_offsets, grad_logits};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return LMOE_ERR_ALIGN;
+  if (!on_current_device({router_logits, topk_ids, grad_topk_weights, grad_loss, expert_counts,
+                          seq_tokens, token_mask, seq_offsets, grad_logits}))
+    return LMOE_ERR_DEVICE;
+  const RouterBatch b{router_logits, topk_ids, token_mask, seq_offsets, T, E, topk, S};
+  LMOE_TRY(launch_router_backward(b, grad_topk_weights, renormalize, routed_scaling_factor,
+                                  grad_loss, expert_counts, seq_tokens, alpha, grad_logits,
+                                  (cudaStream_t)stream));
+  return LMOE_OK;
 }
 
 }  // extern "C"

@@ -114,10 +114,8 @@ __device__ __forceinline__ f32x2 f2_add(f32x2 a, f32x2 b) {
 // elementwise f(x) of a pair through a scalar transcendental op
 #define LMOE_F2_APPLY(f, v) f2_make(__float_as_uint(f(f2_lo(v))), __float_as_uint(f(f2_hi(v))))
 
-// bf16x2 gate / up in, fp32 pair out (lo, hi)
-__device__ __forceinline__ f32x2 situ2_f32(uint32_t g2, uint32_t u2, const SituParams& p) {
-  const f32x2 g = f2_make(g2 << 16, g2 & 0xFFFF0000u);
-  const f32x2 u = f2_make(u2 << 16, u2 & 0xFFFF0000u);
+// fp32 gate / up pairs in, fp32 pair out
+__device__ __forceinline__ f32x2 situ2_pair(f32x2 g, f32x2 u, const SituParams& p) {
   const f32x2 tg = LMOE_F2_APPLY(tanh_fast, f2_mul(g, f2_splat(p.inv_beta)));
   const f32x2 e = LMOE_F2_APPLY(ex2_fast, f2_mul(g, f2_splat(-1.4426950408889634f)));
   const f32x2 up = p.has_lbeta ? f2_mul(LMOE_F2_APPLY(tanh_fast, f2_mul(u, f2_splat(p.inv_lbeta))),
@@ -126,6 +124,11 @@ __device__ __forceinline__ f32x2 situ2_f32(uint32_t g2, uint32_t u2, const SituP
   const f32x2 num = f2_mul(f2_mul(tg, f2_splat(p.beta)), up);
   const f32x2 r = LMOE_F2_APPLY(rcp_fast, f2_add(e, f2_splat(1.0f)));
   return f2_mul(num, r);
+}
+
+// bf16x2 gate / up in, fp32 pair out (lo, hi)
+__device__ __forceinline__ f32x2 situ2_f32(uint32_t g2, uint32_t u2, const SituParams& p) {
+  return situ2_pair(f2_make(g2 << 16, g2 & 0xFFFF0000u), f2_make(u2 << 16, u2 & 0xFFFF0000u), p);
 }
 
 __device__ __forceinline__ uint32_t situ2(uint32_t g2, uint32_t u2, const SituParams& p) {
