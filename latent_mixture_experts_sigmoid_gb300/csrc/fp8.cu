@@ -55,6 +55,13 @@ __device__ __forceinline__ uint4 ld_stream(const void* p) {
   return v;
 }
 
+// A load that stays where it is written: ahead of the waits that follow it.
+__device__ __forceinline__ float ld_ahead(const float* p) {
+  float v;
+  asm volatile("ld.global.nc.f32 %0, [%1];" : "=f"(v) : "l"(p));
+  return v;
+}
+
 // largest magnitude of eight bf16 values, as the bits of a bf16 (magnitudes
 // order like their bit patterns)
 __device__ __forceinline__ uint32_t absmax8(const uint4& v) {
@@ -191,20 +198,21 @@ quantize_scatter_kernel(const uint16_t* __restrict__ Z, const int32_t* __restric
 }
 
 // ---------------------------------------------------------------------------
-// The product: a persistent kernel of ten warps a CTA.
+// The product: a persistent kernel of twelve warps a CTA.
 //   warp 0      TMA producer: 128 K columns of 128 token rows and of kNH x 128
 //               weight rows a stage (128-byte rows, 128-byte swizzle);
 //   warp 1      allocates TMEM; one thread issues the MMAs (kind::f8f6f4,
 //               M = 128 tokens, N = 128 kNH weight rows, K = 32), a K block
 //               into each of the TMEM accumulators in turn;
-//   warps 2..9  read the finished K block from TMEM (warp w: the 32 token rows
-//               of lane quarter w % 4, half h = (w - 2) / 4 of the columns),
+//   warps 4..11 read the finished K block from TMEM (warp w: the 32 token rows
+//               of lane quarter w % 4, half h = (w - 4) / 4 of the columns),
 //               scale and add it in registers, and write the tile.
 // Every wait is bounded: on expiry the code goes to the device error word, the
 // CTA drains its copies and MMAs, frees its TMEM and returns.
 // ---------------------------------------------------------------------------
-constexpr int kThreads = 320;
+constexpr int kEpiWarp0 = 4;                   // the first epilogue warp
 constexpr int kEpiWarps = 8;
+constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
 constexpr int BM = 128;                       // token rows of a tile
 constexpr int kBK = 128;                      // K columns (bytes) of a stage
 constexpr uint32_t kBoxBytes = 128 * kBK;     // a 128-row operand box
@@ -230,7 +238,7 @@ struct Fp8Params {
   SituParams sp;
 };
 
-__device__ __noinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+__device__ __forceinline__ bool wait_slow(uint32_t bar, uint32_t parity, volatile int* abort_flag,
                                        int* err, int code) {
   const long long t0 = clock64();
   while (true) {
@@ -359,8 +367,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + 2 * S + 2 * kAcc + 1);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   uint32_t* amax_ex = tmem_holder + 2;   // [2][2][128] (SituGLU)
-  int* warp_sum = reinterpret_cast<int*>(amax_ex + 512);        // [10]
-  int* prefix = warp_sum + 10;                                  // [G + 1]
+  int* warp_sum = reinterpret_cast<int*>(amax_ex + 512);        // [kThreads / 32]
+  int* prefix = warp_sum + kThreads / 32;                       // [G + 1]
   int* first = prefix + p.groups + 1;                           // [G]
   int* end = first + p.groups;                                  // [G]
 
@@ -404,8 +412,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
   const int ntok = p.offsets ? prefix[p.groups] : (int)((p.rows + BM - 1) / BM);
   const int U = ntok * p.nfeat;
 
-  if (warp == 0) {
-    if (lane == 0) {
+  // the launch's 168 registers a thread, split anew: 168 * 384 = 56 * 128 + 224 * 256
+  if (warp < kEpiWarp0) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    if (warp == 0 && lane == 0) {
       // ---------------- TMA producer ----------------
       uint32_t it = 0, s = 0, ph = 0;
       bool ok = true;
@@ -435,9 +445,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
         if (!wait_phase(full_bar(j % (uint32_t)S), (j / (uint32_t)S) & 1u, &never, p.err, kErrDrain))
           break;
       }
-    }
-  } else if (warp == 1) {
-    if (lane == 0) {
+    } else if (warp == 1 && lane == 0) {
       // ---------------- MMA issuer ----------------
       constexpr uint32_t idesc = idesc_e4m3(BM, kBN);
       const uint64_t d0 = sdesc(smem_u32(smem));
@@ -469,9 +477,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       wait_phase(done_bar, 0u, &never, p.err, kErrDone);
     }
   } else {
-    // ---------------- epilogue (warps 2..9) ----------------
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    // ---------------- epilogue ----------------
     const int q = warp & 3;                 // TMEM lane quarter this warp may access
-    const int h = (warp - 2) >> 2;          // column half
+    const int h = (warp - kEpiWarp0) >> 2;          // column half
     const int r = q * 32 + lane;            // token row of the tile
     uint32_t acc = 0, aph = 0, par = 0;
     bool ok = true;
@@ -488,34 +497,39 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       f32x2 y[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) y[i] = 0ull;
-      float fx = 0.0f, fw = 0.0f, fw2 = 0.0f;
+      // the scales of a K block are loaded one block ahead of its sums
+      float nx = 0.0f, nw = 0.0f, nw2 = 0.0f;
       if (active) {
-        fx = __ldg(xsp);
-        fw = __ldg(wsp);
-        if (kSitu) fw2 = __ldg(wsp2);
+        nx = ld_ahead(xsp);
+        nw = ld_ahead(wsp);
+        if (kSitu) nw2 = ld_ahead(wsp2);
       }
       for (int kb = 0; kb < p.nkb; ++kb) {
-        const f32x2 f = f2_splat(fx * fw);
-        const f32x2 f2 = f2_splat(fx * fw2);
+        const float fx = nx, fw = nw, fw2 = nw2;
         if (active && kb + 1 < p.nkb) {
-          fx = __ldg(xsp + kb + 1);
-          fw = __ldg(wsp + kb + 1);
-          if (kSitu) fw2 = __ldg(wsp2 + kb + 1);
+          nx = ld_ahead(xsp + kb + 1);
+          nw = ld_ahead(wsp + kb + 1);
+          if (kSitu) nw2 = ld_ahead(wsp2 + kb + 1);
         }
         if (!wait_phase(tfull_bar(acc), aph, abort_flag, p.err, kErrEpilogue)) { ok = false; break; }
         tc_fence_after();
         if (active) {
           const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + acc * kBN;
+          const f32x2 f = f2_splat(fx * fw), f2 = f2_splat(fx * fw2);
+          // one chunk's load under way while the one before is added
+          auto col = [&](int i) {
+            return kSitu ? (uint32_t)((i / 2) * 128 + h * 64 + (i % 2) * 32)
+                         : (uint32_t)(h * kCols + i * 32);
+          };
+          uint32_t v[2][32];
+          tmem_ld32(tb + col(0), v[0]);
 #pragma unroll
           for (int i = 0; i < kCols / 32; ++i) {
-            const uint32_t col = kSitu ? (uint32_t)((i / 2) * 128 + h * 64 + (i % 2) * 32)
-                                       : (uint32_t)(h * kCols + i * 32);
-            uint32_t v[32];
-            tmem_ld32(tb + col, v);
-            tmem_wait_ld32(v);
+            tmem_wait_ld32(v[i & 1]);
+            if (i + 1 < kCols / 32) tmem_ld32(tb + col(i + 1), v[(i + 1) & 1]);
 #pragma unroll
             for (int j = 0; j < 16; ++j)
-              y[i * 16 + j] = f2_fma(f2_make(v[2 * j], v[2 * j + 1]),
+              y[i * 16 + j] = f2_fma(f2_make(v[i & 1][2 * j], v[i & 1][2 * j + 1]),
                                      kSitu && i >= kCols / 64 ? f2 : f, y[i * 16 + j]);
           }
         }
@@ -586,6 +600,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
+    __syncwarp();
     tc_fence_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u)
                  : "memory");
@@ -640,7 +655,7 @@ cudaError_t launch_form(const Fp8Gemm& g, cudaStream_t s) {
       !make_map(&mw, g.W, (long long)g.groups * g.feat, g.K, 128))
     return cudaErrorInvalidValue;
   const size_t smem = 1024 + (size_t)p.stages * kStage + (2 * p.stages + 2 * (512 / kBN) + 1) * 8 +
-                      8 + 512 * 4 + 40 + (g.offsets ? (3 * g.groups + 1) * 4 : 4);
+                      8 + 512 * 4 + kThreads / 32 * 4 + (g.offsets ? (3 * g.groups + 1) * 4 : 4);
   auto* kern = fp8_gemm_kernel<kNH, kSitu>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
