@@ -203,9 +203,10 @@ def _dev(t, name: str, dtypes, numel: int) -> int | None:
         return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor, an address or None")
-    if not t.is_cuda:
+    index = t.get_device() if t.is_cuda else -1
+    if index < 0:
         raise ValueError(f"{name}: must be a CUDA tensor (got device {t.device})")
-    if t.get_device() != torch.cuda.current_device():
+    if index != torch._C._cuda_getDevice():
         raise ValueError(f"{name}: on {t.device}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     if not t.is_contiguous():

@@ -51,21 +51,23 @@ __device__ __forceinline__ float warp_max(float v) {
 }
 
 // ---------------------------------------------------------------------------
-// Counts: one cluster of CTAs a sequence, a slice of its tokens each, into a
-// histogram in shared memory; then each CTA sums its share of the experts over
-// the cluster's histograms.  No global atomics and nothing to zero first.
+// Counts: one kernel zeroes them, the next spreads the tokens evenly over its
+// CTAs, each with a histogram in shared memory for the sequence at hand that it
+// adds to the global counts (integers: the order does not matter).
+//
+// Both trigger their dependents after their own wait, so a CTA of a later kernel
+// of the call exists only once all work before the call is complete: it may read
+// the call's inputs before its own wait, which is for what the call itself writes.
 // ---------------------------------------------------------------------------
-__device__ __forceinline__ uint32_t cluster_size() {
-  uint32_t n;
-  asm volatile("mov.u32 %0, %%cluster_nctarank;" : "=r"(n));
-  return n;
-}
-__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
-  uint32_t a;
-  int v;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
-  return v;
+__global__ void __launch_bounds__(256)
+zero_kernel(int32_t* __restrict__ counts, long long n, int32_t* __restrict__ tokens, int S,
+            unsigned* __restrict__ ticket) {
+  pdl_wait();
+  pdl_trigger();
+  const long long i0 = (long long)blockIdx.x * 256 + threadIdx.x, step = (long long)gridDim.x * 256;
+  for (long long i = i0; i < n; i += step) counts[i] = 0;
+  for (long long i = i0; i < S; i += step) tokens[i] = 0;
+  if (i0 == 0) *ticket = 0;
 }
 
 __device__ __forceinline__ int2 sequence_range(const RouterBatch& b, int s) {
@@ -74,53 +76,70 @@ __device__ __forceinline__ int2 sequence_range(const RouterBatch& b, int s) {
   return make_int2(a, min(max(__ldg(b.seq + s + 1), a), b.T));
 }
 
+// The last sequence that begins at or before token t (0 where none does).
+__device__ __forceinline__ int sequence_of(const RouterBatch& b, int t) {
+  if (!b.seq) return 0;
+  int lo = 0, hi = b.S - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (__ldg(b.seq + mid) <= t) lo = mid; else hi = mid - 1;
+  }
+  return lo;
+}
+
 __global__ void __launch_bounds__(kCountThreads)
-count_kernel(const RouterBatch b, int32_t* __restrict__ counts, int32_t* __restrict__ tokens,
-             unsigned* __restrict__ ticket) {
+count_kernel(const RouterBatch b, int per_cta, int32_t* __restrict__ counts,
+             int32_t* __restrict__ tokens) {
   __shared__ int hist[kMaxE + 1];      // [E]: the slice's valid tokens
-  const uint32_t rank = cluster_rank(), nr = cluster_size();
-  const int s = blockIdx.x / nr;
-  pdl_trigger();
+  pdl_trigger();                       // (the kernel before has waited: see above)
   for (int e = threadIdx.x; e <= b.E; e += kCountThreads) hist[e] = 0;
-  pdl_wait();
   __syncthreads();
-  const int2 r = sequence_range(b, s);
-  const int per = (int)(((long long)(r.y - r.x) + nr - 1) / nr);
-  const int t0 = min(r.x + (int)rank * per, r.y), t1 = min(t0 + per, r.y);
-  const long long i0 = (long long)t0 * b.k, i1 = (long long)t1 * b.k;
-  constexpr int kUnroll = 8;
-  for (long long i = i0 + threadIdx.x; i < i1; i += kCountThreads * kUnroll) {
-    int id[kUnroll];
+  bool waited = false;
+  const int first = (int)min((long long)blockIdx.x * per_cta, (long long)b.T);
+  const int last = min(first + per_cta, b.T);
+  for (int t0 = first; t0 < last;) {
+    const int s = sequence_of(b, t0);
+    const int2 r = sequence_range(b, s);
+    if (t0 < r.x) { t0 = min(r.x, last); continue; }   // before the first sequence
+    if (t0 >= r.y) break;                              // behind the last
+    const int t1 = min(r.y, last);
+    const long long i1 = (long long)t1 * b.k;
+    constexpr int kUnroll = 4;
+    for (long long i = (long long)t0 * b.k + threadIdx.x; i < i1; i += kCountThreads * kUnroll) {
+      int id[kUnroll];
+      bool keep[kUnroll];
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j) {
-      const long long at = i + j * kCountThreads;
-      id[j] = -1;
-      if (at < i1) {
-        id[j] = __ldg(b.ids + at);
-        if (b.mask && !__ldg(b.mask + (unsigned)at / (unsigned)b.k)) id[j] = -1;
+      for (int j = 0; j < kUnroll; ++j) {
+        const long long at = i + j * kCountThreads;
+        id[j] = -1;
+        keep[j] = true;
+        if (at < i1) {
+          id[j] = __ldg(b.ids + at);
+          if (b.mask) keep[j] = __ldg(b.mask + (unsigned)at / (unsigned)b.k) != 0;
+        }
       }
-    }
 #pragma unroll
-    for (int j = 0; j < kUnroll; ++j)
-      if ((unsigned)id[j] < (unsigned)b.E) atomicAdd(&hist[id[j]], 1);
+      for (int j = 0; j < kUnroll; ++j)
+        if (keep[j] && (unsigned)id[j] < (unsigned)b.E) atomicAdd(&hist[id[j]], 1);
+    }
+    if (b.mask) {
+      for (int t = t0 + threadIdx.x; t < t1; t += kCountThreads)
+        if (__ldg(b.mask + t)) atomicAdd(&hist[b.E], 1);
+    } else if (threadIdx.x == 0) {
+      hist[b.E] = t1 - t0;
+    }
+    __syncthreads();
+    if (!waited) pdl_wait();           // the counts are zero
+    waited = true;
+    for (int e = threadIdx.x; e <= b.E; e += kCountThreads) {
+      const int n = hist[e];
+      hist[e] = 0;
+      if (n) atomicAdd(e < b.E ? counts + (long long)s * b.E + e : tokens + s, n);
+    }
+    __syncthreads();
+    t0 = t1;
   }
-  if (b.mask) {
-    int n = 0;
-    for (int t = t0 + threadIdx.x; t < t1; t += kCountThreads) n += __ldg(b.mask + t) != 0;
-    n = __reduce_add_sync(kFull, n);
-    if ((threadIdx.x & 31) == 0 && n) atomicAdd(&hist[b.E], n);
-  } else if (threadIdx.x == 0) {
-    hist[b.E] = t1 - t0;
-  }
-  cluster_sync();
-  for (int e = (int)rank * kCountThreads + threadIdx.x; e <= b.E; e += (int)nr * kCountThreads) {
-    int n = 0;
-    for (uint32_t k = 0; k < nr; ++k) n += ld_cluster(&hist[e], k);
-    if (e < b.E) counts[(long long)s * b.E + e] = n;
-    else tokens[s] = n;
-  }
-  if (ticket && blockIdx.x == 0 && threadIdx.x == 0) *ticket = 0;
-  cluster_sync();   // no CTA leaves while another still reads its histogram
+  if (!waited) pdl_wait();
 }
 
 // ---------------------------------------------------------------------------
@@ -133,65 +152,135 @@ __device__ __forceinline__ int expert_of(int i, int j, int lane) {
   return kVec ? (i * 32 + lane) * 4 + j : (i * 4 + j) * 32 + lane;
 }
 
+// A warp's ring of logit rows in shared memory, filled by asynchronous copies.
+// Every lane copies and reads its own experts only, so that its own copies'
+// completion is all there is to wait for.  kSlots rows are on their way per warp:
+// 16 warps an SM and a latency of about 1.5 us need two rows each at full
+// bandwidth; with one (a row ahead in registers) the loss kernel took 17.8 us
+// for 16384 x 896, with this ring 11.
+constexpr int kSlots = 3;
+
 template <int kNI, bool kVec>
-__device__ __forceinline__ void load_row(float (&v)[kNI][4], const float* row, int E, int lane) {
+struct RowRing {
+  float* slots;            // this lane's part of slot 0: [kNI][4] at a stride of 32 lanes
+  __device__ __forceinline__ RowRing(float* smem, int warp, int lane)
+      : slots(smem + (size_t)warp * kSlots * kNI * 128 + lane * 4) {}
+
+  __device__ __forceinline__ void fetch(int slot, const float* row, int E, int lane) {
+    const uint32_t dst = smem_u32(slots + slot * kNI * 128);
 #pragma unroll
-  for (int i = 0; i < kNI; ++i) {
-    if (kVec) {
-      float4 a = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      if (expert_of<kNI, kVec>(i, 0, lane) < E)
-        a = __ldcs(reinterpret_cast<const float4*>(row + expert_of<kNI, kVec>(i, 0, lane)));
-      v[i][0] = a.x; v[i][1] = a.y; v[i][2] = a.z; v[i][3] = a.w;
-    } else {
+    for (int i = 0; i < kNI; ++i) {
+      if (kVec) {
+        const int e = expert_of<kNI, kVec>(i, 0, lane);
+        if (e < E)
+          asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst + i * 512), "l"(row + e)
+                       : "memory");
+      } else {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int e = expert_of<kNI, kVec>(i, j, lane);
-        v[i][j] = e < E ? __ldcs(row + e) : -INFINITY;
+        for (int j = 0; j < 4; ++j) {
+          const int e = expert_of<kNI, kVec>(i, j, lane);
+          if (e < E)
+            asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst + i * 512 + j * 4),
+                         "l"(row + e)
+                         : "memory");
+        }
       }
     }
   }
-}
+  static __device__ __forceinline__ void commit() {
+    asm volatile("cp.async.commit_group;" ::: "memory");
+  }
+  // the oldest of the kSlots groups has landed
+  static __device__ __forceinline__ void wait_oldest() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(kSlots - 1) : "memory");
+  }
+  __device__ __forceinline__ float4 own(int slot, int i) const {
+    return *reinterpret_cast<const float4*>(slots + (slot * kNI + i) * 128);
+  }
+  __device__ __forceinline__ void clear(int slot) {
+#pragma unroll
+    for (int i = 0; i < kNI; ++i)
+      *reinterpret_cast<float4*>(slots + (slot * kNI + i) * 128) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+  }
+  // where expert e's element of a slot is (any lane's)
+  __device__ __forceinline__ float* place(int slot, int e, int lane) {
+    const int at = kVec ? e : (e & ~127) + (e & 31) * 4 + ((e >> 5) & 3);
+    return slots - lane * 4 + slot * kNI * 128 + at;
+  }
+  __device__ __forceinline__ void read(float (&v)[kNI][4], int slot, int E, int lane) const {
+#pragma unroll
+    for (int i = 0; i < kNI; ++i) {
+      const float4 a = own(slot, i);
+      const float x[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        v[i][j] = expert_of<kNI, kVec>(i, j, lane) < E ? x[j] : -INFINITY;
+    }
+  }
+};
 
-// Walk of a warp's tokens through the sequences: `c` holds the counts of the
-// current one, `unit` E / (k n) and `part` 1 / (S n) (0 without valid tokens).
+// Walk of a warp's tokens, in ascending order, through the sequences: `c` holds the
+// counts of the current one, `unit` E / (k n) and `part` 1 / (S n) (0 without valid
+// tokens), bit i of `keep` whether token `base` + i counts as far as the mask goes
+// (one load for 32 tokens: a load a token would be a latency a token).
 template <int kNI, bool kVec>
 struct SequenceWalk {
-  int s = -1, begin = 0, end = 0;
+  int s = 0, begin = 0, end = 0, base = 0;
+  unsigned keep = 0;
+  bool fresh = true;       // the counts of sequence s are not loaded yet
   float unit = 0.0f, part = 0.0f;
   float c[kNI][4];
 
-  // moves to the sequence of token t (tokens come in ascending order)
-  __device__ __forceinline__ void at(const RouterBatch& b, const int32_t* counts,
+  // The place of the warp's first token; reads the call's inputs only.
+  __device__ __forceinline__ void start(const RouterBatch& b, int t, int lane) {
+    find(b, t);
+    masks(b, t, lane);
+  }
+  __device__ __forceinline__ void find(const RouterBatch& b, int t) {
+    s = sequence_of(b, t);
+    const int2 r = sequence_range(b, s);
+    begin = r.x;
+    end = r.y;
+    fresh = true;
+  }
+  __device__ __forceinline__ void masks(const RouterBatch& b, int t, int lane) {
+    base = t;
+    keep = b.mask ? __ballot_sync(kFull, t + lane < b.T && __ldg(b.mask + t + lane) != 0) : kFull;
+  }
+
+  // Moves to token t; whether it counts.
+  __device__ __forceinline__ bool at(const RouterBatch& b, const int32_t* counts,
                                      const int32_t* tokens, int t, int lane) {
-    if (s >= 0 && t < end) return;
-    if (!b.seq) {
-      s = 0; begin = 0; end = b.T;
-    } else {
-      int lo = 0, hi = b.S - 1;       // the last sequence that begins at or before t
-      while (lo < hi) {
-        const int mid = (lo + hi + 1) >> 1;
-        if (__ldg(b.seq + mid) <= t) lo = mid; else hi = mid - 1;
-      }
-      s = lo;
-      const int2 r = sequence_range(b, s);
-      begin = r.x;
-      end = r.y;
-    }
-    const int n = __ldg(tokens + s);
-    unit = n > 0 ? (float)b.E / ((float)b.k * (float)n) : 0.0f;
-    part = n > 0 ? 1.0f / ((float)b.S * (float)n) : 0.0f;
+    if (t >= end && s + 1 < b.S) find(b, t);
+    if (t >= base + 32) masks(b, t, lane);
+    if (t < begin || t >= end || !(keep >> (t - base) & 1u)) return false;
+    if (fresh) load(b, counts, tokens, lane);
+    return true;
+  }
+  __device__ __forceinline__ void load(const RouterBatch& b, const int32_t* counts,
+                                       const int32_t* tokens, int lane) {
+    fresh = false;
     const int32_t* row = counts + (long long)s * b.E;
 #pragma unroll
-    for (int i = 0; i < kNI; ++i)
+    for (int i = 0; i < kNI; ++i) {
+      int4 n = make_int4(0, 0, 0, 0);
+      if (kVec) {
+        if (expert_of<kNI, kVec>(i, 0, lane) < b.E)
+          n = __ldcg(reinterpret_cast<const int4*>(row + expert_of<kNI, kVec>(i, 0, lane)));
+      } else {
+        int x[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int e = expert_of<kNI, kVec>(i, j, lane);
-        c[i][j] = e < b.E ? (float)__ldg(row + e) : 0.0f;
+        for (int j = 0; j < 4; ++j) {
+          const int e = expert_of<kNI, kVec>(i, j, lane);
+          x[j] = e < b.E ? __ldcg(row + e) : 0;
+        }
+        n = make_int4(x[0], x[1], x[2], x[3]);
       }
-  }
-  // whether token t of the walk counts
-  __device__ __forceinline__ bool valid(const RouterBatch& b, int t) const {
-    return t >= begin && t < end && (!b.mask || __ldg(b.mask + t) != 0);
+      c[i][0] = (float)n.x; c[i][1] = (float)n.y; c[i][2] = (float)n.z; c[i][3] = (float)n.w;
+    }
+    const int n = __ldcg(tokens + s);
+    unit = n > 0 ? (float)b.E / ((float)b.k * (float)n) : 0.0f;
+    part = n > 0 ? 1.0f / ((float)b.S * (float)n) : 0.0f;
   }
 };
 
@@ -242,30 +331,38 @@ __global__ void __launch_bounds__(kWarps * 32, 2)
 loss_kernel(const RouterBatch b, float alpha, const int32_t* __restrict__ counts,
             const int32_t* __restrict__ tokens, int per_warp, float* __restrict__ partial,
             unsigned* __restrict__ ticket, float* __restrict__ loss) {
+  extern __shared__ __align__(16) float ring_smem[];
   __shared__ float sums[kWarps];
   __shared__ bool last;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_trigger();
-  pdl_wait();
   const long long w = (long long)blockIdx.x * kWarps + warp;
   const int t0 = (int)min(w * per_warp, (long long)b.T), t1 = min(t0 + per_warp, b.T);
+  RowRing<kNI, kVec> ring(ring_smem, warp, lane);
+  // the logits are complete (see the counts); the counts are not
+  for (int i = 0; i < kSlots; ++i) {
+    if (t0 + i < t1) ring.fetch(i, b.logits + (long long)(t0 + i) * b.E, b.E, lane);
+    ring.commit();
+  }
   SequenceWalk<kNI, kVec> q;
+  if (t0 < t1) q.start(b, t0, lane);
+  pdl_wait();
   float total = 0.0f;
-  float next[kNI][4];
-  if (t0 < t1) load_row<kNI, kVec>(next, b.logits + (long long)t0 * b.E, b.E, lane);
+  int slot = 0;
   for (int t = t0; t < t1; ++t) {
     float v[kNI][4];
-#pragma unroll
-    for (int i = 0; i < kNI; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) v[i][j] = next[i][j];
-    if (t + 1 < t1) load_row<kNI, kVec>(next, b.logits + (long long)(t + 1) * b.E, b.E, lane);
-    q.at(b, counts, tokens, t, lane);
-    if (!q.valid(b, t)) continue;
-    bool tiny;
-    const float2 zd = row_sums<kNI, kVec>(v, q.c, &tiny);
-    if (zd.x > 0.0f) total += q.part * (q.unit * zd.y / zd.x);
-    else if (!(zd.x == 0.0f)) total += zd.x;      // NaN logits stay NaN
+    ring.wait_oldest();
+    if (q.at(b, counts, tokens, t, lane)) {
+      ring.read(v, slot, b.E, lane);
+      bool tiny;
+      const float2 zd = row_sums<kNI, kVec>(v, q.c, &tiny);
+      if (zd.x > 0.0f) total += q.part * (q.unit * zd.y / zd.x);
+      else if (!(zd.x == 0.0f)) total += zd.x;      // NaN logits stay NaN
+    }
+    // refilled once its row is used
+    if (t + kSlots < t1) ring.fetch(slot, b.logits + (long long)(t + kSlots) * b.E, b.E, lane);
+    ring.commit();
+    slot = slot + 1 == kSlots ? 0 : slot + 1;
   }
   if (lane == 0) sums[warp] = total;
   __syncthreads();
@@ -307,35 +404,74 @@ struct BackwardArgs {
 template <int kNI, bool kVec>
 __global__ void __launch_bounds__(kWarps * 32, 2)
 backward_kernel(const RouterBatch b, const BackwardArgs a) {
-  // the weights' gradient of the token at hand, by expert (zero but at the chosen ones)
-  __shared__ float add_all[kWarps][kNI * 128];
+  extern __shared__ __align__(16) float ring_smem[];
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-  float* add = add_all[warp];
   pdl_trigger();
-  for (int e = lane; e < kNI * 128; e += 32) add[e] = 0.0f;
-  __syncwarp();
   pdl_wait();
   const long long w = (long long)blockIdx.x * kWarps + warp;
   const int t0 = (int)min(w * a.per_warp, (long long)b.T), t1 = min(t0 + a.per_warp, b.T);
   const float gl = a.grad_loss ? a.alpha * __ldg(a.grad_loss) : 0.0f;
   SequenceWalk<kNI, kVec> q;
-  float next[kNI][4];
-  if (t0 < t1 && a.grad_loss) load_row<kNI, kVec>(next, b.logits + (long long)t0 * b.E, b.E, lane);
+  RowRing<kNI, kVec> ring(ring_smem, warp, lane);
+  if (t0 < t1 && a.grad_loss) {
+    q.start(b, t0, lane);
+    for (int i = 0; i < kSlots; ++i) {
+      if (t0 + i < t1) ring.fetch(i, b.logits + (long long)(t0 + i) * b.E, b.E, lane);
+      ring.commit();
+    }
+  }
+  // the j-th chosen expert of a token and its gradient are lane j's; they are loaded
+  // a token ahead, as is the expert's logit where the row itself is not read
+  auto choice = [&](int t, int& id, float& g) {
+    id = -1;
+    g = 0.0f;
+    if (a.grad_w && t < t1 && lane < b.k) {
+      id = __ldg(b.ids + (long long)t * b.k + lane);
+      g = __ldg(a.grad_w + (long long)t * b.k + lane);
+    }
+  };
+  auto logit = [&](int t, int id) {
+    return !a.grad_loss && (unsigned)id < (unsigned)b.E ? __ldg(b.logits + (long long)t * b.E + id)
+                                                       : -INFINITY;
+  };
+  int id1, id2;
+  float g1, g2, l1;
+  choice(t0, id1, g1);
+  choice(t0 + 1, id2, g2);
+  l1 = logit(t0, id1);
+  int slot = 0;
   for (int t = t0; t < t1; ++t) {
     const long long row = (long long)t * b.E;
     float v[kNI][4];
-    // 1. the weights' gradient: lane j has the j-th chosen expert
-    int id = -1;
+    int id = id1;
+    float g = g1, l = l1;
+    id1 = id2;
+    g1 = g2;
+    l1 = logit(t + 1, id1);
+    choice(t + 2, id2, g2);
+    if ((unsigned)id >= (unsigned)b.E) {       // no choice of this lane's, or a dropped one
+      id = -1;
+      g = 0.0f;
+    }
+    // 1. the balance loss's gradient: coef (c - mean) s (1 - s)
+    float coef = 0.0f, mean = 0.0f;
+    bool tiny = false;
+    if (a.grad_loss) {
+      ring.wait_oldest();
+      __syncwarp();                            // the whole row has landed
+      if (id >= 0) l = *ring.place(slot, id, lane);
+      if (q.at(b, a.counts, a.tokens, t, lane)) {
+        ring.read(v, slot, b.E, lane);
+        const float2 zd = row_sums<kNI, kVec>(v, q.c, &tiny);
+        if (!(zd.x == 0.0f)) {
+          coef = gl * q.part * q.unit / zd.x;
+          mean = zd.y / zd.x;
+        }
+      }
+    }
+    // 2. the weights' gradient: lane j puts the j-th chosen expert's in its place
+    // of the slot, whose row has been used
     if (a.grad_w) {
-      float l = -INFINITY, g = 0.0f;
-      if (lane < b.k) {
-        id = __ldg(b.ids + (long long)t * b.k + lane);
-        if ((unsigned)id >= (unsigned)b.E) id = -1;      // a dropped choice
-      }
-      if (id >= 0) {
-        l = __ldg(b.logits + row + id);
-        g = __ldg(a.grad_w + (long long)t * b.k + lane);
-      }
       const float s = sigmoid_f(l);
       float d = a.rsf * g * s;
       if (a.renorm) {
@@ -348,35 +484,22 @@ backward_kernel(const RouterBatch b, const BackwardArgs a) {
         p = z == 0.0f ? 0.0f : p / z;
         d = a.rsf * (g - warp_sum(g * p)) * p;
       }
-      if (id >= 0) add[id] = d * (1.0f - s);
+      __syncwarp();                            // every lane has its logit
+      ring.clear(slot);
       __syncwarp();
-    }
-    // 2. the balance loss's
-    float coef = 0.0f, mean = 0.0f;
-    bool tiny = false;
-    if (a.grad_loss) {
-#pragma unroll
-      for (int i = 0; i < kNI; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) v[i][j] = next[i][j];
-      if (t + 1 < t1) load_row<kNI, kVec>(next, b.logits + row + b.E, b.E, lane);
-      q.at(b, a.counts, a.tokens, t, lane);
-      if (q.valid(b, t)) {
-        const float2 zd = row_sums<kNI, kVec>(v, q.c, &tiny);
-        if (!(zd.x == 0.0f)) {
-          coef = gl * q.part * q.unit / zd.x;
-          mean = zd.y / zd.x;
-        }
-      }
+      if (id >= 0) *ring.place(slot, id, lane) = d * (1.0f - s);
+      __syncwarp();
     }
 #pragma unroll
     for (int i = 0; i < kNI; ++i) {
-      float o[4];
+      float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      if (a.grad_w) {
+        const float4 x = ring.own(slot, i);
+        o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+      }
+      if (coef != 0.0f) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int e = expert_of<kNI, kVec>(i, j, lane);
-        o[j] = a.grad_w ? add[e] : 0.0f;
-        if (coef != 0.0f) {
+        for (int j = 0; j < 4; ++j) {
           const float s = v[i][j];
           o[j] += coef * (q.c[i][j] - mean) * (tiny ? s : s * (1.0f - s));
         }
@@ -392,11 +515,12 @@ backward_kernel(const RouterBatch b, const BackwardArgs a) {
         }
       }
     }
-    if (a.grad_w) {
-      __syncwarp();
-      if (id >= 0) add[id] = 0.0f;
-      __syncwarp();
+    // the slot is refilled once all of the row's uses are over
+    if (a.grad_loss) {
+      if (t + kSlots < t1) ring.fetch(slot, b.logits + row + (long long)kSlots * b.E, b.E, lane);
+      ring.commit();
     }
+    slot = slot + 1 == kSlots ? 0 : slot + 1;
   }
 }
 
@@ -410,6 +534,16 @@ TokenGrid token_grid(int T) {
   g.per_warp = (int)((T + warps - 1) / warps);
   g.ctas = ceil_div(ceil_div(T, g.per_warp), kWarps);
   return g;
+}
+
+// A token kernel with its warps' rings of kNI * 128 floats a slot.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_ring(void (*kernel)(KArgs...), int ctas, int ni, cudaStream_t s, Args&&... args) {
+  const size_t smem = (size_t)kWarps * kSlots * ni * 128 * sizeof(float);
+  const cudaError_t e =
+      cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+  if (e != cudaSuccess) return e;
+  return launch_k(kernel, dim3(ctas), dim3(kWarps * 32), smem, s, std::forward<Args>(args)...);
 }
 
 #define LMOE_BY_EXPERTS(E, CALL)                                  \
@@ -445,15 +579,21 @@ cudaError_t launch_balance_loss(const RouterBatch& b, float alpha, float* loss, 
                                 int32_t* tokens, void* workspace, cudaStream_t s) {
   unsigned* ticket = static_cast<unsigned*>(workspace);
   float* partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256);
-  // eight CTAs a sequence where it is long enough to feed them
-  const int cluster = (long long)b.T * b.k > 4096ll * b.S ? 8 : 1;
-  cudaError_t e = launch_k_cluster(count_kernel, dim3(b.S * cluster), dim3(kCountThreads), 0, s,
-                                   cluster, b, counts, tokens, ticket);
+  const long long n = (long long)b.S * b.E;
+  cudaError_t e = launch_k(zero_kernel, dim3((unsigned)(n < 256ll * 64 ? (n + 255) / 256 : 64)), dim3(256),
+                           0, s, counts, n, tokens, b.S, ticket);
+  if (e != cudaSuccess) return e;
+  // a CTA an SM, but no fewer tokens each than fill its threads once
+  const int least = ceil_div(kCountThreads, b.k);
+  const int even = ceil_div(b.T, num_sms());
+  const int per_cta = even > least ? even : least;
+  e = launch_k(count_kernel, dim3(ceil_div(b.T, per_cta)), dim3(kCountThreads), 0, s, b, per_cta, counts,
+               tokens);
   if (e != cudaSuccess) return e;
   const TokenGrid g = token_grid(b.T);
 #define LMOE_CALL(NI, VEC)                                                                       \
-  launch_k(loss_kernel<NI, VEC>, dim3(g.ctas), dim3(kWarps * 32), 0, s, b, alpha,                 \
-           (const int32_t*)counts, (const int32_t*)tokens, g.per_warp, partial, ticket, loss)
+  launch_ring(loss_kernel<NI, VEC>, g.ctas, NI, s, b, alpha, (const int32_t*)counts,              \
+              (const int32_t*)tokens, g.per_warp, partial, ticket, loss)
   LMOE_BY_EXPERTS(b.E, LMOE_CALL);
 #undef LMOE_CALL
 }
@@ -465,7 +605,7 @@ cudaError_t launch_router_backward(const RouterBatch& b, const float* grad_w, in
   const TokenGrid g = token_grid(b.T);
   const BackwardArgs a{grad_w, grad_loss, counts, tokens, alpha, rsf, renorm, g.per_warp, grad};
 #define LMOE_CALL(NI, VEC) \
-  launch_k(backward_kernel<NI, VEC>, dim3(g.ctas), dim3(kWarps * 32), 0, s, b, a)
+  launch_ring(backward_kernel<NI, VEC>, g.ctas, NI, s, b, a)
   LMOE_BY_EXPERTS(b.E, LMOE_CALL);
 #undef LMOE_CALL
 }
