@@ -144,6 +144,11 @@ struct Ws {
   float *A8s, *act8s;
 };
 
+// Up to this many rows the experts' weights are streamed for a few tokens at a
+// time (each expert has them re-read from L2 per eight rows; at more rows a heavily
+// loaded expert would be re-read too often).
+constexpr long long kFp8StreamRows = 512;
+
 // Which form the routed experts' weights have.
 enum class Experts { kBf16, kMxfp4, kFp8 };
 
@@ -226,7 +231,7 @@ size_t carve(const lmoe_dims& d, char* base, Ws* ws, Experts form = Experts::kBf
   if (form == Experts::kFp8) {
     w.A8 = c.take<uint8_t>(T * k * L);
     w.A8s = c.take<float>(T * k * (L / kFp8Block));
-    w.act8 = c.take<uint8_t>(T * k * dI);
+    w.act8 = c.take<uint8_t>(T * k * dI * (T * k <= (size_t)kFp8StreamRows ? sizeof(float) : 1));
     w.act8s = c.take<float>(T * k * (dI / kFp8Block));
   }
   if (ws) *ws = w;
@@ -483,6 +488,7 @@ int check_fp8_experts(const lmoe_fp8_experts& w) {
 }
 
 // One stage of the e4m3 experts: 1 = act from x (product and SituGLU), 2 = y from act.
+// `act` holds codes with scales act_s, or up to kFp8StreamRows rows fp32 values.
 cudaError_t experts_fp8(const lmoe_fp8_experts& w, const uint8_t* x, const float* xs,
                         const int32_t* offsets, uint8_t* act, float* act_s, uint16_t* y,
                         long long rows, int E, int L, int d, float beta, float linear_beta,
@@ -491,6 +497,7 @@ cudaError_t experts_fp8(const lmoe_fp8_experts& w, const uint8_t* x, const float
   g.rows = rows;
   g.groups = E;
   g.offsets = offsets;
+  const bool stream = rows <= kFp8StreamRows;
   if (stage == 1) {
     g.X = x;
     g.xs = xs;
@@ -498,11 +505,13 @@ cudaError_t experts_fp8(const lmoe_fp8_experts& w, const uint8_t* x, const float
     g.ws = w.w13_scales;
     g.feat = 2 * d;
     g.K = L;
-    g.act = act;
+    if (stream) g.act_f32 = reinterpret_cast<float*>(act);
+    else g.act = act;
     g.act_s = act_s;
     g.beta = beta;
     g.linear_beta = linear_beta;
   } else {
+    if (stream) g.act_in = reinterpret_cast<const float*>(act);
     g.X = act;
     g.xs = act_s;
     g.W = w.w2_codes;
@@ -514,8 +523,15 @@ cudaError_t experts_fp8(const lmoe_fp8_experts& w, const uint8_t* x, const float
   return launch_fp8_gemm(g, s);
 }
 
-// Workspace of lmoe_experts_fp8: the activations' codes, then their scales.
-size_t fp8_act_bytes(long long rows, int d) { return ((size_t)rows * d + 255) & ~size_t(255); }
+// Workspace of the activations between the two: their codes (or few rows' fp32
+// values), then the scales.
+size_t fp8_act_bytes(long long rows, int d) {
+  const size_t n = (size_t)rows * d * (rows <= kFp8StreamRows ? sizeof(float) : 1);
+  return (n + 255) & ~size_t(255);
+}
+size_t fp8_scale_bytes(long long rows, int d) {
+  return ((size_t)rows * (d / kFp8Block) * sizeof(float) + 255) & ~size_t(255);
+}
 
 // The checks of the router's training entry points that need no pointer.
 int validate_router(int T, int E, int topk, int S, float alpha) {
@@ -1169,7 +1185,7 @@ size_t lmoe_experts_fp8_workspace_bytes(int64_t rows, int E, int latent, int int
   if (rows < 0 || rows > kMaxFp8Rows || E < 1 || E > 1024 || latent <= 0 || latent % kFp8Block ||
       latent > kMaxFp8Dim || inter <= 0 || inter % kFp8Block || inter > kMaxFp8Dim)
     return 0;
-  return fp8_act_bytes(rows, inter) + fp8_act_bytes(rows, inter / kFp8Block * 4) + 256;
+  return fp8_act_bytes(rows, inter) + fp8_scale_bytes(rows, inter) + 256;
 }
 
 int lmoe_experts_fp8(const lmoe_fp8_experts* experts, const uint8_t* x, const float* xs,

@@ -20,33 +20,11 @@
 #include <mutex>
 
 #include "fp8.cuh"
+#include "fp8_quant.cuh"
 #include "tc_ptx.cuh"
 
 namespace lmoe {
 namespace {
-
-constexpr float kE4m3Max = 448.0f;
-constexpr float kTinyAmax = 7.888609052210118e-31f;   // 2^-100
-
-// two fp32 -> two e4m3 (round to nearest even, saturating; NaN stays NaN)
-__device__ __forceinline__ uint32_t pack_e4m3x2(float lo, float hi) {
-  uint16_t r;
-  asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(hi), "f"(lo));
-  return r;
-}
-__device__ __forceinline__ uint32_t pack_e4m3x4(float a, float b, float c, float d) {
-  return pack_e4m3x2(a, b) | (pack_e4m3x2(c, d) << 16);
-}
-
-struct BlockScale {
-  float scale, inv;
-};
-// `amax` as bits of a non-negative float: their order is the values', NaN above
-// infinity, so that a maximum over them keeps a NaN
-__device__ __forceinline__ BlockScale block_scale(uint32_t amax) {
-  const float a = __uint_as_float(max(amax, __float_as_uint(kTinyAmax)));
-  return {__fdiv_rn(a, kE4m3Max), __fdiv_rn(kE4m3Max, a)};
-}
 
 __device__ __forceinline__ uint4 ld_stream(const void* p) {
   uint4 v;
@@ -226,6 +204,7 @@ enum : int { kErrProducer = 1, kErrMmaFull = 2, kErrMmaTmem = 3, kErrEpilogue = 
 
 struct Fp8Params {
   int feat, nkb, groups, nfeat, stages, ws_rows;
+  int splits;        // > 1: clusters of this many CTAs share a tile's K blocks (one tile a cluster)
   long long rows;
   const int32_t* offsets;
   const float* xs;
@@ -348,12 +327,35 @@ __device__ void build_groups(const Fp8Params& p, int* prefix, int* first, int* e
   }
 }
 
-// kNH: 128-row weight boxes a tile (MMA N = 128 kNH).  kSitu (kNH == 2): the
-// boxes are the gate and the up rows of the same 128 features.
-template <int kNH, bool kSitu>
+// Split K: a cluster's CTAs leave their partial tiles in shared memory, rows
+// kPartPad floats longer than the tile (so that a warp's 16-byte stores, a row a
+// lane, meet no bank twice), and each then sums its share of the tile over the
+// cluster in rank order.
+constexpr int kPartPad = 4;
+constexpr int kMaxSplits = 8;
+
+__device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
+  uint32_t a;
+  float4 v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(a)
+               : "memory");
+  return v;
+}
+
+// Forms of the product.  kFormSitu (kNH == 2): the weight boxes are the gate and
+// the up rows of the same 128 features.  kFormSplit: split K, one tile a cluster.
+enum : int { kFormPlain = 0, kFormSitu = 1, kFormSplit = 2 };
+
+// kNH: 128-row weight boxes a tile (MMA N = 128 kNH).
+template <int kNH, int kForm>
 __global__ void __launch_bounds__(kThreads, 1)
 fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmXs,
                 const __grid_constant__ CUtensorMap tmW, const Fp8Params p) {
+  constexpr bool kSitu = kForm == kFormSitu;
+  constexpr bool kSplit = kForm == kFormSplit;
   constexpr int kBN = 128 * kNH;
   constexpr int kAcc = 512 / kBN;            // TMEM accumulators
   constexpr int kCols = kBN / 2;             // columns an epilogue thread owns
@@ -411,6 +413,12 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
   const uint32_t tmem_base = *tmem_holder;
   const int ntok = p.offsets ? prefix[p.groups] : (int)((p.rows + BM - 1) / BM);
   const int U = ntok * p.nfeat;
+  // this CTA's tiles and K blocks
+  const int rank = kSplit ? (int)cluster_rank() : 0;
+  const int u0 = kSplit ? (int)blockIdx.x / p.splits : (int)blockIdx.x;
+  const int ustep = kSplit ? U : (int)gridDim.x;
+  const int kb0 = kSplit ? p.nkb * rank / p.splits : 0;
+  const int kb1 = kSplit ? p.nkb * (rank + 1) / p.splits : p.nkb;
 
   // the launch's 168 registers a thread, split anew: 168 * 384 = 56 * 128 + 224 * 256
   if (warp < kEpiWarp0) {
@@ -419,7 +427,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       // ---------------- TMA producer ----------------
       uint32_t it = 0, s = 0, ph = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < U && ok; u += gridDim.x) {
+      for (int u = u0; u < U && ok; u += ustep) {
         const Tile x = tile_of(p, prefix, first, end, u);
         const bool small = x.nvalid <= kSmallTok;
         // weight rows of the boxes; a second box past the last feature is left out
@@ -427,7 +435,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
         const int w1 = w0 + (kSitu ? p.feat / 2 : 128);
         const bool two = kNH == 2 && (kSitu || x.feat_tile * kBN + 128 < p.feat);
         const uint32_t bytes = (small ? kSmallTok * kBK : kBoxBytes) + (two ? 2u : 1u) * kBoxBytes;
-        for (int kb = 0; kb < p.nkb; ++kb, ++it) {
+        for (int kb = kb0; kb < kb1; ++kb, ++it) {
           if (!wait_phase(empty_bar(s), ph ^ 1u, abort_flag, p.err, kErrProducer)) { ok = false; break; }
           const uint32_t bar = full_bar(s);
           const uint32_t sa = smem_u32(smem) + s * kStageBytes;
@@ -451,8 +459,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       const uint64_t d0 = sdesc(smem_u32(smem));
       uint32_t s = 0, ph = 0, acc = 0, aph = 0;
       bool ok = true;
-      for (int u = blockIdx.x; u < U && ok; u += gridDim.x) {
-        for (int kb = 0; kb < p.nkb; ++kb) {
+      for (int u = u0; u < U && ok; u += ustep) {
+        for (int kb = kb0; kb < kb1; ++kb) {
           if (!wait_phase(tempty_bar(acc), aph ^ 1u, abort_flag, p.err, kErrMmaTmem) ||
               !wait_phase(full_bar(s), ph, abort_flag, p.err, kErrMmaFull)) {
             ok = false;
@@ -484,7 +492,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
     const int r = q * 32 + lane;            // token row of the tile
     uint32_t acc = 0, aph = 0, par = 0;
     bool ok = true;
-    for (int u = blockIdx.x; u < U && ok; u += gridDim.x) {
+    for (int u = u0; u < U && ok; u += ustep) {
       const Tile x = tile_of(p, prefix, first, end, u);
       // scale blocks of this thread's columns (SituGLU: gate and up)
       const int blk = kSitu ? x.feat_tile : x.feat_tile * kNH + (kNH == 2 ? h : 0);
@@ -500,13 +508,13 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       // the scales of a K block are loaded one block ahead of its sums
       float nx = 0.0f, nw = 0.0f, nw2 = 0.0f;
       if (active) {
-        nx = ld_ahead(xsp);
-        nw = ld_ahead(wsp);
-        if (kSitu) nw2 = ld_ahead(wsp2);
+        nx = ld_ahead(xsp + kb0);
+        nw = ld_ahead(wsp + kb0);
+        if (kSitu) nw2 = ld_ahead(wsp2 + kb0);
       }
-      for (int kb = 0; kb < p.nkb; ++kb) {
+      for (int kb = kb0; kb < kb1; ++kb) {
         const float fx = nx, fw = nw, fw2 = nw2;
-        if (active && kb + 1 < p.nkb) {
+        if (active && kb + 1 < kb1) {
           nx = ld_ahead(xsp + kb + 1);
           nw = ld_ahead(wsp + kb + 1);
           if (kSitu) nw2 = ld_ahead(wsp2 + kb + 1);
@@ -548,7 +556,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
 #pragma unroll
           for (int j = 0; j < 32; ++j) {
             y[j] = situ2_pair(y[j], y[32 + j], p.sp);
-            m = max(m, max((uint32_t)y[j] & 0x7FFFFFFFu, (uint32_t)(y[j] >> 32) & 0x7FFFFFFFu));
+            m = max(m, max(abs_bits(f2_lo(y[j])), abs_bits(f2_hi(y[j]))));
           }
           uint32_t* ex = amax_ex + par * 256;
           ex[h * 128 + r] = m;
@@ -572,6 +580,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             if (h == 0) p.act_s[row * (d / 128) + x.feat_tile] = bs.scale;
           }
           par ^= 1u;
+        }
+      } else if constexpr (kSplit) {
+        // every MMA of this CTA has completed: the ring is free
+        if (active && row_ok) {
+          float* o = reinterpret_cast<float*>(smem) + r * (kBN + kPartPad) + h * kCols;
+#pragma unroll
+          for (int j = 0; j < kCols / 2; j += 2)
+            *reinterpret_cast<float4*>(o + 2 * j) =
+                make_float4(f2_lo(y[j]), f2_hi(y[j]), f2_lo(y[j + 1]), f2_hi(y[j + 1]));
         }
       } else if (active && row_ok) {
         const int col0 = x.feat_tile * kBN + h * kCols;
@@ -597,6 +614,34 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
     }
   }
 
+  if constexpr (kSplit) {
+    __syncwarp();
+    cluster_sync();
+    const Tile x = tile_of(p, prefix, first, end, u0);
+    const int col0 = x.feat_tile * kBN;
+    const int cols = min(kBN, p.feat - col0);        // a multiple of 8
+    const int n4 = x.nvalid * (cols / 4);
+    const uint32_t part = smem_u32(smem);
+    for (int i = rank * kThreads + threadIdx.x; i < n4; i += p.splits * kThreads) {
+      const int row = i / (cols / 4), col = (i - row * (cols / 4)) * 4;
+      const uint32_t at = part + (uint32_t)(row * (kBN + kPartPad) + col) * 4u;
+      float4 v[kMaxSplits];
+#pragma unroll
+      for (int k = 0; k < kMaxSplits; ++k)
+        if (k < p.splits) v[k] = ld_cluster4(at, k);
+      float4 t = v[0];
+#pragma unroll
+      for (int k = 1; k < kMaxSplits; ++k)
+        if (k < p.splits) { t.x += v[k].x; t.y += v[k].y; t.z += v[k].z; t.w += v[k].w; }
+      const long long o = (x.row0 + row) * p.feat + col0 + col;
+      if (p.add) {
+        const uint2 a = __ldg(reinterpret_cast<const uint2*>(p.add + o));
+        t.x += bf16_lo(a.x); t.y += bf16_hi(a.x); t.z += bf16_lo(a.y); t.w += bf16_hi(a.y);
+      }
+      *reinterpret_cast<uint2*>(p.out + o) = make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
+    }
+    cluster_sync();     // no CTA leaves while another still reads its partial tile
+  }
   tc_fence_before();
   __syncthreads();
   if (warp == 1) {
@@ -628,10 +673,12 @@ bool make_map(CUtensorMap* m, const void* base, long long rows, int K, int box_r
 
 constexpr int kRingBytes = 192 * 1024;
 
-template <int kNH, bool kSitu>
-cudaError_t launch_form(const Fp8Gemm& g, cudaStream_t s) {
+template <int kNH, int kForm>
+cudaError_t launch_form(const Fp8Gemm& g, int splits, cudaStream_t s) {
+  constexpr bool kSitu = kForm == kFormSitu;
   constexpr int kBN = 128 * kNH;
   constexpr int kStage = (int)kBoxBytes * (1 + kNH);
+  static_assert(128 * (kBN + kPartPad) * 4 <= kRingBytes / kStage * kStage, "a partial tile fits the ring");
   Fp8Params p{};
   p.feat = g.feat;
   p.nkb = fp8_blocks(g.K);
@@ -647,6 +694,7 @@ cudaError_t launch_form(const Fp8Gemm& g, cudaStream_t s) {
   p.out = g.out;
   p.act = g.act;
   p.act_s = g.act_s;
+  p.splits = splits;
   p.err = device_error_word();
   p.sp = make_situ_params(g.beta > 0.0f ? g.beta : 1.0f, g.linear_beta);
   if (!p.err) return cudaErrorInvalidValue;
@@ -656,25 +704,61 @@ cudaError_t launch_form(const Fp8Gemm& g, cudaStream_t s) {
     return cudaErrorInvalidValue;
   const size_t smem = 1024 + (size_t)p.stages * kStage + (2 * p.stages + 2 * (512 / kBN) + 1) * 8 +
                       8 + 512 * 4 + kThreads / 32 * 4 + (g.offsets ? (3 * g.groups + 1) * 4 : 4);
-  auto* kern = fp8_gemm_kernel<kNH, kSitu>;
+  auto* kern = fp8_gemm_kernel<kNH, kForm>;
   cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   const long long tok = g.offsets ? (g.rows + BM - 1) / BM + (g.rows < g.groups ? g.rows : g.groups)
                                   : (g.rows + BM - 1) / BM;
   const long long units = tok * p.nfeat;
+  if (kForm == kFormSplit)
+    return launch_k_cluster(kern, dim3((unsigned)(units * splits)), dim3(kThreads), smem, s, splits, mx,
+                            mxs, mw, p);
   const int grid = units < num_sms() ? (int)units : num_sms();
   return launch_k(kern, dim3(grid), dim3(kThreads), smem, s, mx, mxs, mw, p);
+}
+
+// Tile width and K split of a dense product: the pair with the least modelled
+// time, in SM cycles.  A wave of CTAs costs its K blocks (the wider tile does twice
+// the work in less than twice the time), a fixed part (launch, prologue, first
+// load, output) and, split, the exchange of the partial tiles.  Clusters of 4 and 8
+// leave some SMs of a GPC without one.
+struct DenseForm {
+  bool wide;
+  int splits;
+};
+DenseForm dense_form(long long T, int N, int nkb, int nsm) {
+  constexpr double kBlock[2] = {650, 1000}, kFixed = 3000, kSplit = 2500, kExchange = 1.0 / 40;
+  DenseForm best{false, 1};
+  double least = -1;
+  const long long tok = (T + BM - 1) / BM;
+  const double rows = T < BM ? (double)T : (double)BM;
+  for (int wide = 0; wide < 2; ++wide) {
+    const int bn = wide ? 256 : 128;
+    const long long tiles = tok * ((N + bn - 1) / bn);
+    for (int c = 1; c <= kMaxSplits && c <= nkb; c *= 2) {
+      const int slots = c <= 2 ? nsm : nsm / 19 * (c == 4 ? 18 : 16);
+      // unsplit tiles are walked by resident CTAs, whose fixed part is paid once
+      const double waves = (double)((tiles * c + slots - 1) / slots);
+      const double blocks = (double)((nkb + c - 1) / c) * kBlock[wide];
+      const double cost = c == 1 ? waves * (blocks + 500) + kFixed
+                                 : waves * (blocks + kFixed + kSplit + rows * bn * 4 * kExchange);
+      if (least < 0 || cost < least) { least = cost; best = DenseForm{wide != 0, c}; }
+    }
+  }
+  return best;
 }
 
 }  // namespace
 
 cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
-  if (g.act) return launch_form<2, true>(g, s);
-  // 256 weight rows a tile halve the token operand's traffic and the MMA count; 128 where
-  // wider tiles would leave SMs without one
-  const long long tok = (g.rows + BM - 1) / BM;
-  const bool narrow = !g.offsets && tok * ((g.feat + 255) / 256) < num_sms();
-  return narrow || g.feat <= 128 ? launch_form<1, false>(g, s) : launch_form<2, false>(g, s);
+  if (g.act_f32 || g.act_in || (!g.offsets && g.rows <= kStreamRows)) return launch_fp8_stream(g, s);
+  if (g.act) return launch_form<2, kFormSitu>(g, 1, s);
+  DenseForm f{g.feat > 128, 1};
+  if (!g.offsets) f = dense_form(g.rows, g.feat, fp8_blocks(g.K), num_sms());
+  if (f.splits > 1)
+    return f.wide ? launch_form<2, kFormSplit>(g, f.splits, s)
+                  : launch_form<1, kFormSplit>(g, f.splits, s);
+  return f.wide ? launch_form<2, kFormPlain>(g, 1, s) : launch_form<1, kFormPlain>(g, 1, s);
 }
 
 cudaError_t launch_quantize_scatter_fp8(const uint16_t* Z, int T, int L, int k,

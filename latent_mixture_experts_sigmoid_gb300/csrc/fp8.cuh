@@ -29,9 +29,20 @@ struct Fp8Gemm {
   uint8_t* act;
   float* act_s;
   float beta, linear_beta;
+  // few rows an expert: the activations in fp32 [rows, d] between the two
+  // products, the first's output (instead of act) and the second's input
+  // (instead of X and xs), which quantises them by the same rule
+  float* act_f32;
+  const float* act_in;
 };
 
+// Dense products of up to this many token rows stream their weights through
+// registers (fp8_stream.cu).
+constexpr int kStreamRows = 16;
+
 cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s);
+// ... for few token rows (grouped: with act_f32 or act_in)
+cudaError_t launch_fp8_stream(const Fp8Gemm& g, cudaStream_t s);
 
 // codes / scales of bf16 x [rows, K], one scale per block_rows (1 or 128) rows x 128 columns
 cudaError_t launch_quantize_fp8(const uint16_t* x, uint8_t* codes, float* scales, long long rows,

@@ -105,7 +105,8 @@ def test_quantize_extreme_values(block_rows):
 
 @pytest.mark.parametrize("with_add", [False, True])
 @pytest.mark.parametrize("T,N,K", [
-    (1, 8, 16), (1, 128, 128), (1, 2048, 7168), (2, 136, 272), (8, 8192, 1024), (15, 256, 144),
+    (1, 8, 16), (1, 128, 128), (1, 2048, 7168), (2, 136, 272), (5, 1000, 4112), (8, 8192, 1024),
+    (9, 24, 7168), (15, 256, 144),
     (16, 264, 256), (17, 128, 512), (32, 1024, 2048), (33, 120, 640), (64, 1032, 128), (128, 256, 1024),
     (129, 392, 272), (255, 640, 400), (300, 512, 192), (513, 1000, 1168), (1024, 768, 512),
     (2050, 2056, 336)])
@@ -204,9 +205,12 @@ def expert_weights(g, E, L, d):
     return q
 
 
-def check_experts(x, xs, off, Q, L, d, beta, lbeta, y, act, act_s):
-    """Both stages against float64: the activations from the same x, y from the
-    GPU's own activations."""
+def check_experts(x, xs, off, Q, L, d, beta, lbeta, y):
+    """y against float64.  The kernel's activations differ from the reference's by
+    the first product's sum (through SituGLU's derivatives, |d gate_out| <= 1.1 and
+    |d up_out| <= 1) and by 2^-9 (the hardware tanh, 2^-11, twice, the exponential and
+    the reciprocal); their codes lie between those of the two ends of that range,
+    and y may be off by what that makes of them."""
     for e in range(len(off) - 1):
         a, b = int(off[e]), int(off[e + 1])
         if b <= a:
@@ -215,21 +219,22 @@ def check_experts(x, xs, off, Q, L, d, beta, lbeta, y, act, act_s):
         ref = O.situ(h[:, :d], h[:, d:], beta, lbeta)
         gate, up = h[:, :d], h[:, d:]
         up_out = lbeta * np.tanh(up / lbeta) if lbeta > 0 else up
-        gate_out = beta * np.tanh(gate / beta) / (1 + np.exp(-gate))
+        with np.errstate(over="ignore"):
+            gate_out = beta * np.tanh(gate / beta) / (1 + np.exp(-gate))
         eh = sum_tolerance(L) * mag
-        # h's error through the derivatives (|d gate_out| <= 1.1, |d up_out| <= 1), and 2^-9:
-        # the hardware tanh (2^-11, twice), exponential and reciprocal
         err = eh[:, :d] * 1.1 * np.abs(up_out) + eh[:, d:] * np.abs(gate_out) + 2.0 ** -9 * np.abs(ref)
-        amax = np.abs(ref).reshape(b - a, -1, 128).max(-1)
-        emax = err.reshape(b - a, -1, 128).max(-1)
-        s = act_s[a:b].astype(np.float64)
-        assert np.all(np.abs(s * 448 - amax) <= emax + 2.0 ** -22 * amax + 2.0 ** -99)
-        S = np.repeat(s, 128, 1)
-        v = F.e4m3_value(act[a:b]) * S
-        half = np.maximum((np.abs(ref) + err) * 2.0 ** -4, S * 2.0 ** -10)
-        assert np.all(np.abs(v - ref) <= half + err * (1 + 2.0 ** -4) + 2.0 ** -22 * np.abs(ref))
-        yr, ym = F.linear(act[a:b], act_s[a:b], Q["w2_q"][e], Q["w2_s"][e])
-        assert_close(y[a:b], yr, ym, d)
+        amax = np.maximum(np.abs(ref).reshape(b - a, -1, 128).max(-1), 2.0 ** -100)
+        es = np.repeat(err.reshape(b - a, -1, 128).max(-1) / amax + 2.0 ** -22, 128, 1)
+        S = np.repeat(amax / 448, 128, 1)
+        t = ref / S
+        delta = err / S + np.abs(t) * es
+        q, lo, hi = (F.e4m3_value(F.e4m3_code(v)) for v in (t, t - delta, t + delta))
+        D = np.maximum(hi - q, q - lo) * S + np.abs(q) * S * es
+        W2 = F.dequantize(Q["w2_q"][e], Q["w2_s"][e], 128)
+        yr, ym = (q * S) @ W2.T, (np.abs(q) * S) @ np.abs(W2).T
+        off_by = D @ np.abs(W2).T + sum_tolerance(d) * ym
+        bad = np.abs(y[a:b] - yr) > off_by + 2.0 ** -8 * (np.abs(yr) + off_by)
+        assert not bad.any(), (e, np.argwhere(bad)[:3])
 
 
 @pytest.mark.parametrize("E,L,d,counts,lbeta", [
@@ -241,6 +246,9 @@ def check_experts(x, xs, off, Q, L, d, beta, lbeta, y, act, act_s):
     (64, 128, 256, [i % 7 for i in range(64)], 8.0),
     (1024, 128, 128, [int(i % 9 == 4) * 2 for i in range(1024)], 8.0),
     (2, 2048, 512, [260, 140], 8.0),
+    (6, 512, 384, [8, 9, 16, 17, 0, 40], 8.0),       # passes of eight tokens
+    (900, 256, 128, [i % 2 for i in range(900)], 8.0),
+    (900, 128, 256, [int(i % 3 > 0) for i in range(900)], 8.0),    # over 512 rows, few each
 ])
 def test_experts_match_float64(E, L, d, counts, lbeta):
     from tests.gpu_util import host_bits
@@ -255,11 +263,7 @@ def test_experts_match_float64(E, L, d, counts, lbeta):
                         beta=BETA, linear_beta=lbeta)
     got = O.bf16_to_f64(host_bits(y))
     assert lm.lmoe_device_error() == 0
-    w = ws.cpu().numpy()
-    at = -(-R * d // 256) * 256
-    act = w[:R * d].reshape(R, d)
-    act_s = w[at:at + R * (d // 128) * 4].view(np.float32).reshape(R, d // 128)
-    check_experts(x, xs, off, Q, L, d, BETA, lbeta, got, act, act_s)
+    check_experts(x, xs, off, Q, L, d, BETA, lbeta, got)
     assert bool((buf[-GUARD:] == 7.0).all())
 
 
@@ -335,8 +339,8 @@ def test_layer_forward(T, E, topk, shared):
     rows = v["A"] if T <= 128 else v["Z"][tok_of_row]
     assert_stage_close(O.bf16_to_f64(rows), Zref[tok_of_row], "Z")
     x, xs = F.quantize(rows)
-    # y from the activations the GPU kept is checked in test_experts_match_float64; here the
-    # reference quantises its own, so a code may round the other way (2^-3 of a term)
+    # the bounds are test_experts_match_float64's: here a code may round the other way (2^-3
+    # of a term), far under the difference between experts
     yr, _, _ = F.experts(x, xs, offsets, Q, d.inter, d.beta, d.linear_beta)
     Y = O.bf16_to_f64(v["Y"])
     assert np.linalg.norm(Y - yr) <= 0.01 * np.linalg.norm(yr)
