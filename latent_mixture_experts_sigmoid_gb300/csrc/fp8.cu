@@ -420,9 +420,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
   const int kb0 = kSplit ? p.nkb * rank / p.splits : 0;
   const int kb1 = kSplit ? p.nkb * (rank + 1) / p.splits : p.nkb;
 
-  // the launch's 168 registers a thread, split anew: 168 * 384 = 56 * 128 + 224 * 256
+  // the launch's 168 registers a thread, split anew: 168 * 384 = 72 * 128 + 216 * 256
   if (warp < kEpiWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 56;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
     if (warp == 0 && lane == 0) {
       // ---------------- TMA producer ----------------
       uint32_t it = 0, s = 0, ph = 0;
@@ -485,7 +485,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       wait_phase(done_bar, 0u, &never, p.err, kErrDone);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 224;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
     // ---------------- epilogue ----------------
     const int q = warp & 3;                 // TMEM lane quarter this warp may access
     const int h = (warp - kEpiWarp0) >> 2;          // column half
@@ -505,6 +505,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       f32x2 y[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) y[i] = 0ull;
+      auto release = [&]() {                      // the accumulator is free again
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(tempty_bar(acc));
+      };
       // the scales of a K block are loaded one block ahead of its sums
       float nx = 0.0f, nw = 0.0f, nw2 = 0.0f;
       if (active) {
@@ -524,26 +529,22 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
         if (active) {
           const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + acc * kBN;
           const f32x2 f = f2_splat(fx * fw), f2 = f2_splat(fx * fw2);
-          // one chunk's load under way while the one before is added
-          auto col = [&](int i) {
-            return kSitu ? (uint32_t)((i / 2) * 128 + h * 64 + (i % 2) * 32)
-                         : (uint32_t)(h * kCols + i * 32);
-          };
-          uint32_t v[2][32];
-          tmem_ld32(tb + col(0), v[0]);
+          // A load waits for the MMA that the tensor core is at, whatever its width: two of 64
+          // columns cost half of what four of 32 do.
 #pragma unroll
-          for (int i = 0; i < kCols / 32; ++i) {
-            tmem_wait_ld32(v[i & 1]);
-            if (i + 1 < kCols / 32) tmem_ld32(tb + col(i + 1), v[(i + 1) & 1]);
+          for (int i = 0; i < kCols / 64; ++i) {
+            uint32_t v[64];
+            tmem_ld64(tb + (kSitu ? (uint32_t)(i * 128 + h * 64) : (uint32_t)(h * kCols + i * 64)), v);
+            tmem_wait_ld64(v);
+            if (i == kCols / 64 - 1) release();   // ahead of the last sums
 #pragma unroll
-            for (int j = 0; j < 16; ++j)
-              y[i * 16 + j] = f2_fma(f2_make(v[i & 1][2 * j], v[i & 1][2 * j + 1]),
-                                     kSitu && i >= kCols / 64 ? f2 : f, y[i * 16 + j]);
+            for (int j = 0; j < 32; ++j)
+              y[i * 32 + j] = f2_fma(f2_make(v[2 * j], v[2 * j + 1]), kSitu && i == 1 ? f2 : f,
+                                     y[i * 32 + j]);
           }
+        } else {
+          release();
         }
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(tempty_bar(acc));
         if (++acc == kAcc) { acc = 0; aph ^= 1u; }
       }
       if (!ok) break;
@@ -748,10 +749,20 @@ DenseForm dense_form(long long T, int N, int nkb, int nsm) {
   return best;
 }
 
+// Whether the pair kernel (fp8_pair.cu) has enough tiles to fill the SMs.
+bool pair_form(long long T, int N) { return T > 256 && (T + 255) / 256 * ((N + 255) / 256) * 2 >= num_sms(); }
+
 }  // namespace
 
 cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
-  if (g.act_f32 || g.act_in || (!g.offsets && g.rows <= kStreamRows)) return launch_fp8_stream(g, s);
+  // 9 to 16 tokens cost a stream's unit as many bytes of tokens as of weights, from L2:
+  // [16, 4096] x [7168, 4096] 11.8 us as a stream, 12.8 here, [16, 7168] x [8192, 7168] 22.4
+  // and 17.5
+  const long long weights = (long long)g.feat * g.K;
+  if (g.act_f32 || g.act_in ||
+      (!g.offsets && (g.rows <= kStreamRows / 2 || (g.rows <= kStreamRows && weights <= 40ll << 20))))
+    return launch_fp8_stream(g, s);
+  if (!g.offsets && !g.act && pair_form(g.rows, g.feat)) return launch_fp8_pair(g, s);
   if (g.act) return launch_form<2, kFormSitu>(g, 1, s);
   DenseForm f{g.feat > 128, 1};
   if (!g.offsets) f = dense_form(g.rows, g.feat, fp8_blocks(g.K), num_sms());

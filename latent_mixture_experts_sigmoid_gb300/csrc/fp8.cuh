@@ -43,6 +43,8 @@ constexpr int kStreamRows = 16;
 cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s);
 // ... for few token rows (grouped: with act_f32 or act_in)
 cudaError_t launch_fp8_stream(const Fp8Gemm& g, cudaStream_t s);
+// ... dense, for many tiles of 256 x 256
+cudaError_t launch_fp8_pair(const Fp8Gemm& g, cudaStream_t s);
 
 // codes / scales of bf16 x [rows, K], one scale per block_rows (1 or 128) rows x 128 columns
 cudaError_t launch_quantize_fp8(const uint16_t* x, uint8_t* codes, float* scales, long long rows,

@@ -503,10 +503,23 @@ cudaError_t launch_stream(const Fp8Gemm& g, cudaStream_t s) {
 cudaError_t launch_fp8_stream(const Fp8Gemm& g, cudaStream_t s) {
   if (g.act_f32) return launch_stream<64, 1, kGateUp, 4, 1>(g, s);
   if (g.act_in) return launch_stream<64, 1, kSecond, 4, 1>(g, s);
-  // one group: a product of few rows has few units, and the whole ring should serve each
   if (g.K % kFp8Block)
     return g.rows <= 8 ? launch_stream<16, 1, kDense, 1, 1>(g, s) : launch_stream<16, 2, kDense, 1, 1>(g, s);
-  return g.rows <= 8 ? launch_stream<16, 1, kDense, 1, 4>(g, s) : launch_stream<16, 2, kDense, 1, 2>(g, s);
+  // as many groups as leave each a ring of about one unit: long rows need the whole
+  // ring for one unit, short ones would leave most warps without a stage
+  const int nkb = g.K / kFp8Block;
+  if (g.rows <= 8) {
+    if (nkb <= 16) return launch_stream<16, 1, kDense, 4, 4>(g, s);
+    if (nkb <= 32) return launch_stream<16, 1, kDense, 2, 4>(g, s);
+    // units of 32 rows read the tokens half as often; not where their coarser waves cost
+    // more ([8, 7168] x [8192, 7168]: 13.6 against 15.0 us; 7168 rows: 2 waves against 3 halves)
+    if (ceil_div(ceil_div(g.feat, 32), num_sms()) * 2 <= ceil_div(ceil_div(g.feat, 16), num_sms()))
+      return launch_stream<32, 1, kDense, 1, 2>(g, s);
+    return launch_stream<16, 1, kDense, 1, 4>(g, s);
+  }
+  if (nkb <= 8) return launch_stream<16, 2, kDense, 4, 2>(g, s);
+  if (nkb <= 16) return launch_stream<16, 2, kDense, 2, 2>(g, s);
+  return launch_stream<16, 2, kDense, 1, 2>(g, s);
 }
 
 }  // namespace lmoe

@@ -109,7 +109,7 @@ def test_quantize_extreme_values(block_rows):
     (9, 24, 7168), (15, 256, 144),
     (16, 264, 256), (17, 128, 512), (32, 1024, 2048), (33, 120, 640), (64, 1032, 128), (128, 256, 1024),
     (129, 392, 272), (255, 640, 400), (300, 512, 192), (513, 1000, 1168), (1024, 768, 512),
-    (2050, 2056, 336)])
+    (2050, 2056, 336), (1300, 4104, 1040), (2049, 2304, 2176)])
 def test_linear_matches_float64(T, N, K, with_add):
     from tests.gpu_util import dev_bf16, host_bits
     g = np.random.default_rng(T * 7 + N + K)
