@@ -508,7 +508,7 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       auto release = [&]() {                      // the accumulator is free again
         tc_fence_before();
         __syncwarp();
-        if (lane == 0) mbar_arrive(tempty_bar(acc));
+        if (lane == 0) mbar_arrive_relaxed(tempty_bar(acc));
       };
       // the scales of a K block are loaded one block ahead of its sums
       float nx = 0.0f, nw = 0.0f, nw2 = 0.0f;
