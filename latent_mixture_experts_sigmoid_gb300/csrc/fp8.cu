@@ -332,7 +332,7 @@ __device__ void build_groups(const Fp8Params& p, int* prefix, int* first, int* e
 // lane, meet no bank twice), and each then sums its share of the tile over the
 // cluster in rank order.
 constexpr int kPartPad = 4;
-constexpr int kMaxSplits = 8;
+constexpr int kMaxSplits = 4;
 
 __device__ __forceinline__ float4 ld_cluster4(uint32_t addr, uint32_t rank) {
   uint32_t a;
@@ -718,39 +718,42 @@ cudaError_t launch_form(const Fp8Gemm& g, int splits, cudaStream_t s) {
   return launch_k(kern, dim3(grid), dim3(kThreads), smem, s, mx, mxs, mw, p);
 }
 
-// Tile width and K split of a dense product: the pair with the least modelled
-// time, in SM cycles.  A wave of CTAs costs its K blocks (the wider tile does twice
-// the work in less than twice the time), a fixed part (launch, prologue, first
-// load, output) and, split, the exchange of the partial tiles.  Clusters of 4 and 8
-// leave some SMs of a GPC without one.
+// Form of a dense product: the one with the least modelled time, in SM cycles.
+//   pair          256 x 256 tiles on two SMs each (fp8_pair.cu)
+//   wide / splits 128 x 256 or 128 x 128 tiles, their K blocks split over clusters
+// A wave of tiles costs its K blocks (more with more token rows; the wide tile does twice
+// the work in 1.3 times the time) and its output, a launch a fixed part, a split the
+// cluster's start and the exchange of the partial tiles.  The constants were fitted to
+// sweeps of the forms over T 24 .. 4096 at [N, K] = [1024, 1024], [2048, 7168], [7168, 2048],
+// [7168, 4096] and [8192, 7168]: the chosen form is within 20 % of the best one at all of them, within 5 % at most
+// (T = 128, [2048, 7168]: split four ways 11.8 us, unsplit 26.1; T = 4096, [8192, 7168]: pair
+// 198 us, wide 215).  Clusters of eight were never clearly the best: about 13 fit at once.
 struct DenseForm {
-  bool wide;
+  bool pair, wide;
   int splits;
 };
 DenseForm dense_form(long long T, int N, int nkb, int nsm) {
-  constexpr double kBlock[2] = {650, 1000}, kFixed = 3000, kSplit = 2500, kExchange = 1.0 / 40;
-  DenseForm best{false, 1};
-  double least = -1;
+  constexpr double kLaunch = 5500, kSplit = 2700, kExchange = 1.0 / 20;
   const long long tok = (T + BM - 1) / BM;
   const double rows = T < BM ? (double)T : (double)BM;
+  const auto waves = [](long long n, int slots) { return (double)((n + slots - 1) / slots); };
+  DenseForm best{true, true, 1};
+  double least = waves((T + 255) / 256 * ((N + 255) / 256), nsm / 2) * (nkb * 950.0 + 2500) + kLaunch;
   for (int wide = 0; wide < 2; ++wide) {
     const int bn = wide ? 256 : 128;
+    const double block = (wide ? 830 : 650) + 1.1 * rows;
     const long long tiles = tok * ((N + bn - 1) / bn);
     for (int c = 1; c <= kMaxSplits && c <= nkb; c *= 2) {
-      const int slots = c <= 2 ? nsm : nsm / 19 * (c == 4 ? 18 : 16);
-      // unsplit tiles are walked by resident CTAs, whose fixed part is paid once
-      const double waves = (double)((tiles * c + slots - 1) / slots);
-      const double blocks = (double)((nkb + c - 1) / c) * kBlock[wide];
-      const double cost = c == 1 ? waves * (blocks + 500) + kFixed
-                                 : waves * (blocks + kFixed + kSplit + rows * bn * 4 * kExchange);
-      if (least < 0 || cost < least) { least = cost; best = DenseForm{wide != 0, c}; }
+      // clusters of four that fit at once: 32 of 152 / 4
+      const int slots = c == 1 ? nsm : c == 2 ? nsm / 2 : nsm * 32 / 152;
+      const double cost = c == 1 ? waves(tiles, slots) * (nkb * block + (wide ? 4000 : 2000)) + kLaunch
+                                 : waves(tiles, slots) * ((nkb + c - 1) / c * block + kLaunch + kSplit +
+                                                          rows * bn * 4 * kExchange);
+      if (cost < least) { least = cost; best = DenseForm{false, wide != 0, c}; }
     }
   }
   return best;
 }
-
-// Whether the pair kernel (fp8_pair.cu) has enough tiles to fill the SMs.
-bool pair_form(long long T, int N) { return T > 256 && (T + 255) / 256 * ((N + 255) / 256) * 2 >= num_sms(); }
 
 }  // namespace
 
@@ -762,10 +765,10 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   if (g.act_f32 || g.act_in ||
       (!g.offsets && (g.rows <= kStreamRows / 2 || (g.rows <= kStreamRows && weights <= 40ll << 20))))
     return launch_fp8_stream(g, s);
-  if (!g.offsets && !g.act && pair_form(g.rows, g.feat)) return launch_fp8_pair(g, s);
   if (g.act) return launch_form<2, kFormSitu>(g, 1, s);
-  DenseForm f{g.feat > 128, 1};
+  DenseForm f{false, g.feat > 128, 1};
   if (!g.offsets) f = dense_form(g.rows, g.feat, fp8_blocks(g.K), num_sms());
+  if (f.pair) return launch_fp8_pair(g, s);
   if (f.splits > 1)
     return f.wide ? launch_form<2, kFormSplit>(g, f.splits, s)
                   : launch_form<1, kFormSplit>(g, f.splits, s);
