@@ -199,14 +199,27 @@ def _dev(t, name: str, dtypes, numel: int) -> int | None:
     access it as the C ABI describes: a contiguous tensor on the current CUDA
     device, of one of `dtypes`, holding at least `numel` elements.  None and raw
     integer addresses pass through unchecked (the caller vouches for them)."""
-    if t is None or isinstance(t, int):
+    if t is None:
+        return None
+    try:
+        # one pass of cheap queries; whatever fails it is told apart below
+        if (t.get_device() == torch._C._cuda_getDevice() and t.is_contiguous()
+                and (t.dtype is dtypes or t.dtype in dtypes) and t.numel() >= numel):
+            return t.data_ptr()
+    except (AttributeError, TypeError, RuntimeError):
+        pass
+    return _dev_slow(t, name, dtypes, numel)
+
+
+def _dev_slow(t, name: str, dtypes, numel: int) -> int:
+    """_dev's checks one by one, for the error that names what is wrong."""
+    if isinstance(t, int):
         return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor, an address or None")
-    index = t.get_device() if t.is_cuda else -1
-    if index < 0:
+    if not t.is_cuda:
         raise ValueError(f"{name}: must be a CUDA tensor (got device {t.device})")
-    if index != torch._C._cuda_getDevice():
+    if t.get_device() != torch.cuda.current_device():
         raise ValueError(f"{name}: on {t.device}, but the current device is "
                          f"cuda:{torch.cuda.current_device()}")
     if not t.is_contiguous():

@@ -594,20 +594,27 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       } else if (active && row_ok) {
         const int col0 = x.feat_tile * kBN + h * kCols;
         const long long at = row * p.feat + col0;
+        if (p.add) {
+          // the addend's row, all of its loads ahead of their use
+          uint4 a[kCols / 8];
+#pragma unroll
+          for (int i = 0; i < kCols / 8; ++i)
+            a[i] = col0 + 8 * i < p.feat ? __ldg(reinterpret_cast<const uint4*>(p.add + at + 8 * i))
+                                         : make_uint4(0, 0, 0, 0);
+#pragma unroll
+          for (int i = 0; i < kCols / 8; ++i) {
+            const uint32_t w[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              y[4 * i + j] = f2_add(y[4 * i + j], f2_make(w[j] << 16, w[j] & 0xFFFF0000u));
+          }
+        }
 #pragma unroll
         for (int j = 0; j < kCols / 2; j += 4) {
           if (col0 + 2 * j < p.feat) {     // feat % 8 == 0
             uint32_t w[4];
-            if (p.add) {
-              const uint4 a = __ldg(reinterpret_cast<const uint4*>(p.add + at + 2 * j));
-              const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-              for (int i = 0; i < 4; ++i)
-                w[i] = pack_bf16x2(f2_lo(y[j + i]) + bf16_lo(aw[i]), f2_hi(y[j + i]) + bf16_hi(aw[i]));
-            } else {
-#pragma unroll
-              for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(f2_lo(y[j + i]), f2_hi(y[j + i]));
-            }
+            for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(f2_lo(y[j + i]), f2_hi(y[j + i]));
             *reinterpret_cast<uint4*>(p.out + at + 2 * j) = make_uint4(w[0], w[1], w[2], w[3]);
           }
         }

@@ -123,6 +123,8 @@ __device__ __forceinline__ int2 tile_of(const PairParams& p, int u) {
   return make_int2(t, band * kBand + rem - t * width);
 }
 
+// kAdd: with an addend (a form of its own: its code, even unused, cost the other 14 %)
+template <bool kAdd>
 __global__ void __launch_bounds__(kThreads, 1)
 fp8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
                 const PairParams p) {
@@ -279,6 +281,12 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       const int row0 = x.x * kTile + (int)rank * kHalf;
       const int blk = min(x.y * 2 + h, p.ws_rows - 1);
       const float* wsp = p.ws + (long long)blk * p.nkb;
+      if constexpr (kAdd) {      // the addend's row on its way into L2 while the sums run
+        const int n = row0 + r < p.T ? min(kHalf, p.feat - x.y * kTile - h * kHalf) : 0;
+        for (int j = 0; j < n; j += 64)
+          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.add + (long long)(row0 + r) * p.feat +
+                                                          x.y * kTile + h * kHalf + j));
+      }
       f32x2 y[kHalf / 2];
 #pragma unroll
       for (int i = 0; i < kHalf / 2; ++i) y[i] = 0ull;
@@ -318,24 +326,28 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       const int row = row0 + r, col0 = x.y * kTile + h * kHalf;
       const int ncol = row < p.T ? min(kHalf, p.feat - col0) : 0;    // a multiple of 8
       const long long at = (long long)row * p.feat + col0;
+      if constexpr (kAdd) {
+        // the addend's row, all of its loads ahead of their use (one after the other they
+        // were eight latencies a tile: 5 us of 19 at T = 300)
+        uint4 a[kHalf / 8];
+#pragma unroll
+        for (int i = 0; i < kHalf / 8; ++i)
+          a[i] = 8 * i < ncol ? __ldg(reinterpret_cast<const uint4*>(p.add + at + 8 * i))
+                              : make_uint4(0, 0, 0, 0);
+#pragma unroll
+        for (int i = 0; i < kHalf / 8; ++i) {
+          const uint32_t w[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            y[4 * i + j] = f2_add(y[4 * i + j], f2_make(w[j] << 16, w[j] & 0xFFFF0000u));
+        }
+      }
 #pragma unroll
       for (int j = 0; j < kHalf / 2; j += 8) {   // 16 columns: 32 bytes
         if (2 * j >= ncol) break;
         uint32_t w[8];
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-          if (2 * j + 8 * half < ncol) {
-            uint4 a = make_uint4(0, 0, 0, 0);
-            if (p.add) a = __ldg(reinterpret_cast<const uint4*>(p.add + at + 2 * j + 8 * half));
-            const uint32_t aw[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const f32x2 v = y[j + 4 * half + i];
-              w[4 * half + i] = p.add ? pack_bf16x2(f2_lo(v) + bf16_lo(aw[i]), f2_hi(v) + bf16_hi(aw[i]))
-                                      : pack_bf16x2(f2_lo(v), f2_hi(v));
-            }
-          }
-        }
+        for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(f2_lo(y[j + i]), f2_hi(y[j + i]));
         if (p.wide_store) {
           asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p.out + at + 2 * j),
                        "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -386,6 +398,7 @@ constexpr size_t kSmem = 1024 + kStages * kStageBytes +
                          (2 * kStages + 2 * kAcc + 1 + 2 * kScaleBuffers) * 8 + 8;
 
 // Pairs that fit on the current device at once (pairs share a GPC), 0 on failure.
+template <bool kAdd>
 int pairs_resident() {
   static int cache[64] = {};
   static std::mutex mu;
@@ -393,8 +406,8 @@ int pairs_resident() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   std::lock_guard<std::mutex> lock(mu);
   if (cache[dev]) return cache[dev];
-  if (cudaFuncSetAttribute(fp8_pair_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) !=
-      cudaSuccess)
+  auto* kern = fp8_pair_kernel<kAdd>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kSmem) != cudaSuccess)
     return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * num_sms());
@@ -408,8 +421,17 @@ int pairs_resident() {
   cfg.attrs = attr;
   cfg.numAttrs = 1;
   int n = 0;
-  if (cudaOccupancyMaxActiveClusters(&n, fp8_pair_kernel, &cfg) != cudaSuccess) return 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
   return cache[dev] = n;
+}
+
+template <bool kAdd>
+cudaError_t launch_pair(const CUtensorMap& mx, const CUtensorMap& mw, const PairParams& p, cudaStream_t s) {
+  const int pairs = pairs_resident<kAdd>();
+  if (pairs < 1) return cudaErrorInvalidConfiguration;
+  const long long units = (long long)p.ntok * p.nfeat;
+  return launch_k_cluster(fp8_pair_kernel<kAdd>, dim3(2 * (unsigned)(units < pairs ? units : pairs)),
+                          dim3(kThreads), kSmem, s, 2, mx, mw, p);
 }
 
 }  // namespace
@@ -431,11 +453,7 @@ cudaError_t launch_fp8_pair(const Fp8Gemm& g, cudaStream_t s) {
   CUtensorMap mx, mw;
   if (!p.err || !make_map(&mx, g.X, g.rows, g.K) || !make_map(&mw, g.W, g.feat, g.K))
     return cudaErrorInvalidValue;
-  const int pairs = pairs_resident();
-  if (pairs < 1) return cudaErrorInvalidConfiguration;
-  const long long units = (long long)p.ntok * p.nfeat;
-  return launch_k_cluster(fp8_pair_kernel, dim3(2 * (unsigned)(units < pairs ? units : pairs)),
-                          dim3(kThreads), kSmem, s, 2, mx, mw, p);
+  return g.add ? launch_pair<true>(mx, mw, p, s) : launch_pair<false>(mx, mw, p, s);
 }
 
 }  // namespace lmoe
