@@ -204,6 +204,7 @@ enum : int { kErrProducer = 1, kErrMmaFull = 2, kErrMmaTmem = 3, kErrEpilogue = 
 
 struct Fp8Params {
   int feat, nkb, groups, nfeat, stages, ws_rows;
+  int wide_store;    // rows of out start on 32 bytes
   int splits;        // > 1: clusters of this many CTAs share a tile's K blocks (one tile a cluster)
   long long rows;
   const int32_t* offsets;
@@ -568,15 +569,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
             const int d = p.feat / 2;
             uint8_t* o = p.act + row * d + x.feat_tile * 128 + h * 64;
 #pragma unroll
-            for (int j = 0; j < 32; j += 8) {
-              uint32_t w[4];
+            for (int j = 0; j < 32; j += 16) {     // 32 codes
+              uint32_t w[8];
 #pragma unroll
-              for (int i = 0; i < 4; ++i) {
+              for (int i = 0; i < 8; ++i) {
                 const f32x2 a = y[j + 2 * i], b = y[j + 2 * i + 1];
                 w[i] = pack_e4m3x4(__fmul_rn(f2_lo(a), bs.inv), __fmul_rn(f2_hi(a), bs.inv),
                                    __fmul_rn(f2_lo(b), bs.inv), __fmul_rn(f2_hi(b), bs.inv));
               }
-              *reinterpret_cast<uint4*>(o + 2 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+              st_global32(o + 2 * j, w);
             }
             if (h == 0) p.act_s[row * (d / 128) + x.feat_tile] = bs.scale;
           }
@@ -610,12 +611,17 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
           }
         }
 #pragma unroll
-        for (int j = 0; j < kCols / 2; j += 4) {
-          if (col0 + 2 * j < p.feat) {     // feat % 8 == 0
-            uint32_t w[4];
+        for (int j = 0; j < kCols / 2; j += 8) {   // 16 columns
+          if (col0 + 2 * j >= p.feat) break;       // feat % 8 == 0
+          uint32_t w[8];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) w[i] = pack_bf16x2(f2_lo(y[j + i]), f2_hi(y[j + i]));
+          for (int i = 0; i < 8; ++i) w[i] = pack_bf16x2(f2_lo(y[j + i]), f2_hi(y[j + i]));
+          if (p.wide_store) {
+            st_global32(p.out + at + 2 * j, w);
+          } else {
             *reinterpret_cast<uint4*>(p.out + at + 2 * j) = make_uint4(w[0], w[1], w[2], w[3]);
+            if (col0 + 2 * j + 8 < p.feat)
+              *reinterpret_cast<uint4*>(p.out + at + 2 * j + 8) = make_uint4(w[4], w[5], w[6], w[7]);
           }
         }
       }
@@ -703,6 +709,7 @@ cudaError_t launch_form(const Fp8Gemm& g, int splits, cudaStream_t s) {
   p.act = g.act;
   p.act_s = g.act_s;
   p.splits = splits;
+  p.wide_store = g.feat % 16 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 31u) == 0;
   p.err = device_error_word();
   p.sp = make_situ_params(g.beta > 0.0f ? g.beta : 1.0f, g.linear_beta);
   if (!p.err) return cudaErrorInvalidValue;

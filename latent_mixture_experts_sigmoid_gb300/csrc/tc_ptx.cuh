@@ -53,6 +53,14 @@ __device__ __forceinline__ bool mbar_try_wait_ns(uint32_t bar, uint32_t parity, 
   return ok != 0;
 }
 
+// 32 bytes (32-byte aligned) as one store: a whole sector.  Where a warp's lanes write a row
+// each, a store costs its 32 lines whatever its width.
+__device__ __forceinline__ void st_global32(void* p, const uint32_t (&w)[8]) {
+  asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
+               "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+               : "memory");
+}
+
 __device__ __forceinline__ void tma_load_2d(const CUtensorMap* map, uint32_t dst, uint32_t bar,
                                             int c0, int c1) {
   asm volatile(
