@@ -325,8 +325,7 @@ def _workspace(workspace, workspace_bytes):
     n = have if workspace_bytes is None else int(workspace_bytes)
     if n > have:
         raise ValueError(f"workspace: {have} bytes, {n} claimed")
-    _dev(workspace, "workspace", (workspace.dtype,), 0)
-    return workspace.data_ptr(), n
+    return _dev(workspace, "workspace", workspace.dtype, 0), n
 
 
 def latent_moe_workspace_bytes(dims) -> int:
@@ -632,7 +631,7 @@ def lmoe_experts_fp8(experts, x, xs, expert_offsets, y, workspace, inter: int, b
         rows, latent = x.shape
     if E is None:
         E = expert_offsets.numel() - 1
-    rows, L, E, d = int(rows), int(latent), int(E), int(inter)
+    L, d = latent, inter
     qq = experts if isinstance(experts, LmoeFp8Experts) else make_fp8_experts(
         experts, E=E, latent=L, inter=d)
     wsp, wsn = _workspace(workspace, None)
@@ -684,9 +683,9 @@ def _router_batch(router_logits, topk_ids, token_mask, seq_offsets, shape):
     if shape is not None:
         T, E, k, S = (int(v) for v in shape)
     else:
-        T, E = (int(v) for v in router_logits.shape)
-        k = int(topk_ids.shape[-1])
-        S = 1 if seq_offsets is None else int(seq_offsets.numel()) - 1
+        T, E = router_logits.shape
+        k = topk_ids.shape[-1]
+        S = 1 if seq_offsets is None else seq_offsets.numel() - 1
     ptrs = (_dev(router_logits, "router_logits", torch.float32, T * E),
             _dev(topk_ids, "topk_ids", torch.int32, T * k),
             _dev(token_mask, "token_mask", (torch.uint8, torch.bool), T),

@@ -248,15 +248,17 @@ struct SequenceWalk {
     keep = b.mask ? __ballot_sync(kFull, t + lane < b.T && __ldg(b.mask + t + lane) != 0) : kFull;
   }
 
-  // Moves to token t; whether it counts.
+  // Moves to token t; whether it counts.  (kShared: counts and tokens are in shared memory.)
+  template <bool kShared = false>
   __device__ __forceinline__ bool at(const RouterBatch& b, const int32_t* counts,
                                      const int32_t* tokens, int t, int lane) {
     if (t >= end && s + 1 < b.S) find(b, t);
     if (t >= base + 32) masks(b, t, lane);
     if (t < begin || t >= end || !(keep >> (t - base) & 1u)) return false;
-    if (fresh) load(b, counts, tokens, lane);
+    if (fresh) load<kShared>(b, counts, tokens, lane);
     return true;
   }
+  template <bool kShared>
   __device__ __forceinline__ void load(const RouterBatch& b, const int32_t* counts,
                                        const int32_t* tokens, int lane) {
     fresh = false;
@@ -266,19 +268,20 @@ struct SequenceWalk {
       int4 n = make_int4(0, 0, 0, 0);
       if (kVec) {
         if (expert_of<kNI, kVec>(i, 0, lane) < b.E)
-          n = __ldcg(reinterpret_cast<const int4*>(row + expert_of<kNI, kVec>(i, 0, lane)));
+          n = kShared ? *reinterpret_cast<const int4*>(row + expert_of<kNI, kVec>(i, 0, lane))
+                      : __ldcg(reinterpret_cast<const int4*>(row + expert_of<kNI, kVec>(i, 0, lane)));
       } else {
         int x[4];
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int e = expert_of<kNI, kVec>(i, j, lane);
-          x[j] = e < b.E ? __ldcg(row + e) : 0;
+          x[j] = e >= b.E ? 0 : kShared ? row[e] : __ldcg(row + e);
         }
         n = make_int4(x[0], x[1], x[2], x[3]);
       }
       c[i][0] = (float)n.x; c[i][1] = (float)n.y; c[i][2] = (float)n.z; c[i][3] = (float)n.w;
     }
-    const int n = __ldcg(tokens + s);
+    const int n = kShared ? tokens[s] : __ldcg(tokens + s);
     unit = n > 0 ? (float)b.E / ((float)b.k * (float)n) : 0.0f;
     part = n > 0 ? 1.0f / ((float)b.S * (float)n) : 0.0f;
   }
@@ -389,6 +392,102 @@ loss_kernel(const RouterBatch b, float alpha, const int32_t* __restrict__ counts
     for (int i = 0; i < kWarps; ++i) v += sums[i];
     *loss = alpha * v;
   }
+}
+
+// The whole of a small batch's loss in one cluster: counts per CTA, summed over the cluster
+// through its shared memory, then the tokens' terms, then their sum.  Three launches one
+// after the other cost such a batch more than its work.
+constexpr int kSmallCtas = 8;
+constexpr int kSmallTokens = 4 * kSmallCtas * kWarps;    // at most four tokens a warp
+constexpr int kSmallCounts = 4096;                       // S * (E + 1) at most
+
+__device__ __forceinline__ int ld_cluster(const int* p, uint32_t rank) {
+  uint32_t a;
+  int v;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(a) : "memory");
+  return v;
+}
+
+template <int kNI, bool kVec>
+__global__ void __launch_bounds__(kWarps * 32, 2)
+small_loss_kernel(const RouterBatch b, float alpha, int32_t* __restrict__ counts,
+                  int32_t* __restrict__ tokens, int per_warp, float* __restrict__ loss) {
+  extern __shared__ __align__(16) float ring_smem[];
+  __shared__ __align__(16) int hist[kSmallCounts];       // this CTA's counts [S, E], tokens [S]
+  __shared__ __align__(16) int total[kSmallCounts];      // the cluster's
+  __shared__ float sums[kWarps];
+  __shared__ float part;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  const int rank = (int)cluster_rank(), n = b.S * b.E;
+  pdl_trigger();
+  for (int i = threadIdx.x; i < n + b.S; i += kWarps * 32) hist[i] = 0;
+  pdl_wait();
+  const int w = rank * kWarps + warp;
+  const int t0 = min(w * per_warp, b.T), t1 = min(t0 + per_warp, b.T);
+  RowRing<kNI, kVec> ring(ring_smem, warp, lane);
+  for (int i = 0; i < kSlots; ++i) {
+    if (t0 + i < t1) ring.fetch(i, b.logits + (long long)(t0 + i) * b.E, b.E, lane);
+    ring.commit();
+  }
+  SequenceWalk<kNI, kVec> q;
+  if (t0 < t1) q.start(b, t0, lane);
+  __syncthreads();
+  // this warp's tokens, 32 choices at a time
+  for (int i = t0 * b.k + lane; i < t1 * b.k; i += 32) {
+    const int t = i / b.k, id = __ldg(b.ids + i);
+    const int s = sequence_of(b, t);
+    const int2 r = sequence_range(b, s);
+    const bool counts_in = t >= r.x && t < r.y && (!b.mask || __ldg(b.mask + t) != 0);
+    if (counts_in && (unsigned)id < (unsigned)b.E) atomicAdd(&hist[s * b.E + id], 1);
+    if (counts_in && i == t * b.k) atomicAdd(&hist[n + s], 1);
+  }
+  cluster_sync();
+  for (int i = threadIdx.x; i < n + b.S; i += kWarps * 32) {
+    int v[kSmallCtas], c = 0;
+#pragma unroll
+    for (int k = 0; k < kSmallCtas; ++k) v[k] = ld_cluster(&hist[i], (uint32_t)k);
+#pragma unroll
+    for (int k = 0; k < kSmallCtas; ++k) c += v[k];
+    total[i] = c;
+    if (rank == 0) {
+      if (i < n) counts[i] = c;
+      else tokens[i - n] = c;
+    }
+  }
+  __syncthreads();
+  float sum = 0.0f;
+  int slot = 0;
+  for (int t = t0; t < t1; ++t) {
+    float v[kNI][4];
+    ring.wait_oldest();
+    if (q.template at<true>(b, total, total + n, t, lane)) {
+      ring.read(v, slot, b.E, lane);
+      bool tiny;
+      const float2 zd = row_sums<kNI, kVec>(v, q.c, &tiny);
+      if (zd.x > 0.0f) sum += q.part * (q.unit * zd.y / zd.x);
+      else if (!(zd.x == 0.0f)) sum += zd.x;
+    }
+    if (t + kSlots < t1) ring.fetch(slot, b.logits + (long long)(t + kSlots) * b.E, b.E, lane);
+    ring.commit();
+    slot = slot + 1 == kSlots ? 0 : slot + 1;
+  }
+  if (lane == 0) sums[warp] = sum;
+  __syncthreads();
+  if (threadIdx.x == 0) {
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kWarps; ++i) v += sums[i];
+    part = v;
+  }
+  cluster_sync();
+  if (rank == 0 && threadIdx.x == 0) {
+    float v = 0.0f;
+    for (int k = 0; k < kSmallCtas; ++k)
+      v += __int_as_float(ld_cluster(reinterpret_cast<const int*>(&part), (uint32_t)k));
+    *loss = alpha * v;
+  }
+  cluster_sync();   // no CTA leaves while another still reads its shared memory
 }
 
 struct BackwardArgs {
@@ -538,11 +637,15 @@ TokenGrid token_grid(int T) {
 
 // A token kernel with its warps' rings of kNI * 128 floats a slot.
 template <typename... KArgs, typename... Args>
-cudaError_t launch_ring(void (*kernel)(KArgs...), int ctas, int ni, cudaStream_t s, Args&&... args) {
+cudaError_t launch_ring(void (*kernel)(KArgs...), int ctas, int ni, int cluster, cudaStream_t s,
+                        Args&&... args) {
   const size_t smem = (size_t)kWarps * kSlots * ni * 128 * sizeof(float);
   const cudaError_t e =
       cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
+  if (cluster > 1)
+    return launch_k_cluster(kernel, dim3(ctas), dim3(kWarps * 32), smem, s, cluster,
+                            std::forward<Args>(args)...);
   return launch_k(kernel, dim3(ctas), dim3(kWarps * 32), smem, s, std::forward<Args>(args)...);
 }
 
@@ -575,8 +678,22 @@ size_t balance_workspace_bytes(int T) {
   return (n + 255) & ~size_t(255);
 }
 
+namespace {
+cudaError_t launch_small_loss(const RouterBatch& b, float alpha, float* loss, int32_t* counts,
+                              int32_t* tokens, cudaStream_t s) {
+  const int per_warp = ceil_div(b.T, kSmallCtas * kWarps);
+#define LMOE_CALL(NI, VEC)                                                                      \
+  launch_ring(small_loss_kernel<NI, VEC>, kSmallCtas, NI, kSmallCtas, s, b, alpha, counts, tokens, \
+              per_warp, loss)
+  LMOE_BY_EXPERTS(b.E, LMOE_CALL);
+#undef LMOE_CALL
+}
+}  // namespace
+
 cudaError_t launch_balance_loss(const RouterBatch& b, float alpha, float* loss, int32_t* counts,
                                 int32_t* tokens, void* workspace, cudaStream_t s) {
+  if (b.T <= kSmallTokens && (long long)b.S * (b.E + 1) <= kSmallCounts)
+    return launch_small_loss(b, alpha, loss, counts, tokens, s);
   unsigned* ticket = static_cast<unsigned*>(workspace);
   float* partial = reinterpret_cast<float*>(static_cast<char*>(workspace) + 256);
   const long long n = (long long)b.S * b.E;
@@ -592,7 +709,7 @@ cudaError_t launch_balance_loss(const RouterBatch& b, float alpha, float* loss, 
   if (e != cudaSuccess) return e;
   const TokenGrid g = token_grid(b.T);
 #define LMOE_CALL(NI, VEC)                                                                       \
-  launch_ring(loss_kernel<NI, VEC>, g.ctas, NI, s, b, alpha, (const int32_t*)counts,              \
+  launch_ring(loss_kernel<NI, VEC>, g.ctas, NI, 1, s, b, alpha, (const int32_t*)counts,              \
               (const int32_t*)tokens, g.per_warp, partial, ticket, loss)
   LMOE_BY_EXPERTS(b.E, LMOE_CALL);
 #undef LMOE_CALL
@@ -605,7 +722,7 @@ cudaError_t launch_router_backward(const RouterBatch& b, const float* grad_w, in
   const TokenGrid g = token_grid(b.T);
   const BackwardArgs a{grad_w, grad_loss, counts, tokens, alpha, rsf, renorm, g.per_warp, grad};
 #define LMOE_CALL(NI, VEC) \
-  launch_ring(backward_kernel<NI, VEC>, g.ctas, NI, s, b, a)
+  launch_ring(backward_kernel<NI, VEC>, g.ctas, NI, 1, s, b, a)
   LMOE_BY_EXPERTS(b.E, LMOE_CALL);
 #undef LMOE_CALL
 }
