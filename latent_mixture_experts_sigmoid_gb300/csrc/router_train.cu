@@ -97,6 +97,11 @@ count_kernel(const RouterBatch b, int per_cta, int32_t* __restrict__ counts,
   bool waited = false;
   const int first = (int)min((long long)blockIdx.x * per_cta, (long long)b.T);
   const int last = min(first + per_cta, b.T);
+  // the slice's choices and masks on their way while the sequence is looked up
+  for (long long i = (long long)first * b.k + threadIdx.x * 32; i < (long long)last * b.k; i += kCountThreads * 32)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(b.ids + i));
+  if (b.mask && first + threadIdx.x * 128 < last)
+    asm volatile("prefetch.global.L2 [%0];" ::"l"(b.mask + first + threadIdx.x * 128));
   for (int t0 = first; t0 < last;) {
     const int s = sequence_of(b, t0);
     const int2 r = sequence_range(b, s);
@@ -156,9 +161,9 @@ __device__ __forceinline__ int expert_of(int i, int j, int lane) {
 // Every lane copies and reads its own experts only, so that its own copies'
 // completion is all there is to wait for.  kSlots rows are on their way per warp:
 // 16 warps an SM and a latency of about 1.5 us need two rows each at full
-// bandwidth; with one (a row ahead in registers) the loss kernel took 17.8 us
-// for 16384 x 896, with this ring 11.
-constexpr int kSlots = 3;
+// bandwidth (16384 x 896: two slots 24.2 us for the gradient, three 24.9, four 25.7; with a
+// row ahead in registers instead 37).
+constexpr int kSlots = 2;
 
 template <int kNI, bool kVec>
 struct RowRing {
@@ -207,14 +212,19 @@ struct RowRing {
     const int at = kVec ? e : (e & ~127) + (e & 31) * 4 + ((e >> 5) & 3);
     return slots - lane * 4 + slot * kNI * 128 + at;
   }
-  __device__ __forceinline__ void read(float (&v)[kNI][4], int slot, int E, int lane) const {
+  // the row as pairs; places past the last expert (in the last 128 only) read as -infinity
+  __device__ __forceinline__ void read(f32x2 (&v)[kNI][2], int slot, int E, int lane) const {
 #pragma unroll
     for (int i = 0; i < kNI; ++i) {
-      const float4 a = own(slot, i);
-      const float x[4] = {a.x, a.y, a.z, a.w};
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        v[i][j] = expert_of<kNI, kVec>(i, j, lane) < E ? x[j] : -INFINITY;
+      float4 a = own(slot, i);
+      if (i == kNI - 1) {
+        if (expert_of<kNI, kVec>(i, 0, lane) >= E) a.x = -INFINITY;
+        if (expert_of<kNI, kVec>(i, 1, lane) >= E) a.y = -INFINITY;
+        if (expert_of<kNI, kVec>(i, 2, lane) >= E) a.z = -INFINITY;
+        if (expert_of<kNI, kVec>(i, 3, lane) >= E) a.w = -INFINITY;
+      }
+      v[i][0] = f2_make(__float_as_uint(a.x), __float_as_uint(a.y));
+      v[i][1] = f2_make(__float_as_uint(a.z), __float_as_uint(a.w));
     }
   }
 };
@@ -229,7 +239,7 @@ struct SequenceWalk {
   unsigned keep = 0;
   bool fresh = true;       // the counts of sequence s are not loaded yet
   float unit = 0.0f, part = 0.0f;
-  float c[kNI][4];
+  f32x2 c[kNI][2];
 
   // The place of the warp's first token; reads the call's inputs only.
   __device__ __forceinline__ void start(const RouterBatch& b, int t, int lane) {
@@ -279,7 +289,8 @@ struct SequenceWalk {
         }
         n = make_int4(x[0], x[1], x[2], x[3]);
       }
-      c[i][0] = (float)n.x; c[i][1] = (float)n.y; c[i][2] = (float)n.z; c[i][3] = (float)n.w;
+      c[i][0] = f2_make(__float_as_uint((float)n.x), __float_as_uint((float)n.y));
+      c[i][1] = f2_make(__float_as_uint((float)n.z), __float_as_uint((float)n.w));
     }
     const int n = kShared ? tokens[s] : __ldcg(tokens + s);
     unit = n > 0 ? (float)b.E / ((float)b.k * (float)n) : 0.0f;
@@ -287,45 +298,52 @@ struct SequenceWalk {
   }
 };
 
-// A row of logits -> sigmoids in place; returns {Z, sum_e c s}.  Where Z would
-// underflow the row becomes exp(l - max l) instead (see kTinySum), `tiny` set.
+// The row of a slot -> its sigmoids; returns {Z, sum_e c s}.  Where Z would underflow the
+// row becomes exp(l - max l) instead (see kTinySum), `tiny` set.  Pairs of experts go
+// through the packed fp32 operations: 4 instructions an expert.
 template <int kNI, bool kVec>
-__device__ __forceinline__ float2 row_sums(float (&v)[kNI][4], const float (&c)[kNI][4], bool* tiny) {
-  float s[kNI][4];
-  float z = 0.0f, dot = 0.0f;
+__device__ __forceinline__ float2 row_sums(f32x2 (&s)[kNI][2], const f32x2 (&c)[kNI][2],
+                                           const RowRing<kNI, kVec>& ring, int slot, int E, int lane,
+                                           bool* tiny) {
+  ring.read(s, slot, E, lane);
+  f32x2 z2 = 0ull, dot2 = 0ull;
 #pragma unroll
   for (int i = 0; i < kNI; ++i)
 #pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      s[i][j] = sigmoid_f(v[i][j]);
-      z += s[i][j];
-      dot = fmaf(c[i][j], s[i][j], dot);
+    for (int j = 0; j < 2; ++j) {
+      const f32x2 e = LMOE_F2_APPLY(ex2_fast, f2_mul(s[i][j], f2_splat(-kLog2e)));
+      s[i][j] = LMOE_F2_APPLY(rcp_fast, f2_add(e, f2_splat(1.0f)));
+      z2 = f2_add(z2, s[i][j]);
+      dot2 = f2_fma(c[i][j], s[i][j], dot2);
     }
-  z = warp_sum(z);
+  float z = f2_lo(z2) + f2_hi(z2), dot = f2_lo(dot2) + f2_hi(dot2);
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    z += __shfl_xor_sync(kFull, z, o);
+    dot += __shfl_xor_sync(kFull, dot, o);
+  }
   *tiny = z < kTinySum;
   if (*tiny) {
+    ring.read(s, slot, E, lane);
     float m = -INFINITY;
 #pragma unroll
     for (int i = 0; i < kNI; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) m = fmaxf(m, v[i][j]);
+      for (int j = 0; j < 2; ++j) m = fmaxf(m, fmaxf(f2_lo(s[i][j]), f2_hi(s[i][j])));
     m = warp_max(m);
-    z = dot = 0.0f;
+    z2 = dot2 = 0ull;
 #pragma unroll
     for (int i = 0; i < kNI; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        s[i][j] = m == -INFINITY ? 0.0f : ex2_fast(kLog2e * (v[i][j] - m));
-        z += s[i][j];
-        dot = fmaf(c[i][j], s[i][j], dot);
+      for (int j = 0; j < 2; ++j) {
+        const f32x2 d = f2_add(s[i][j], f2_splat(-m));
+        s[i][j] = m == -INFINITY ? 0ull : LMOE_F2_APPLY(ex2_fast, f2_mul(d, f2_splat(kLog2e)));
+        z2 = f2_add(z2, s[i][j]);
+        dot2 = f2_fma(c[i][j], s[i][j], dot2);
       }
-    z = warp_sum(z);
+    z = warp_sum(f2_lo(z2) + f2_hi(z2));
+    dot = warp_sum(f2_lo(dot2) + f2_hi(dot2));
   }
-  dot = warp_sum(dot);
-#pragma unroll
-  for (int i = 0; i < kNI; ++i)
-#pragma unroll
-    for (int j = 0; j < 4; ++j) v[i][j] = s[i][j];
   return make_float2(z, dot);
 }
 
@@ -353,12 +371,11 @@ loss_kernel(const RouterBatch b, float alpha, const int32_t* __restrict__ counts
   float total = 0.0f;
   int slot = 0;
   for (int t = t0; t < t1; ++t) {
-    float v[kNI][4];
+    f32x2 v[kNI][2];
     ring.wait_oldest();
     if (q.at(b, counts, tokens, t, lane)) {
-      ring.read(v, slot, b.E, lane);
       bool tiny;
-      const float2 zd = row_sums<kNI, kVec>(v, q.c, &tiny);
+      const float2 zd = row_sums<kNI, kVec>(v, q.c, ring, slot, b.E, lane, &tiny);
       if (zd.x > 0.0f) total += q.part * (q.unit * zd.y / zd.x);
       else if (!(zd.x == 0.0f)) total += zd.x;      // NaN logits stay NaN
     }
@@ -459,12 +476,11 @@ small_loss_kernel(const RouterBatch b, float alpha, int32_t* __restrict__ counts
   float sum = 0.0f;
   int slot = 0;
   for (int t = t0; t < t1; ++t) {
-    float v[kNI][4];
+    f32x2 v[kNI][2];
     ring.wait_oldest();
     if (q.template at<true>(b, total, total + n, t, lane)) {
-      ring.read(v, slot, b.E, lane);
       bool tiny;
-      const float2 zd = row_sums<kNI, kVec>(v, q.c, &tiny);
+      const float2 zd = row_sums<kNI, kVec>(v, q.c, ring, slot, b.E, lane, &tiny);
       if (zd.x > 0.0f) sum += q.part * (q.unit * zd.y / zd.x);
       else if (!(zd.x == 0.0f)) sum += zd.x;
     }
@@ -541,7 +557,7 @@ backward_kernel(const RouterBatch b, const BackwardArgs a) {
   int slot = 0;
   for (int t = t0; t < t1; ++t) {
     const long long row = (long long)t * b.E;
-    float v[kNI][4];
+    f32x2 v[kNI][2];
     int id = id1;
     float g = g1, l = l1;
     id1 = id2;
@@ -560,8 +576,7 @@ backward_kernel(const RouterBatch b, const BackwardArgs a) {
       __syncwarp();                            // the whole row has landed
       if (id >= 0) l = *ring.place(slot, id, lane);
       if (q.at(b, a.counts, a.tokens, t, lane)) {
-        ring.read(v, slot, b.E, lane);
-        const float2 zd = row_sums<kNI, kVec>(v, q.c, &tiny);
+        const float2 zd = row_sums<kNI, kVec>(v, q.c, ring, slot, b.E, lane, &tiny);
         if (!(zd.x == 0.0f)) {
           coef = gl * q.part * q.unit / zd.x;
           mean = zd.y / zd.x;
@@ -589,28 +604,34 @@ backward_kernel(const RouterBatch b, const BackwardArgs a) {
       if (id >= 0) *ring.place(slot, id, lane) = d * (1.0f - s);
       __syncwarp();
     }
+    // coef (c - mean) s (1 - s), with 1 - s = 1 where the row holds exponentials
+    const f32x2 scale = f2_splat(coef), shift = f2_splat(-coef * mean);
+    const f32x2 minus = f2_splat(tiny ? 0.0f : -1.0f);
 #pragma unroll
     for (int i = 0; i < kNI; ++i) {
-      float o[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+      f32x2 o[2] = {0ull, 0ull};
       if (a.grad_w) {
         const float4 x = ring.own(slot, i);
-        o[0] = x.x; o[1] = x.y; o[2] = x.z; o[3] = x.w;
+        o[0] = f2_make(__float_as_uint(x.x), __float_as_uint(x.y));
+        o[1] = f2_make(__float_as_uint(x.z), __float_as_uint(x.w));
       }
       if (coef != 0.0f) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float s = v[i][j];
-          o[j] += coef * (q.c[i][j] - mean) * (tiny ? s : s * (1.0f - s));
+        for (int j = 0; j < 2; ++j) {
+          const f32x2 s = v[i][j];
+          o[j] = f2_fma(f2_fma(q.c[i][j], scale, shift), f2_fma(f2_mul(s, minus), s, s), o[j]);
         }
       }
+      const float4 r = make_float4(f2_lo(o[0]), f2_hi(o[0]), f2_lo(o[1]), f2_hi(o[1]));
       if (kVec) {
         const int e = expert_of<kNI, kVec>(i, 0, lane);
-        if (e < b.E) *reinterpret_cast<float4*>(a.grad + row + e) = make_float4(o[0], o[1], o[2], o[3]);
+        if (i < kNI - 1 || e < b.E) *reinterpret_cast<float4*>(a.grad + row + e) = r;
       } else {
+        const float x[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           const int e = expert_of<kNI, kVec>(i, j, lane);
-          if (e < b.E) a.grad[row + e] = o[j];
+          if (i < kNI - 1 || e < b.E) a.grad[row + e] = x[j];
         }
       }
     }
