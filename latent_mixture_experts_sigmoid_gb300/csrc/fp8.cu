@@ -58,7 +58,7 @@ __device__ __forceinline__ uint2 quant8(const uint4& v, float inv) {
 }
 
 constexpr int kQuantThreads = 256;
-constexpr int kQuantUnroll = 2;
+constexpr int kQuantUnroll = 1;
 
 // One scale per row and 128 columns: eight lanes a block, 16 elements a lane
 // (a lane's elements are all inside the row or all outside: K % 16 == 0).

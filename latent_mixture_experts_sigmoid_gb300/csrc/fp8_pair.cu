@@ -36,7 +36,7 @@ constexpr uint32_t kBoxBytes = kHalf * kBK;
 constexpr uint32_t kStageBytes = 2 * kBoxBytes;    // of one CTA
 constexpr int kStages = 6;
 constexpr int kAcc = 2;                            // TMEM accumulators of 256 columns
-constexpr int kScaleBlocks = 8, kScaleBuffers = 3, kScaleStride = kHalf + 4;
+constexpr int kScaleBlocks = 16, kScaleBuffers = 2, kScaleStride = kHalf + 4;
 constexpr int kBand = 8;                           // feature tiles of a band of the walk
 enum : int { kErrProducer = 1, kErrMmaFull = 2, kErrMmaTmem = 3, kErrEpilogue = 4,
              kErrDrain = 5, kErrDone = 6 };        // device error word codes
@@ -250,13 +250,17 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
           ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kSempty + buf), ph ^ 1u, abort_flag, p.err, kErrProducer));
           if (!ok) break;
           // a lane: one of the K blocks of every fourth row (eight lanes: a row's sector)
-          const int k = kb + (lane & 7);
-          if (k < p.nkb) {
-            uint32_t dst = smem_u32(tok_scale + (buf * kScaleBlocks + (lane & 7)) * kScaleStride + (lane >> 3));
-            for (int r = lane >> 3; r < rows; r += 4, dst += 16u)
-              asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst),
-                           "l"(src + (long long)r * p.nkb + k)
-                           : "memory");
+#pragma unroll
+          for (int k8 = 0; k8 < kScaleBlocks; k8 += 8) {
+            const int k = kb + k8 + (lane & 7);
+            if (k < p.nkb) {
+              uint32_t dst =
+                  smem_u32(tok_scale + (buf * kScaleBlocks + k8 + (lane & 7)) * kScaleStride + (lane >> 3));
+              for (int r = lane >> 3; r < rows; r += 4, dst += 16u)
+                asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst),
+                             "l"(src + (long long)r * p.nkb + k)
+                             : "memory");
+            }
           }
           asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(bar_at(kSfull + buf))
                        : "memory");
