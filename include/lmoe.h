@@ -413,7 +413,8 @@ typedef struct lmoe_fp8_experts {
 /* y [rows, latent] bf16.  Requires 1 <= E <= 1024, latent % 128 == 0,         */
 /* inter % 128 == 0, latent and inter <= 8192, 0 <= rows <= 2^27.             */
 /* The workspace (lmoe_experts_fp8_workspace_bytes, 256-byte aligned) holds  */
-/* act (up to 512 rows in fp32, which the second product quantises itself).  */
+/* act (of experts with few rows in fp32: their second product quantises     */
+/* it).  Weights, scales and offsets are read in stream order.     */
 size_t lmoe_experts_fp8_workspace_bytes(int64_t rows, int E, int latent, int inter);
 int lmoe_experts_fp8(const lmoe_fp8_experts* experts, const uint8_t* x, const float* xs,
                      const int32_t* expert_offsets, lmoe_bf16* y, int64_t rows, int E, int latent,

@@ -141,13 +141,30 @@ struct Ws {
   int32_t *light, *n_light, *h_expert, *h_count, *h_offset, *h_prefix;
   // e4m3 forward: expert-major rows and activations, codes and scales
   uint8_t *A8, *act8;
-  float *A8s, *act8s;
+  float *A8s, *act8s, *act8f;
 };
 
-// Up to this many rows the experts' weights are streamed for a few tokens at a
-// time (each expert has them re-read from L2 per eight rows; at more rows a heavily
-// loaded expert would be re-read too often).
-constexpr long long kFp8StreamRows = 512;
+// Kernels of the e4m3 experts: light ones' weights are streamed for eight rows at a time
+// (fp8_stream.cu), heavy ones run on the tensor-core kernel (fp8.cu).  Where a call has both,
+// each kernel picks its own from the offsets on the device, and one without experts costs 2 to
+// 3 us, so most calls have one of them only:
+//   heavy  above eight rows an expert in the mean ([128 rows, 8 experts] 20 us, streamed 32;
+//          [1024, 64] 50 and 131), and above one where an expert may have many (896 experts,
+//          latent 2048, inter 512: 1024 rows 178 us, streamed 170, both 190; 2048 rows 210, 254
+//          and 243);
+//   light  where no expert can have more than kFp8LightRows, or up to kFp8LightTotal rows in
+//          all (128 rows: 58 us, 72 heavy, 64 both; if one expert has all of them, 85 and 17);
+//   both   otherwise (512 rows, up to 12 an expert: 121 light, 139 heavy, 132 both).
+constexpr int kFp8LightRows = 32, kFp8LightTotal = 128;
+struct Fp8Plan {
+  bool light, heavy;
+};
+// max_rows: the most rows that one expert can have.
+Fp8Plan fp8_plan(long long rows, int E, long long max_rows) {
+  if (max_rows > 8 && rows > 8ll * E) return {false, true};
+  if (max_rows <= kFp8LightRows || rows <= kFp8LightTotal) return {true, false};
+  return {rows <= E, true};
+}
 
 // Which form the routed experts' weights have.
 enum class Experts { kBf16, kMxfp4, kFp8 };
@@ -231,8 +248,10 @@ size_t carve(const lmoe_dims& d, char* base, Ws* ws, Experts form = Experts::kBf
   if (form == Experts::kFp8) {
     w.A8 = c.take<uint8_t>(T * k * L);
     w.A8s = c.take<float>(T * k * (L / kFp8Block));
-    w.act8 = c.take<uint8_t>(T * k * dI * (T * k <= (size_t)kFp8StreamRows ? sizeof(float) : 1));
-    w.act8s = c.take<float>(T * k * (dI / kFp8Block));
+    const Fp8Plan fp = fp8_plan((long long)(T * k), d.num_experts, d.T);
+    w.act8 = fp.heavy ? c.take<uint8_t>(T * k * dI) : nullptr;
+    w.act8s = fp.heavy ? c.take<float>(T * k * (dI / kFp8Block)) : nullptr;
+    w.act8f = fp.light ? c.take<float>(T * k * dI) : nullptr;
   }
   if (ws) *ws = w;
   return (c.off + 255) & ~size_t(255);
@@ -333,6 +352,7 @@ struct Plan {
   int g1_bn, g2_bn;  // MMA N of the grouped GEMMs
   bool fp4_direct;   // the MXFP4 forward runs the 4-bit expert kernels
   int fp4_heavy;     // heavy-expert slots of the MXFP4 forward
+  Fp8Plan fp8;       // kernels of the e4m3 experts
   DenseCfg down, s1, s2, up;
   DenseCfg rtr;      // the router GEMM: at decode stacked after the down-projection's rows
                      // (one launch), otherwise its own launch
@@ -347,6 +367,7 @@ Plan make_plan(const lmoe_dims& d, int nsm, bool router = false) {
   p.tile = p.decode ? round_up(d.T, 16) : 128;
   p.fp4_direct = fp4_direct(d);
   p.fp4_heavy = fp4_heavy_slots(d);
+  p.fp8 = fp8_plan((long long)d.T * d.topk, d.num_experts, d.T);
   p.g1_bn = p.decode ? p.tile : ((2 * d.inter) % 256 == 0 ? 256 : 128);
   // tokens on M: a 256-row B operand of 128 gate + 128 up rows; weights on M
   // (decode): the two halves as two MMAs of N = tile tokens
@@ -372,9 +393,10 @@ int plan_launches(const Plan& p, bool shared, Experts form = Experts::kBf16) {
   // without the 4-bit kernels, one dequantization kernel first
   int experts = p.fuse_g1 ? 2 : 3;
   if (mxfp4) experts = p.fp4_direct ? 2 + (p.fp4_heavy > 0 ? 3 : 0) : experts + 1;
-  // e4m3: one kernel per stage, and at decode sizes the quantisation of the
+  // e4m3: one or two kernels per stage, and at decode sizes the quantisation of the
   // scattered rows (above, the scatter quantises)
-  if (form == Experts::kFp8) experts = 2 + (p.decode ? 1 : 0);
+  if (form == Experts::kFp8)
+    experts = 2 * (p.fp8.light + p.fp8.heavy) + (p.decode ? 1 : 0);
   // route, down, permute, scatter (fused into the permutation at decode sizes),
   // experts, combine
   int n = 1 + 1 + perm + (p.decode ? 0 : 1) + experts + 1;
@@ -487,50 +509,70 @@ int check_fp8_experts(const lmoe_fp8_experts& w) {
   return LMOE_OK;
 }
 
+// The activations between the e4m3 experts' two products: codes and scales of the heavy
+// experts' rows, fp32 values of the light ones' (their second product quantises them).
+struct Fp8Act {
+  uint8_t* codes;
+  float* scales;
+  float* values;
+};
+
 // One stage of the e4m3 experts: 1 = act from x (product and SituGLU), 2 = y from act.
-// `act` holds codes with scales act_s, or up to kFp8StreamRows rows fp32 values.
+// Kernels of one call may overlap, but each launch's end says that all before it are
+// complete: of stage 1 the heavy experts' comes first and waits, the light experts' runs
+// beside it and waits at its end; of stage 2 the light experts' comes first, so that it reads
+// its first weights while stage 1 ends.
 cudaError_t experts_fp8(const lmoe_fp8_experts& w, const uint8_t* x, const float* xs,
-                        const int32_t* offsets, uint8_t* act, float* act_s, uint16_t* y,
-                        long long rows, int E, int L, int d, float beta, float linear_beta,
+                        const int32_t* offsets, const Fp8Act& act, uint16_t* y, long long rows,
+                        int E, int L, int d, float beta, float linear_beta, const Fp8Plan& plan,
                         int stage, cudaStream_t s) {
-  Fp8Gemm g{};
-  g.rows = rows;
-  g.groups = E;
-  g.offsets = offsets;
-  const bool stream = rows <= kFp8StreamRows;
+  Fp8Gemm heavy{};
+  heavy.rows = rows;
+  heavy.groups = E;
+  heavy.offsets = offsets;
+  heavy.W = stage == 1 ? w.w13_codes : w.w2_codes;
+  heavy.ws = stage == 1 ? w.w13_scales : w.w2_scales;
+  heavy.feat = stage == 1 ? 2 * d : L;
+  heavy.K = stage == 1 ? L : d;
+  heavy.beta = beta;
+  heavy.linear_beta = linear_beta;
+  if (stage == 2) heavy.out = y;
+  Fp8Gemm light = heavy;
+  heavy.X = stage == 1 ? x : act.codes;
+  heavy.xs = stage == 1 ? xs : act.scales;
   if (stage == 1) {
-    g.X = x;
-    g.xs = xs;
-    g.W = w.w13_codes;
-    g.ws = w.w13_scales;
-    g.feat = 2 * d;
-    g.K = L;
-    if (stream) g.act_f32 = reinterpret_cast<float*>(act);
-    else g.act = act;
-    g.act_s = act_s;
-    g.beta = beta;
-    g.linear_beta = linear_beta;
+    heavy.act = act.codes;
+    heavy.act_s = act.scales;
+    light.X = x;
+    light.xs = xs;
+    light.act_f32 = act.values;
+    light.beside = plan.heavy;
   } else {
-    if (stream) g.act_in = reinterpret_cast<const float*>(act);
-    g.X = act;
-    g.xs = act_s;
-    g.W = w.w2_codes;
-    g.ws = w.w2_scales;
-    g.feat = L;
-    g.K = d;
-    g.out = y;
+    light.act_in = act.values;
   }
-  return launch_fp8_gemm(g, s);
+  if (plan.light) heavy.min_rows = kFp8LightRows;
+  if (plan.heavy) light.max_rows = kFp8LightRows;
+  for (int i = 0; i < 2; ++i) {
+    const bool is_heavy = (i == 0) == (stage == 1);
+    if (is_heavy ? !plan.heavy : !plan.light) continue;
+    const cudaError_t e = is_heavy ? launch_fp8_gemm(heavy, s) : launch_fp8_stream(light, s);
+    if (e != cudaSuccess) return e;
+  }
+  return cudaSuccess;
 }
 
-// Workspace of the activations between the two: their codes (or few rows' fp32
-// values), then the scales.
-size_t fp8_act_bytes(long long rows, int d) {
-  const size_t n = (size_t)rows * d * (rows <= kFp8StreamRows ? sizeof(float) : 1);
-  return (n + 255) & ~size_t(255);
-}
-size_t fp8_scale_bytes(long long rows, int d) {
-  return ((size_t)rows * (d / kFp8Block) * sizeof(float) + 255) & ~size_t(255);
+// Workspace of lmoe_experts_fp8 (base NULL: its size).
+size_t carve_fp8_act(long long rows, int d, const Fp8Plan& plan, char* base, Fp8Act* act) {
+  Carver c;
+  c.base = base;
+  Fp8Act a{};
+  if (plan.heavy) {
+    a.codes = c.take<uint8_t>((size_t)rows * d);
+    a.scales = c.take<float>((size_t)rows * (d / kFp8Block));
+  }
+  if (plan.light) a.values = c.take<float>((size_t)rows * d);
+  if (act) *act = a;
+  return ((c.off + 255) & ~size_t(255)) + 256;
 }
 
 // The checks of the router's training entry points that need no pointer.
@@ -922,13 +964,14 @@ static int forward_impl(const lmoe_dims* dims, const lmoe_weights* wt, const lmo
   const uint16_t* W13 = wt->w13;
   const uint16_t* W2 = wt->w2;
   if (e8) {
-    LMOE_TRY(experts_fp8(*e8, ws.A8, ws.A8s, ws.offsets, ws.act8, ws.act8s, ws.Y, rows, E, L, dI,
-                         d.beta, d.linear_beta, 1, s));
-    if (!mark(LMOE_STAGE_GEMM1 + 1) || !mark(LMOE_STAGE_SITU + 1)) return LMOE_ERR_CUDA;
     st = fork_shared_late();
     if (st != LMOE_OK) return st;
-    LMOE_TRY(experts_fp8(*e8, ws.A8, ws.A8s, ws.offsets, ws.act8, ws.act8s, ws.Y, rows, E, L, dI,
-                         d.beta, d.linear_beta, 2, s));
+    const Fp8Act act{ws.act8, ws.act8s, ws.act8f};
+    for (int stage = 1; stage <= 2; ++stage) {
+      LMOE_TRY(experts_fp8(*e8, ws.A8, ws.A8s, ws.offsets, act, ws.Y, rows, E, L, dI, d.beta,
+                           d.linear_beta, pl.fp8, stage, s));
+      if (stage == 1 && (!mark(LMOE_STAGE_GEMM1 + 1) || !mark(LMOE_STAGE_SITU + 1))) return LMOE_ERR_CUDA;
+    }
     if (!mark(LMOE_STAGE_GEMM2 + 1)) return LMOE_ERR_CUDA;
   } else if (fq && pl.fp4_direct) {
     // MXFP4: GEMM1 + SituGLU and GEMM2 straight from the 4-bit weights, one
@@ -1185,7 +1228,7 @@ size_t lmoe_experts_fp8_workspace_bytes(int64_t rows, int E, int latent, int int
   if (rows < 0 || rows > kMaxFp8Rows || E < 1 || E > 1024 || latent <= 0 || latent % kFp8Block ||
       latent > kMaxFp8Dim || inter <= 0 || inter % kFp8Block || inter > kMaxFp8Dim)
     return 0;
-  return fp8_act_bytes(rows, inter) + fp8_scale_bytes(rows, inter) + 256;
+  return carve_fp8_act(rows, inter, fp8_plan(rows, E, rows), nullptr, nullptr);
 }
 
 int lmoe_experts_fp8(const lmoe_fp8_experts* experts, const uint8_t* x, const float* xs,
@@ -1207,11 +1250,12 @@ int lmoe_experts_fp8(const lmoe_fp8_experts* experts, const uint8_t* x, const fl
   if (!on_current_device({experts->w13_codes, experts->w13_scales, experts->w2_codes,
                           experts->w2_scales, x, xs, expert_offsets, y, workspace}))
     return LMOE_ERR_DEVICE;
-  uint8_t* act = static_cast<uint8_t*>(workspace);
-  float* act_s = reinterpret_cast<float*>(act + fp8_act_bytes(rows, inter));
+  const Fp8Plan plan = fp8_plan(rows, E, rows);
+  Fp8Act act;
+  carve_fp8_act(rows, inter, plan, static_cast<char*>(workspace), &act);
   for (int stage = 1; stage <= 2; ++stage)
-    LMOE_TRY(experts_fp8(*experts, x, xs, expert_offsets, act, act_s, y, rows, E, latent, inter,
-                         beta, linear_beta, stage, (cudaStream_t)stream));
+    LMOE_TRY(experts_fp8(*experts, x, xs, expert_offsets, act, y, rows, E, latent, inter, beta,
+                         linear_beta, plan, stage, (cudaStream_t)stream));
   return LMOE_OK;
 }
 

@@ -205,6 +205,7 @@ enum : int { kErrProducer = 1, kErrMmaFull = 2, kErrMmaTmem = 3, kErrEpilogue = 
 struct Fp8Params {
   int feat, nkb, groups, nfeat, stages, ws_rows;
   int wide_store;    // rows of out start on 32 bytes
+  int min_rows;      // groups of up to this many rows are another kernel's
   int splits;        // > 1: clusters of this many CTAs share a tile's K blocks (one tile a cluster)
   long long rows;
   const int32_t* offsets;
@@ -305,7 +306,7 @@ __device__ void build_groups(const Fp8Params& p, int* prefix, int* first, int* e
       const int b = min(max(__ldg(p.offsets + g + 1), a), R);
       first[g] = a;
       end[g] = b;
-      tiles[i] = (b - a + BM - 1) / BM;
+      tiles[i] = b - a > p.min_rows ? (b - a + BM - 1) / BM : 0;
     }
     sum += tiles[i];
   }
@@ -384,7 +385,15 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
   auto tempty_bar = [&](uint32_t a) { return bar0 + 8u * (2u * S + kAcc + a); };
   const uint32_t done_bar = bar0 + 8u * (2u * S + 2u * kAcc);
 
-  pdl_trigger();
+  // Operands, scales and offsets may come from the preceding kernel: nothing is read before
+  // the wait.  (Grouped: nothing after this kernel starts before it either, see Fp8Gemm::beside.)
+  if (p.offsets) {
+    pdl_wait();
+    pdl_trigger();
+    build_groups(p, prefix, first, end, warp_sum);
+    __syncthreads();
+    if (prefix[p.groups] == 0) return;     // no group of this kernel's
+  }
   if (threadIdx.x == 0) {
     for (int s = 0; s < S; ++s) {
       mbar_init(full_bar(s), 1);
@@ -405,9 +414,10 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
                  : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
   }
-  // operands, scales and offsets may come from the preceding kernel: nothing is read before this
-  pdl_wait();
-  if (p.offsets) build_groups(p, prefix, first, end, warp_sum);
+  if (!p.offsets) {
+    pdl_trigger();
+    pdl_wait();
+  }
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -709,6 +719,7 @@ cudaError_t launch_form(const Fp8Gemm& g, int splits, cudaStream_t s) {
   p.act = g.act;
   p.act_s = g.act_s;
   p.splits = splits;
+  p.min_rows = g.min_rows;
   p.wide_store = g.feat % 16 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 31u) == 0;
   p.err = device_error_word();
   p.sp = make_situ_params(g.beta > 0.0f ? g.beta : 1.0f, g.linear_beta);
@@ -776,8 +787,8 @@ cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   // [16, 4096] x [7168, 4096] 11.8 us as a stream, 12.8 here, [16, 7168] x [8192, 7168] 22.4
   // and 17.5
   const long long weights = (long long)g.feat * g.K;
-  if (g.act_f32 || g.act_in ||
-      (!g.offsets && (g.rows <= kStreamRows / 2 || (g.rows <= kStreamRows && weights <= 40ll << 20))))
+  if (!g.offsets &&
+      (g.rows <= kStreamRows / 2 || (g.rows <= kStreamRows && weights <= 40ll << 20)))
     return launch_fp8_stream(g, s);
   if (g.act) return launch_form<2, kFormSitu>(g, 1, s);
   DenseForm f{false, g.feat > 128, 1};

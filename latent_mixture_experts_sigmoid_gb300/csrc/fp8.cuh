@@ -34,6 +34,13 @@ struct Fp8Gemm {
   // (instead of X and xs), which quantises them by the same rule
   float* act_f32;
   const float* act_in;
+  // grouped: only groups of more than min_rows rows (the tensor-core kernel), of up to
+  // max_rows (the streaming kernel; 0: any number)
+  int min_rows, max_rows;
+  // the kernel launched before this one writes nothing that this one reads, and has waited
+  // for all work before it: this one waits at its end only, so that its own end says
+  // that both are complete
+  int beside;
 };
 
 // Dense products of up to this many token rows stream their weights through

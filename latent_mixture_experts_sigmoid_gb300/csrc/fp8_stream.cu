@@ -44,6 +44,8 @@ struct StreamParams {
   float* act_out;            // kGateUp: fp32 [rows, feat / 2]
   const int32_t* offsets;    // grouped: [groups + 1]
   int rows, feat, K, nkb, ws_rows, groups, stages;
+  int max_rows;              // experts of more rows are another kernel's
+  int beside;                // kGateUp: see Fp8Gemm
   int* err;
   SituParams sp;
 };
@@ -85,7 +87,7 @@ __device__ __forceinline__ uint4 ld_chunk(const uint8_t* box, int row, int chunk
   return *reinterpret_cast<const uint4*>(box + row * 128 + ((chunk ^ (row & 7)) << 4));
 }
 
-// The experts that have rows, in expert order (clamped to the rows there are).
+// The experts that have rows (up to max_rows), in expert order (clamped to the rows there are).
 struct ExpertList {
   uint16_t* id;
   int* first;
@@ -102,6 +104,7 @@ __device__ int build_list(const StreamParams& p, const ExpertList& l, int* warp_
     if (g0 + i < p.groups) {
       a[i] = min(max(__ldg(p.offsets + g0 + i), 0), p.rows);
       n[i] = min(max(__ldg(p.offsets + g0 + i + 1), a[i]), p.rows) - a[i];
+      if (n[i] > p.max_rows) n[i] = 0;
     }
     has += n[i] > 0;
   }
@@ -218,7 +221,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
   // The first product triggers the second only after its own wait, so by then
   // everything before the first is complete: the second reads its weights, their
   // scales and the offsets, none of which the first writes, ahead of its wait.
-  if (kMode != kSecond) pdl_wait();
+  if (kMode == kDense || (kMode == kGateUp && !p.beside)) pdl_wait();
   pdl_trigger();
   const int feats = kMode == kGateUp ? kRows / 2 : kRows;
   const int nfb = kMode == kDense ? (p.feat + kRows - 1) / kRows : p.feat / kRows;
@@ -422,6 +425,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
       }
       asm volatile("bar.sync %0, %1;" ::"r"(1 + group), "n"(kGroupWarps * 32) : "memory");   // the parts are free again
     }
+    if (kMode == kGateUp && p.beside) pdl_wait();
   }
 }
 
@@ -468,6 +472,8 @@ cudaError_t launch_stream(const Fp8Gemm& g, cudaStream_t s) {
   p.nkb = fp8_blocks(g.K);
   p.ws_rows = fp8_blocks(g.feat);
   p.groups = g.groups;
+  p.max_rows = g.max_rows > 0 ? g.max_rows : 0x7FFFFFFF;
+  p.beside = g.beside;
   constexpr int kFit = (kRingBytes + 16 * 1024 - kPart) / kStage;
   constexpr int kStages = kFit < kMaxStages ? kFit : kMaxStages;
   constexpr int kGroupWarps = kConsumers / kGroups;

@@ -99,9 +99,13 @@ def test_layer(lib):
     assert lib.latent_moe_workspace_bytes_fp8(B(half)) == 0
     assert f(B(half), B(w), B(q), p, p, p, p, nb, None, None) == -2
     assert lib.latent_moe_launch_count_fp8(B(half), 1) == 0
+    # the quantisation of the scattered rows at decode sizes; a second kernel per product
+    # for experts with more than 32 rows where the mean expert has one at the most
     for T, more in ((8, 1), (128, 1), (129, 0), (300, 0)):
         dt = lm.make_dims(dataclasses.replace(W.TINY, T=T))
         assert lib.latent_moe_launch_count_fp8(B(dt), 1) == lib.latent_moe_launch_count(B(dt), 1) + more
+    many = lm.make_dims(dataclasses.replace(W.TINY, T=40, num_experts=1024))
+    assert lib.latent_moe_launch_count_fp8(B(many), 1) == lib.latent_moe_launch_count(B(many), 1) + 3
 
 
 def test_balance_loss(lib):

@@ -249,6 +249,10 @@ def check_experts(x, xs, off, Q, L, d, beta, lbeta, y):
     (6, 512, 384, [8, 9, 16, 17, 0, 40], 8.0),       # passes of eight tokens
     (900, 256, 128, [i % 2 for i in range(900)], 8.0),
     (900, 128, 256, [int(i % 3 > 0) for i in range(900)], 8.0),    # over 512 rows, few each
+    (200, 256, 128, [1, 33, 32, 0, 70] + [i % 2 for i in range(195)] , 8.0),   # light and heavy experts
+    (300, 256, 128, [i % 2 for i in range(300)], 8.0),                         # ... none heavy
+    (300, 128, 256, [0] * 7 + [290] + [0] * 292, 8.0),                         # ... none light
+    (20, 256, 128, [120] + [0] * 18 + [8], 8.0),     # few rows, nearly all one expert's
 ])
 def test_experts_match_float64(E, L, d, counts, lbeta):
     from tests.gpu_util import host_bits
@@ -307,7 +311,7 @@ def quantized_experts(wts):
 
 
 @pytest.mark.parametrize("T,E,topk,shared", [(1, 64, 4, True), (8, 64, 4, True), (100, 16, 4, True),
-                                             (128, 64, 4, False), (129, 64, 4, True), (300, 64, 4, True),
+                                             (128, 64, 4, False), (40, 1024, 4, True), (129, 64, 4, True), (300, 64, 4, True),
                                              (257, 8, 8, False)])
 def test_layer_forward(T, E, topk, shared):
     # Z (or the scattered rows) from the GPU -> quantised rows -> experts' Y, each
