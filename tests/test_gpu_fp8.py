@@ -125,6 +125,35 @@ def test_linear_matches_float64(T, N, K, with_add):
     assert bool((buf[-GUARD:] == 7.0).all())
 
 
+@pytest.mark.parametrize("T,N,K", [(3, 48, 272), (40, 272, 400), (140, 1040, 384), (1300, 4112, 144)])
+def test_linear_16_byte_alignment(T, N, K):
+    # every operand 16 bytes past a 256-byte boundary: what the header asks for and no more
+    from tests.gpu_util import dev_bf16, host_bits
+    g = np.random.default_rng(T)
+    x, xs = codes_of(g, T, K, 1)
+    w, ws = codes_of(g, N, K, 128, 0.02)
+    add = O.f64_to_bf16_bits(g.standard_normal((T, N)))
+
+    def off(t):
+        n = 16 // t.element_size()
+        buf = torch.zeros(t.numel() + n, dtype=t.dtype, device="cuda")
+        buf[n:].copy_(t.flatten())
+        return buf[n:].view(t.shape)
+
+    out = off(torch.full((T, N), 7.0, dtype=torch.bfloat16, device="cuda"))
+    assert out.data_ptr() % 32 == 16
+    for a in (None, off(dev_bf16(add))):
+        lm.lmoe_linear_fp8(off(dev(x)), off(dev(xs)), off(dev(w)), off(dev(ws)), out, add=a)
+        ref, mag = F.linear(x, xs, w, ws, None if a is None else O.bf16_to_f64(add))
+        assert_close(O.bf16_to_f64(host_bits(out)), ref, mag, K)
+    codes, scales = off(torch.zeros((T, K), dtype=torch.uint8, device="cuda")), off(torch.zeros((T, F.blocks(K)), device="cuda"))
+    bits = O.f64_to_bf16_bits(g.standard_normal((T, K)))
+    lm.lmoe_quantize_fp8(off(dev_bf16(bits)), codes, scales)
+    want, want_s = F.quantize(bits)
+    np.testing.assert_array_equal(codes.cpu().numpy(), want)
+    np.testing.assert_array_equal(scales.cpu().numpy(), want_s)
+
+
 def test_linear_every_code():
     # every finite e4m3 code as an operand, one product a row: exact but for the bf16 rounding
     from tests.gpu_util import host_bits
