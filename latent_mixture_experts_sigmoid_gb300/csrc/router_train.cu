@@ -670,25 +670,24 @@ cudaError_t launch_ring(void (*kernel)(KArgs...), int ctas, int ni, int cluster,
   return launch_k(kernel, dim3(ctas), dim3(kWarps * 32), smem, s, std::forward<Args>(args)...);
 }
 
-#define LMOE_BY_EXPERTS(E, CALL)                                  \
-  do {                                                            \
-    const int ni = ((E) + 127) / 128;                             \
-    if ((E) % 4 == 0) {                                           \
-      switch (ni) {                                               \
-        case 1: return CALL(1, true);                             \
-        case 2: return CALL(2, true);                             \
-        case 3: return CALL(3, true);                             \
-        case 4: return CALL(4, true);                             \
-        case 5: return CALL(5, true);                             \
-        case 6: return CALL(6, true);                             \
-        case 7: return CALL(7, true);                             \
-        default: return CALL(8, true);                            \
-      }                                                           \
-    }                                                             \
-    if (ni <= 1) return CALL(1, false);                           \
-    if (ni <= 2) return CALL(2, false);                           \
-    if (ni <= 4) return CALL(4, false);                           \
-    return CALL(8, false);                                        \
+// kNI is ceil(E / 128) exactly: the kernels take all of a row's chunks but the last as full.
+#define LMOE_BY_CHUNKS(NI, CALL, VEC)     \
+  switch (NI) {                           \
+    case 1: return CALL(1, VEC);          \
+    case 2: return CALL(2, VEC);          \
+    case 3: return CALL(3, VEC);          \
+    case 4: return CALL(4, VEC);          \
+    case 5: return CALL(5, VEC);          \
+    case 6: return CALL(6, VEC);          \
+    case 7: return CALL(7, VEC);          \
+    case 8: return CALL(8, VEC);          \
+    default: return cudaErrorInvalidValue; \
+  }
+#define LMOE_BY_EXPERTS(E, CALL)                        \
+  do {                                                  \
+    const int ni = ((E) + 127) / 128;                   \
+    if ((E) % 4 == 0) LMOE_BY_CHUNKS(ni, CALL, true)    \
+    LMOE_BY_CHUNKS(ni, CALL, false)                     \
   } while (0)
 
 }  // namespace

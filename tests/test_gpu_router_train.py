@@ -71,7 +71,10 @@ def loss_tolerance(l, E, T):
 CASES = [(1, 8, 1, 1, False), (2, 4, 4, 1, False), (16, 64, 4, 2, False), (33, 50, 3, 3, True),
          (100, 1, 1, 1, True), (257, 127, 8, 5, True), (300, 896, 16, 2, False), (512, 1024, 32, 4, True),
          (777, 1023, 16, 1, True), (64, 300, 5, 40, False), (5000, 129, 2, 3, True), (2500, 768, 8, 7, True),
-         (3000, 640, 8, 1, False), (700, 384, 6, 2, False), (700, 512, 6, 2, True), (1200, 260, 6, 2, True)]
+         (3000, 640, 8, 1, False), (700, 384, 6, 2, False), (700, 512, 6, 2, True), (1200, 260, 6, 2, True),
+         # every number of 128-expert chunks, odd sizes that end early in the last one
+         (90, 257, 4, 2, True), (400, 259, 4, 1, False), (300, 385, 4, 2, True), (310, 513, 4, 2, False),
+         (40, 641, 8, 3, True), (320, 642, 8, 3, True), (330, 769, 8, 1, True), (340, 897, 16, 2, False)]
 
 
 @pytest.mark.parametrize("T,E,k,S,mask", CASES)
