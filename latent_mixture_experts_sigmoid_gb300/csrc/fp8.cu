@@ -18,6 +18,7 @@
 #include <cuda.h>
 
 #include <mutex>
+#include <type_traits>
 
 #include "fp8.cuh"
 #include "fp8_quant.cuh"
@@ -289,6 +290,21 @@ __device__ __forceinline__ Tile tile_of(const Fp8Params& p, const int* prefix, c
   return x;
 }
 
+// tile_of by a whole warp: the group from two votes of 32 (kMaxGroups = 32 * 32).
+__device__ __forceinline__ Tile tile_of_warp(const Fp8Params& p, const int* prefix, const int* first,
+                                             const int* end, int u, int lane) {
+  if (p.offsets == nullptr) return tile_of(p, prefix, first, end, u);
+  Tile x;
+  const int t = u / p.nfeat;
+  x.feat_tile = u - t * p.nfeat;
+  const int b = __popc(__ballot_sync(0xFFFFFFFFu, lane * 32 < p.groups && prefix[lane * 32] <= t)) - 1;
+  const int g = b * 32 + lane;
+  x.group = b * 32 + __popc(__ballot_sync(0xFFFFFFFFu, g < p.groups && prefix[g] <= t)) - 1;
+  x.row0 = (long long)first[x.group] + (long long)(t - prefix[x.group]) * BM;
+  x.nvalid = (int)min((long long)BM, (long long)end[x.group] - x.row0);
+  return x;
+}
+
 // prefix / first / end of the groups from their offsets, by all threads of the
 // CTA.  Offsets are clamped to [0, rows] and to be ascending within a group, so
 // that no offset can lead outside the buffers.
@@ -431,9 +447,9 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
   const int kb0 = kSplit ? p.nkb * rank / p.splits : 0;
   const int kb1 = kSplit ? p.nkb * (rank + 1) / p.splits : p.nkb;
 
-  // the launch's 168 registers a thread, split anew: 168 * 384 = 72 * 128 + 216 * 256
+  // the launch's 168 registers a thread, split anew: 168 * 384 = 40 * 128 + 232 * 256
   if (warp < kEpiWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0 && lane == 0) {
       // ---------------- TMA producer ----------------
       uint32_t it = 0, s = 0, ph = 0;
@@ -496,23 +512,41 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       wait_phase(done_bar, 0u, &never, p.err, kErrDone);
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     // ---------------- epilogue ----------------
     const int q = warp & 3;                 // TMEM lane quarter this warp may access
     const int h = (warp - kEpiWarp0) >> 2;          // column half
     const int r = q * 32 + lane;            // token row of the tile
     uint32_t acc = 0, aph = 0, par = 0;
     bool ok = true;
-    for (int u = u0; u < U && ok; u += ustep) {
-      const Tile x = tile_of(p, prefix, first, end, u);
-      // scale blocks of this thread's columns (SituGLU: gate and up)
-      const int blk = kSitu ? x.feat_tile : x.feat_tile * kNH + (kNH == 2 ? h : 0);
-      const bool active = q * 32 < x.nvalid && blk < p.ws_rows;   // warp-uniform
-      const bool row_ok = r < x.nvalid;
-      const long long row = x.row0 + (row_ok ? r : 0);
-      const float* xsp = p.xs + row * p.nkb;
-      const float* wsp = p.ws + ((long long)x.group * p.ws_rows + blk) * p.nkb;
-      const float* wsp2 = kSitu ? wsp + (long long)(p.ws_rows / 2) * p.nkb : wsp;
+    // The tile, this thread's row of it and its scales: those of a K block are loaded one
+    // block ahead of its sums, a tile's first ones ahead of the output of the tile before
+    // (65536 rows over 896 experts: 608 -> 565 us with that and no branch around the loads).
+    int ft = 0, row = 0;
+    bool active = false, row_ok = false;
+    const float *xsp = nullptr, *wsp = nullptr;
+    const long long up_scales = kSitu ? (long long)(p.ws_rows / 2) * p.nkb : 0;
+    float nx = 0.0f, nw = 0.0f, nw2 = 0.0f;
+    auto scales = [&](int kb) {      // (without a branch, behind which the loads would be waited for)
+      nx = ld_ahead(xsp + kb);
+      nw = ld_ahead(wsp + kb);
+      if (kSitu) nw2 = ld_ahead(wsp + up_scales + kb);
+    };
+    auto move_to = [&](int u) {
+      const Tile x = tile_of_warp(p, prefix, first, end, u, lane);
+      ft = x.feat_tile;
+      // scale block of this thread's columns (SituGLU: the gate's)
+      int blk = kSitu ? ft : ft * kNH + (kNH == 2 ? h : 0);
+      active = q * 32 < x.nvalid && blk < p.ws_rows;   // warp-uniform
+      blk = min(blk, p.ws_rows - 1);
+      row_ok = active && r < x.nvalid;
+      row = (int)x.row0 + (row_ok ? r : 0);
+      xsp = p.xs + (long long)row * p.nkb;
+      wsp = p.ws + ((long long)x.group * p.ws_rows + blk) * p.nkb;
+      scales(kb0);
+    };
+    if (u0 < U) move_to(u0);
+    for (int u = u0; u < U; u += ustep) {
       f32x2 y[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) y[i] = 0ull;
@@ -521,25 +555,16 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
         __syncwarp();
         if (lane == 0) mbar_arrive_relaxed(tempty_bar(acc));
       };
-      // the scales of a K block are loaded one block ahead of its sums
-      float nx = 0.0f, nw = 0.0f, nw2 = 0.0f;
-      if (active) {
-        nx = ld_ahead(xsp + kb0);
-        nw = ld_ahead(wsp + kb0);
-        if (kSitu) nw2 = ld_ahead(wsp2 + kb0);
-      }
-      for (int kb = kb0; kb < kb1; ++kb) {
-        const float fx = nx, fw = nw, fw2 = nw2;
-        if (active && kb + 1 < kb1) {
-          nx = ld_ahead(xsp + kb + 1);
-          nw = ld_ahead(wsp + kb + 1);
-          if (kSitu) nw2 = ld_ahead(wsp2 + kb + 1);
-        }
-        if (!wait_phase(tfull_bar(acc), aph, abort_flag, p.err, kErrEpilogue)) { ok = false; break; }
+      for (int kb = kb0; kb < kb1 && ok; ++kb) {
+        const float fg = nx * nw, fu = nx * nw2;
+        scales(min(kb + 1, kb1 - 1));
+        // (one outcome for the warp, whose lanes meet again below)
+        ok = __all_sync(0xFFFFFFFFu, wait_phase(tfull_bar(acc), aph, abort_flag, p.err, kErrEpilogue));
+        if (!ok) break;
         tc_fence_after();
         if (active) {
           const uint32_t tb = tmem_base + ((uint32_t)(q * 32) << 16) + acc * kBN;
-          const f32x2 f = f2_splat(fx * fw), f2 = f2_splat(fx * fw2);
+          const f32x2 f = f2_splat(fg), f2 = f2_splat(fu);
           // A load waits for the MMA that the tensor core is at, whatever its width: two of 64
           // columns cost half of what four of 32 do.
 #pragma unroll
@@ -558,26 +583,33 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
         }
         if (++acc == kAcc) { acc = 0; aph ^= 1u; }
       }
-      if (!ok) break;
+      const bool store = active, store_row = ok && row_ok;
+      const int orow = row, oft = ft;
+      if (u + ustep < U) move_to(u + ustep);
+      // (a warp whose waits ran out still meets the other half's below)
       if constexpr (kSitu) {
-        if (active) {
+        if (store) {
           // 64 gate columns (y[0..31]) and the up columns of the same features
           // (y[32..63]); the row's other 64 features are the warp of the other
           // half's.  Their joint maximum is the row's scale for these 128.
           uint32_t m = 0;
+          auto situ = [&](auto linear) {
 #pragma unroll
-          for (int j = 0; j < 32; ++j) {
-            y[j] = situ2_pair(y[j], y[32 + j], p.sp);
-            m = max(m, max(abs_bits(f2_lo(y[j])), abs_bits(f2_hi(y[j]))));
-          }
+            for (int j = 0; j < 32; ++j) {
+              y[j] = situ2_pair_as<decltype(linear)::value>(y[j], y[32 + j], p.sp);
+              m = max(m, max(abs_bits(f2_lo(y[j])), abs_bits(f2_hi(y[j]))));
+            }
+          };
+          // (one branch a tile, so that the 32 chains of special functions interleave)
+          if (p.sp.has_lbeta) situ(std::true_type{}); else situ(std::false_type{});
           uint32_t* ex = amax_ex + par * 256;
           ex[h * 128 + r] = m;
           asm volatile("bar.sync %0, 64;" ::"r"(1 + q) : "memory");
           m = max(m, ex[(h ^ 1) * 128 + r]);
           const BlockScale bs = block_scale(m);
-          if (row_ok) {
+          if (store_row) {
             const int d = p.feat / 2;
-            uint8_t* o = p.act + row * d + x.feat_tile * 128 + h * 64;
+            uint8_t* o = p.act + (long long)orow * d + oft * 128 + h * 64;
 #pragma unroll
             for (int j = 0; j < 32; j += 16) {     // 32 codes
               uint32_t w[8];
@@ -589,22 +621,22 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
               }
               st_global32(o + 2 * j, w);
             }
-            if (h == 0) p.act_s[row * (d / 128) + x.feat_tile] = bs.scale;
+            if (h == 0) p.act_s[(long long)orow * (d / 128) + oft] = bs.scale;
           }
           par ^= 1u;
         }
       } else if constexpr (kSplit) {
         // every MMA of this CTA has completed: the ring is free
-        if (active && row_ok) {
+        if (store_row) {
           float* o = reinterpret_cast<float*>(smem) + r * (kBN + kPartPad) + h * kCols;
 #pragma unroll
           for (int j = 0; j < kCols / 2; j += 2)
             *reinterpret_cast<float4*>(o + 2 * j) =
                 make_float4(f2_lo(y[j]), f2_hi(y[j]), f2_lo(y[j + 1]), f2_hi(y[j + 1]));
         }
-      } else if (active && row_ok) {
-        const int col0 = x.feat_tile * kBN + h * kCols;
-        const long long at = row * p.feat + col0;
+      } else if (store_row) {
+        const int col0 = oft * kBN + h * kCols;
+        const long long at = (long long)orow * p.feat + col0;
         if (p.add) {
           // the addend's row, all of its loads ahead of their use
           uint4 a[kCols / 8];

@@ -114,16 +114,21 @@ __device__ __forceinline__ f32x2 f2_add(f32x2 a, f32x2 b) {
 // elementwise f(x) of a pair through a scalar transcendental op
 #define LMOE_F2_APPLY(f, v) f2_make(__float_as_uint(f(f2_lo(v))), __float_as_uint(f(f2_hi(v))))
 
-// fp32 gate / up pairs in, fp32 pair out
-__device__ __forceinline__ f32x2 situ2_pair(f32x2 g, f32x2 u, const SituParams& p) {
+// fp32 gate / up pairs in, fp32 pair out.  kLinear: p.has_lbeta, for callers whose loops
+// over pairs interleave only without the branch.
+template <bool kLinear>
+__device__ __forceinline__ f32x2 situ2_pair_as(f32x2 g, f32x2 u, const SituParams& p) {
   const f32x2 tg = LMOE_F2_APPLY(tanh_fast, f2_mul(g, f2_splat(p.inv_beta)));
   const f32x2 e = LMOE_F2_APPLY(ex2_fast, f2_mul(g, f2_splat(-1.4426950408889634f)));
-  const f32x2 up = p.has_lbeta ? f2_mul(LMOE_F2_APPLY(tanh_fast, f2_mul(u, f2_splat(p.inv_lbeta))),
-                                        f2_splat(p.lbeta))
-                               : u;
+  const f32x2 up = kLinear ? f2_mul(LMOE_F2_APPLY(tanh_fast, f2_mul(u, f2_splat(p.inv_lbeta))),
+                                    f2_splat(p.lbeta))
+                           : u;
   const f32x2 num = f2_mul(f2_mul(tg, f2_splat(p.beta)), up);
   const f32x2 r = LMOE_F2_APPLY(rcp_fast, f2_add(e, f2_splat(1.0f)));
   return f2_mul(num, r);
+}
+__device__ __forceinline__ f32x2 situ2_pair(f32x2 g, f32x2 u, const SituParams& p) {
+  return p.has_lbeta ? situ2_pair_as<true>(g, u, p) : situ2_pair_as<false>(g, u, p);
 }
 
 // bf16x2 gate / up in, fp32 pair out (lo, hi)
