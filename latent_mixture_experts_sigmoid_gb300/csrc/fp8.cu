@@ -550,6 +550,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       f32x2 y[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) y[i] = 0ull;
+      if (kForm == kFormPlain && p.add && row_ok)
+        add_first<kCols>(y, p.add + (long long)row * p.feat, ft * kBN + h * kCols, p.feat);
       auto release = [&]() {                      // the accumulator is free again
         tc_fence_before();
         __syncwarp();
@@ -637,21 +639,6 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       } else if (store_row) {
         const int col0 = oft * kBN + h * kCols;
         const long long at = (long long)orow * p.feat + col0;
-        if (p.add) {
-          // the addend's row, all of its loads ahead of their use
-          uint4 a[kCols / 8];
-#pragma unroll
-          for (int i = 0; i < kCols / 8; ++i)
-            a[i] = col0 + 8 * i < p.feat ? __ldg(reinterpret_cast<const uint4*>(p.add + at + 8 * i))
-                                         : make_uint4(0, 0, 0, 0);
-#pragma unroll
-          for (int i = 0; i < kCols / 8; ++i) {
-            const uint32_t w[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              y[4 * i + j] = f2_add(y[4 * i + j], f2_make(w[j] << 16, w[j] & 0xFFFF0000u));
-          }
-        }
 #pragma unroll
         for (int j = 0; j < kCols / 2; j += 8) {   // 16 columns
           if (col0 + 2 * j >= p.feat) break;       // feat % 8 == 0

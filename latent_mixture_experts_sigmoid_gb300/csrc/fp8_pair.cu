@@ -285,15 +285,12 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       const int row0 = x.x * kTile + (int)rank * kHalf;
       const int blk = min(x.y * 2 + h, p.ws_rows - 1);
       const float* wsp = p.ws + (long long)blk * p.nkb;
-      if constexpr (kAdd) {      // the addend's row on its way into L2 while the sums run
-        const int n = row0 + r < p.T ? min(kHalf, p.feat - x.y * kTile - h * kHalf) : 0;
-        for (int j = 0; j < n; j += 64)
-          asm volatile("prefetch.global.L2 [%0];" ::"l"(p.add + (long long)(row0 + r) * p.feat +
-                                                          x.y * kTile + h * kHalf + j));
-      }
       f32x2 y[kHalf / 2];
 #pragma unroll
       for (int i = 0; i < kHalf / 2; ++i) y[i] = 0ull;
+      if constexpr (kAdd)
+        if (row0 + r < p.T)
+          add_first<kHalf>(y, p.add + (long long)(row0 + r) * p.feat, x.y * kTile + h * kHalf, p.feat);
       float nw = __ldg(wsp);                     // a K block's scale is loaded one block ahead
       for (int kb0 = 0; kb0 < p.nkb && ok; kb0 += kScaleBlocks) {
         if (!wait_phase(bar_at(kSfull + sbuf), sph, abort_flag, p.err, kErrEpilogue)) { ok = false; break; }
@@ -330,22 +327,6 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       const int row = row0 + r, col0 = x.y * kTile + h * kHalf;
       const int ncol = row < p.T ? min(kHalf, p.feat - col0) : 0;    // a multiple of 8
       const long long at = (long long)row * p.feat + col0;
-      if constexpr (kAdd) {
-        // the addend's row, all of its loads ahead of their use (one after the other they
-        // were eight latencies a tile: 5 us of 19 at T = 300)
-        uint4 a[kHalf / 8];
-#pragma unroll
-        for (int i = 0; i < kHalf / 8; ++i)
-          a[i] = 8 * i < ncol ? __ldg(reinterpret_cast<const uint4*>(p.add + at + 8 * i))
-                              : make_uint4(0, 0, 0, 0);
-#pragma unroll
-        for (int i = 0; i < kHalf / 8; ++i) {
-          const uint32_t w[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            y[4 * i + j] = f2_add(y[4 * i + j], f2_make(w[j] << 16, w[j] & 0xFFFF0000u));
-        }
-      }
 #pragma unroll
       for (int j = 0; j < kHalf / 2; j += 8) {   // 16 columns: 32 bytes
         if (2 * j >= ncol) break;
