@@ -21,6 +21,7 @@
 #include <type_traits>
 
 #include "fp8.cuh"
+#include "fp8_epilogue.cuh"
 #include "fp8_quant.cuh"
 #include "tc_ptx.cuh"
 
@@ -205,7 +206,7 @@ enum : int { kErrProducer = 1, kErrMmaFull = 2, kErrMmaTmem = 3, kErrEpilogue = 
 
 struct Fp8Params {
   int feat, nkb, groups, nfeat, stages, ws_rows;
-  int wide_store;    // rows of out start on 32 bytes
+  int wide_store, wide_add;    // rows of out / of add start on 32 bytes
   int min_rows;      // groups of up to this many rows are another kernel's
   int splits;        // > 1: clusters of this many CTAs share a tile's K blocks (one tile a cluster)
   long long rows;
@@ -550,8 +551,8 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       f32x2 y[kCols / 2];
 #pragma unroll
       for (int i = 0; i < kCols / 2; ++i) y[i] = 0ull;
-      if (kForm == kFormPlain && p.add && row_ok)
-        add_first<kCols>(y, p.add + (long long)row * p.feat, ft * kBN + h * kCols, p.feat);
+      if (kForm == kFormPlain && p.add)     // (`row` exists for every thread)
+        add_first<kCols>(y, p.add + (long long)row * p.feat, ft * kBN + h * kCols, p.feat, p.wide_add);
       auto release = [&]() {                      // the accumulator is free again
         tc_fence_before();
         __syncwarp();
@@ -587,7 +588,11 @@ fp8_gemm_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       }
       const bool store = active, store_row = ok && row_ok;
       const int orow = row, oft = ft;
-      if (u + ustep < U) move_to(u + ustep);
+      if (u + ustep < U) {
+        move_to(u + ustep);
+        if (kForm == kFormPlain && p.add && row_ok)
+          prefetch_addend<kCols>(p.add + (long long)row * p.feat, ft * kBN + h * kCols, p.feat);
+      }
       // (a warp whose waits ran out still meets the other half's below)
       if constexpr (kSitu) {
         if (store) {
@@ -740,6 +745,7 @@ cudaError_t launch_form(const Fp8Gemm& g, int splits, cudaStream_t s) {
   p.splits = splits;
   p.min_rows = g.min_rows;
   p.wide_store = g.feat % 16 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 31u) == 0;
+  p.wide_add = g.feat % 16 == 0 && (reinterpret_cast<uintptr_t>(g.add) & 31u) == 0;
   p.err = device_error_word();
   p.sp = make_situ_params(g.beta > 0.0f ? g.beta : 1.0f, g.linear_beta);
   if (!p.err) return cudaErrorInvalidValue;

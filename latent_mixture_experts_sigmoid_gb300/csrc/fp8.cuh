@@ -63,21 +63,4 @@ cudaError_t launch_quantize_scatter_fp8(const uint16_t* Z, int T, int L, int k,
                                         const int32_t* row_of, uint8_t* codes, float* scales,
                                         cudaStream_t s);
 
-// The sums of a thread's kCols columns from col0 on begin with the addend's row (feat % 8 == 0):
-// its loads run beside the first operands', where after the sums nothing would hide them.
-template <int kCols>
-__device__ __forceinline__ void add_first(f32x2 (&y)[kCols / 2], const uint16_t* row, int col0, int feat) {
-  uint4 a[kCols / 8];
-#pragma unroll
-  for (int i = 0; i < kCols / 8; ++i)
-    a[i] = col0 + 8 * i < feat ? __ldg(reinterpret_cast<const uint4*>(row + col0 + 8 * i))
-                               : make_uint4(0, 0, 0, 0);
-#pragma unroll
-  for (int i = 0; i < kCols / 8; ++i) {
-    const uint32_t w[4] = {a[i].x, a[i].y, a[i].z, a[i].w};
-#pragma unroll
-    for (int j = 0; j < 4; ++j) y[4 * i + j] = f2_make(w[j] << 16, w[j] & 0xFFFF0000u);
-  }
-}
-
 }  // namespace lmoe

@@ -22,6 +22,7 @@
 #include <mutex>
 
 #include "fp8.cuh"
+#include "fp8_epilogue.cuh"
 #include "tc_ptx.cuh"
 
 namespace lmoe {
@@ -42,7 +43,8 @@ enum : int { kErrProducer = 1, kErrMmaFull = 2, kErrMmaTmem = 3, kErrEpilogue = 
              kErrDrain = 5, kErrDone = 6 };        // device error word codes
 
 struct PairParams {
-  int T, feat, nkb, nfeat, ntok, ws_rows, wide_store;
+  int T, feat, nkb, nfeat, ntok, ws_rows;
+  int wide_store, wide_add;    // rows of out / of add start on 32 bytes
   const float* xs;
   const float* ws;
   const uint16_t* add;
@@ -123,7 +125,7 @@ __device__ __forceinline__ int2 tile_of(const PairParams& p, int u) {
   return make_int2(t, band * kBand + rem - t * width);
 }
 
-// kAdd: with an addend (a form of its own: its code, even unused, cost the other 14 %)
+// kAdd: with an addend (an instance of its own: the branch cost the other 2 %)
 template <bool kAdd>
 __global__ void __launch_bounds__(kThreads, 1)
 fp8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__ CUtensorMap tmW,
@@ -177,9 +179,10 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
   const int U = p.ntok * p.nfeat;
   const int u0 = (int)(blockIdx.x >> 1), ustep = (int)(gridDim.x >> 1);
 
-  // the launch's 168 registers a thread, split anew: 168 * 384 = 72 * 128 + 216 * 256
+  // the launch's 168 registers a thread, split anew: 168 * 384 = 40 * 128 + 232 * 256
+  // (216 an epilogue thread: 195 us for [4096, 7168] x [8192, 7168], 232: 187)
   if (warp < kEpiWarp0) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 72;");
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
     if (warp == 0 && lane == 0) {
       // ---------------- TMA producer ----------------
       int s = 0;
@@ -270,7 +273,7 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       asm volatile("cp.async.wait_all;" ::: "memory");
     }
   } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 216;");
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     // ---------------- epilogue ----------------
     const int q = warp & 3;                      // TMEM lane quarter this warp may access
     const int h = (warp - kEpiWarp0) >> 2;       // column half: one block of weight scales
@@ -288,18 +291,28 @@ fp8_pair_kernel(const __grid_constant__ CUtensorMap tmX, const __grid_constant__
       f32x2 y[kHalf / 2];
 #pragma unroll
       for (int i = 0; i < kHalf / 2; ++i) y[i] = 0ull;
-      if constexpr (kAdd)
-        if (row0 + r < p.T)
-          add_first<kHalf>(y, p.add + (long long)(row0 + r) * p.feat, x.y * kTile + h * kHalf, p.feat);
+      if constexpr (kAdd) {
+        add_first<kHalf>(y, p.add + (long long)min(row0 + r, p.T - 1) * p.feat,
+                         x.y * kTile + h * kHalf, p.feat, p.wide_add);
+        if (u + ustep < U) {
+          const int2 n = tile_of(p, u + ustep);
+          const int row = n.x * kTile + (int)rank * kHalf + r;
+          if (row < p.T)
+            prefetch_addend<kHalf>(p.add + (long long)row * p.feat, n.y * kTile + h * kHalf, p.feat);
+        }
+      }
       float nw = __ldg(wsp);                     // a K block's scale is loaded one block ahead
       for (int kb0 = 0; kb0 < p.nkb && ok; kb0 += kScaleBlocks) {
-        if (!wait_phase(bar_at(kSfull + sbuf), sph, abort_flag, p.err, kErrEpilogue)) { ok = false; break; }
+        // (a wait's outcome is one for the warp, whose lanes meet again below)
+        ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kSfull + sbuf), sph, abort_flag, p.err, kErrEpilogue));
+        if (!ok) break;
         const float* sp = tok_scale + sbuf * kScaleBlocks * kScaleStride + r;
         const int kb1 = min(kb0 + kScaleBlocks, p.nkb);
         for (int kb = kb0; kb < kb1; ++kb, sp += kScaleStride) {
           const f32x2 f = f2_splat(*sp * nw);
           nw = __ldg(wsp + min(kb + 1, p.nkb - 1));
-          if (!wait_phase(bar_at(kTfull + (int)acc), aph, abort_flag, p.err, kErrEpilogue)) { ok = false; break; }
+          ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kTfull + (int)acc), aph, abort_flag, p.err, kErrEpilogue));
+          if (!ok) break;
           tc_fence_after();
           // A load waits for the MMA that the tensor core is at, whatever its width: two of 64
           // columns cost half of what four of 32 do.
@@ -428,6 +441,7 @@ cudaError_t launch_fp8_pair(const Fp8Gemm& g, cudaStream_t s) {
   p.ntok = ceil_div(g.rows, kTile);
   p.ws_rows = fp8_blocks(g.feat);
   p.wide_store = g.feat % 16 == 0 && (reinterpret_cast<uintptr_t>(g.out) & 31u) == 0;
+  p.wide_add = g.feat % 16 == 0 && (reinterpret_cast<uintptr_t>(g.add) & 31u) == 0;
   p.xs = g.xs;
   p.ws = g.ws;
   p.add = g.add;
