@@ -147,14 +147,15 @@ struct Ws {
 // Kernels of the e4m3 experts: light ones' weights are streamed for eight rows at a time
 // (fp8_stream.cu), heavy ones run on the tensor-core kernel (fp8.cu).  Where a call has both,
 // each kernel picks its own from the offsets on the device, and one without experts costs 2 to
-// 3 us, so most calls have one of them only:
-//   heavy  above eight rows an expert in the mean ([128 rows, 8 experts] 20 us, streamed 32;
-//          [1024, 64] 50 and 131), and above one where an expert may have many (896 experts,
-//          latent 2048, inter 512: 1024 rows 178 us, streamed 170, both 190; 2048 rows 210, 254
-//          and 243);
-//   light  where no expert can have more than kFp8LightRows, or up to kFp8LightTotal rows in
-//          all (128 rows: 58 us, 72 heavy, 64 both; if one expert has all of them, 85 and 17);
-//   both   otherwise (512 rows, up to 12 an expert: 121 light, 139 heavy, 132 both).
+// 3 us, so most calls have one of them only, by the first rule that holds (us of a call with
+// latent 2048, inter 512, streamed / tensor cores / both):
+//   heavy  above eight rows an expert in the mean ([1024 rows, 64 experts] 131 / 50 / 92,
+//          [128, 8] 32 / 21 / 35);
+//   light  where no expert can have more than kFp8LightRows ([512, 896], up to 12 an expert,
+//          123 / 132 / 132), or up to kFp8LightTotal rows in all ([128, 896] 59 / 70 / 65;
+//          with all of them an expert's 85 / 17);
+//   both   up to half a row an expert in the mean;
+//   heavy  otherwise ([1024, 896] 171 / 168 / 182, [2048, 896] 256 / 197 / 265).
 constexpr int kFp8LightRows = 32, kFp8LightTotal = 128;
 struct Fp8Plan {
   bool light, heavy;
@@ -163,7 +164,7 @@ struct Fp8Plan {
 Fp8Plan fp8_plan(long long rows, int E, long long max_rows) {
   if (max_rows > 8 && rows > 8ll * E) return {false, true};
   if (max_rows <= kFp8LightRows || rows <= kFp8LightTotal) return {true, false};
-  return {rows <= E, true};
+  return {2 * rows <= E, true};
 }
 
 // Which form the routed experts' weights have.

@@ -60,52 +60,42 @@ __device__ __forceinline__ uint2 quant8(const uint4& v, float inv) {
 }
 
 constexpr int kQuantThreads = 256;
-constexpr int kQuantUnroll = 1;
 
 // One scale per row and 128 columns: eight lanes a block, 16 elements a lane
 // (a lane's elements are all inside the row or all outside: K % 16 == 0).
+// Memory bound: each element is read once (2 bytes) and written once (1).  One block a group
+// of lanes and many CTAs: two or four blocks each, their loads all ahead, were no faster
+// ([4096, 7168]: QP_US; [8, 7168]: QD_US).
 __global__ void __launch_bounds__(kQuantThreads)
 quantize_rows_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ codes,
                      float* __restrict__ scales, uint32_t nblocks, uint32_t nkb, int K) {
   pdl_trigger();
   pdl_wait();
   const uint32_t sub = threadIdx.x & 7;
-  constexpr uint32_t kPer = kQuantThreads / 8;   // blocks a CTA handles per step
-  const bool whole = (uint32_t)K == nkb * kFp8Block;
-  const uint32_t b0 = blockIdx.x * (kPer * kQuantUnroll) + (threadIdx.x >> 3);
-  uint4 v[kQuantUnroll][2];
-  long long at[kQuantUnroll];
-#pragma unroll
-  for (int i = 0; i < kQuantUnroll; ++i) {
-    const uint32_t b = b0 + i * kPer;
-    v[i][0] = v[i][1] = make_uint4(0, 0, 0, 0);
-    at[i] = -1;
-    if (b < nblocks) {
-      if (whole) {
-        at[i] = (long long)b * kFp8Block + sub * 16;
-      } else {
-        const uint32_t row = b / nkb, col = (b - row * nkb) * kFp8Block + sub * 16;
-        if (col < (uint32_t)K) at[i] = (long long)row * K + col;
-      }
-    }
-    if (at[i] >= 0) {
-      v[i][0] = ld_stream(x + at[i]);
-      v[i][1] = ld_stream(x + at[i] + 8);
+  const uint32_t b = blockIdx.x * (kQuantThreads / 8) + (threadIdx.x >> 3);
+  long long at = -1;
+  if (b < nblocks) {
+    if ((uint32_t)K == nkb * kFp8Block) {
+      at = (long long)b * kFp8Block + sub * 16;
+    } else {
+      const uint32_t row = b / nkb, col = (b - row * nkb) * kFp8Block + sub * 16;
+      if (col < (uint32_t)K) at = (long long)row * K + col;
     }
   }
-#pragma unroll
-  for (int i = 0; i < kQuantUnroll; ++i) {
-    const uint32_t b = b0 + i * kPer;
-    uint32_t m = max(absmax8(v[i][0]), absmax8(v[i][1]));
-#pragma unroll
-    for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    const BlockScale bs = block_scale(m << 16);
-    if (at[i] >= 0) {
-      const uint2 lo = quant8(v[i][0], bs.inv), hi = quant8(v[i][1], bs.inv);
-      *reinterpret_cast<uint4*>(codes + at[i]) = make_uint4(lo.x, lo.y, hi.x, hi.y);
-    }
-    if (sub == 0 && b < nblocks) scales[b] = bs.scale;
+  uint4 v0 = make_uint4(0, 0, 0, 0), v1 = v0;
+  if (at >= 0) {
+    v0 = ld_stream(x + at);
+    v1 = ld_stream(x + at + 8);
   }
+  uint32_t m = max(absmax8(v0), absmax8(v1));
+#pragma unroll
+  for (int o = 1; o < 8; o <<= 1) m = max(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+  const BlockScale bs = block_scale(m << 16);
+  if (at >= 0) {
+    const uint2 lo = quant8(v0, bs.inv), hi = quant8(v1, bs.inv);
+    *reinterpret_cast<uint4*>(codes + at) = make_uint4(lo.x, lo.y, hi.x, hi.y);
+  }
+  if (sub == 0 && b < nblocks) scales[b] = bs.scale;
 }
 
 // One scale per 128 rows x 128 columns: a CTA a block, eight lanes a row.
@@ -837,7 +827,7 @@ cudaError_t launch_quantize_fp8(const uint16_t* x, uint8_t* codes, float* scales
   const uint32_t nkb = (uint32_t)fp8_blocks(K);
   if (block_rows == 1) {
     const uint32_t nblocks = (uint32_t)(rows * nkb);
-    const uint32_t per = kQuantThreads / 8 * kQuantUnroll;
+    constexpr uint32_t per = kQuantThreads / 8;
     return launch_k(quantize_rows_kernel, dim3((nblocks + per - 1) / per), dim3(kQuantThreads), 0, s,
                     x, codes, scales, nblocks, nkb, K);
   }
