@@ -761,32 +761,32 @@ cudaError_t launch_form(const Fp8Gemm& g, int splits, cudaStream_t s) {
 // Form of a dense product: the one with the least modelled time, in SM cycles.
 //   pair          256 x 256 tiles on two SMs each (fp8_pair.cu)
 //   wide / splits 128 x 256 or 128 x 128 tiles, their K blocks split over clusters
-// A wave of tiles costs its K blocks (more with more token rows; the wide tile does twice
-// the work in 1.3 times the time) and its output, a launch a fixed part, a split the
-// cluster's start and the exchange of the partial tiles.  The constants were fitted to
-// sweeps of the forms over T 24 .. 4096 at [N, K] = [1024, 1024], [2048, 7168], [7168, 2048],
-// [7168, 4096] and [8192, 7168]: the chosen form is within 20 % of the best one at all of them, within 5 % at most
-// (T = 128, [2048, 7168]: split four ways 11.8 us, unsplit 26.1; T = 4096, [8192, 7168]: pair
-// 198 us, wide 215).  Clusters of eight were never clearly the best: about 13 fit at once.
+// A wave of tiles costs its K blocks (more with more token rows) and its output, a launch a
+// fixed part, a split the cluster's start and the exchange of the partial tiles.  The
+// constants were fitted to sweeps of all forms over T 24 .. 4096 at [N, K] = [1024, 1024],
+// [2048, 7168], [7168, 2048], [7168, 4096] and [8192, 7168]: the chosen form is within 5 % of
+// the best one at all 50 of them (T = 128, [2048, 7168]: split four ways 12.6 us, unsplit
+// 24.4; T = 4096, [8192, 7168]: pair 188 us, wide 202, narrow 305).  Clusters of eight were never
+// clearly the best: about 13 fit at once.
 struct DenseForm {
   bool pair, wide;
   int splits;
 };
 DenseForm dense_form(long long T, int N, int nkb, int nsm) {
-  constexpr double kLaunch = 5500, kSplit = 2700, kExchange = 1.0 / 20;
+  constexpr double kLaunch = 5700, kSplit = 5000, kExchange = 1.0 / 15;
   const long long tok = (T + BM - 1) / BM;
   const double rows = T < BM ? (double)T : (double)BM;
   const auto waves = [](long long n, int slots) { return (double)((n + slots - 1) / slots); };
   DenseForm best{true, true, 1};
-  double least = waves((T + 255) / 256 * ((N + 255) / 256), nsm / 2) * (nkb * 950.0 + 2500) + kLaunch;
+  double least = waves((T + 255) / 256 * ((N + 255) / 256), nsm / 2) * (nkb * 900.0 + 5700) + kLaunch;
   for (int wide = 0; wide < 2; ++wide) {
     const int bn = wide ? 256 : 128;
-    const double block = (wide ? 830 : 650) + 1.1 * rows;
+    const double block = (wide ? 700 : 350) + 2.3 * rows;
     const long long tiles = tok * ((N + bn - 1) / bn);
     for (int c = 1; c <= kMaxSplits && c <= nkb; c *= 2) {
       // clusters of four that fit at once: 32 of 152 / 4
       const int slots = c == 1 ? nsm : c == 2 ? nsm / 2 : nsm * 32 / 152;
-      const double cost = c == 1 ? waves(tiles, slots) * (nkb * block + (wide ? 4000 : 2000)) + kLaunch
+      const double cost = c == 1 ? waves(tiles, slots) * (nkb * block + (wide ? 3800 : 3300)) + kLaunch
                                  : waves(tiles, slots) * ((nkb + c - 1) / c * block + kLaunch + kSplit +
                                                           rows * bn * 4 * kExchange);
       if (cost < least) { least = cost; best = DenseForm{false, wide != 0, c}; }
