@@ -64,8 +64,9 @@ constexpr int kQuantThreads = 256;
 // One scale per row and 128 columns: eight lanes a block, 16 elements a lane
 // (a lane's elements are all inside the row or all outside: K % 16 == 0).
 // Memory bound: each element is read once (2 bytes) and written once (1).  One block a group
-// of lanes and many CTAs: two or four blocks each, their loads all ahead, were no faster
-// ([4096, 7168]: QP_US; [8, 7168]: QD_US).
+// of lanes and many CTAs: two or four blocks each, their loads all ahead, were slower
+// ([4096, 7168] 14.9 us, 14.5 with one: 6.1 TB/s; [8192, 7168] 27.1 us, 6.6 TB/s; [8, 7168]
+// 1.3 us, the launch).
 __global__ void __launch_bounds__(kQuantThreads)
 quantize_rows_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ codes,
                      float* __restrict__ scales, uint32_t nblocks, uint32_t nkb, int K) {
@@ -98,7 +99,8 @@ quantize_rows_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ codes
   if (sub == 0 && b < nblocks) scales[b] = bs.scale;
 }
 
-// One scale per 128 rows x 128 columns: a CTA a block, eight lanes a row.
+// One scale per 128 rows x 128 columns: a CTA a block, eight lanes a row, the block in
+// registers between its maximum and its codes.  Memory bound ([8192, 7168] 27.2 us, 6.5 TB/s).
 __global__ void __launch_bounds__(kQuantThreads)
 quantize_blocks_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ codes,
                        float* __restrict__ scales, long long rows, uint32_t nkb, int K) {
@@ -139,7 +141,8 @@ quantize_blocks_kernel(const uint16_t* __restrict__ x, uint8_t* __restrict__ cod
 }
 
 // A token's row quantised once and written to its k expert-major rows: a CTA a
-// token and 4096 columns, 16 columns a thread, eight lanes a block.
+// token and 4096 columns, 16 columns a thread, eight lanes a block.  Bound by the writes
+// (T = 4096, L = 2048, k = 16: 159 MB in 23.3 us, 6.8 TB/s, part of it still in L2).
 __global__ void __launch_bounds__(kQuantThreads)
 quantize_scatter_kernel(const uint16_t* __restrict__ Z, const int32_t* __restrict__ row_of, int L,
                         int k, uint8_t* __restrict__ codes, float* __restrict__ scales) {
@@ -177,6 +180,14 @@ quantize_scatter_kernel(const uint16_t* __restrict__ Z, const int32_t* __restric
 //   warps 4..11 read the finished K block from TMEM (warp w: the 32 token rows
 //               of lane quarter w % 4, half h = (w - 4) / 4 of the columns),
 //               scale and add it in registers, and write the tile.
+// Few rows an expert: bound by the weights' bytes; many: by the epilogue, in which a K block
+// takes about 1050 cycles where its MMAs take 512 (kNH = 2): a TMEM load waits for the MMA in
+// progress, then 128 columns are added up, and the accumulator goes back through a barrier.
+// The wide tile (kNH = 2) halves the token bytes a product reads and the barriers.  SituGLU,
+// four special functions an output, costs a tile another 4500 cycles, in which the tensor core
+// runs two K blocks ahead and the ring fills.
+// 65536 rows over 896 experts, latent 2048, inter 512: first product 362 us (1.84 GB, 5.1 TB/s),
+// second 198 us (1.13 GB, 5.7 TB/s).
 // Every wait is bounded: on expiry the code goes to the device error word, the
 // CTA drains its copies and MMAs, frees its TMEM and returns.
 // ---------------------------------------------------------------------------
@@ -799,11 +810,11 @@ DenseForm dense_form(long long T, int N, int nkb, int nsm) {
 
 cudaError_t launch_fp8_gemm(const Fp8Gemm& g, cudaStream_t s) {
   // 9 to 16 tokens cost a stream's unit as many bytes of tokens as of weights, from L2:
-  // [16, 4096] x [7168, 4096] 11.8 us as a stream, 12.8 here, [16, 7168] x [8192, 7168] 22.4
-  // and 17.5
+  // [16, 7168] x [2048, 7168] 7.0 us as a stream, 10.2 here, [16, 4096] x [7168, 4096] 11.9 and
+  // 11.1, [16, 7168] x [8192, 7168] 22.4 and 15.7 (8 tokens 13.7 and 15.4)
   const long long weights = (long long)g.feat * g.K;
   if (!g.offsets &&
-      (g.rows <= kStreamRows / 2 || (g.rows <= kStreamRows && weights <= 40ll << 20)))
+      (g.rows <= kStreamRows / 2 || (g.rows <= kStreamRows && weights <= 24ll << 20)))
     return launch_fp8_stream(g, s);
   if (g.act) return launch_form<2, kFormSitu>(g, 1, s);
   DenseForm f{false, g.feat > 128, 1};

@@ -2,11 +2,15 @@
 // for one SM).
 //
 // A tile of 128 x 256 on one SM moves 48 KB of operands through its shared memory per
-// K block of 512 tensor cycles, once in from L2 and once out to the tensor core: with
-// the epilogue left out that kernel still takes 970 cycles a block.  Here the two CTAs
-// of a cluster compute one 256 x 256 tile (tcgen05 cta_group::2, M = 256, N = 256): each
-// brings in its own 128 token rows and 128 of the weight rows, 32 KB a block, and the
+// K block of 512 tensor cycles, once in from L2 and once out to the tensor core.  Here the
+// two CTAs of a cluster compute one 256 x 256 tile (tcgen05 cta_group::2, M = 256, N = 256):
+// each brings in its own 128 token rows and 128 of the weight rows, 32 KB a block, and the
 // tensor cores of both read both halves.
+//
+// Bound by the epilogue: a K block must leave TMEM and be scaled before the accumulator takes
+// the next but one (about 930 cycles a block; sixteen epilogue warps of half the columns each
+// took longer, two accumulators of N = 128 per half too).  [4096, 7168] x [8192, 7168]: 188 us,
+// 2.56 PFLOP/s, tensor pipe 55 % busy; the one-SM form takes 202.
 //
 //   warp 0      TMA producer of this CTA's halves; their bytes count on the leader's
 //               (rank 0's) barrier;
