@@ -109,7 +109,7 @@ def test_quantize_extreme_values(block_rows):
     (9, 24, 7168), (15, 256, 144),
     (16, 264, 256), (17, 128, 512), (32, 1024, 2048), (33, 120, 640), (64, 1032, 128), (128, 256, 1024),
     (129, 392, 272), (255, 640, 400), (300, 512, 192), (513, 1000, 1168), (1024, 768, 512),
-    (2050, 2056, 336), (1300, 4104, 1040), (2049, 2304, 2176)])
+    (2050, 2056, 336), (1300, 4104, 1040), (2049, 2304, 2176), (300, 4104, 528), (500, 2560, 272)])
 def test_linear_matches_float64(T, N, K, with_add):
     from tests.gpu_util import dev_bf16, host_bits
     g = np.random.default_rng(T * 7 + N + K)
@@ -282,6 +282,9 @@ def check_experts(x, xs, off, Q, L, d, beta, lbeta, y):
     (300, 256, 128, [i % 2 for i in range(300)], 8.0),                         # ... none heavy
     (300, 128, 256, [0] * 7 + [290] + [0] * 292, 8.0),                         # ... none light
     (20, 256, 128, [120] + [0] * 18 + [8], 8.0),     # few rows, nearly all one expert's
+    (700, 256, 128, [1, 33, 32, 0, 70] + [int(i % 4 == 1) for i in range(695)], 8.0),  # both kernels
+    (700, 128, 256, [0] * 7 + [290] + [0] * 692, 8.0),                       # ... light one without work
+    (1024, 128, 128, [int(i % 31 == 30) * 40 for i in range(1024)], 8.0),    # heavy, groups far apart
 ])
 def test_experts_match_float64(E, L, d, counts, lbeta):
     from tests.gpu_util import host_bits

@@ -74,7 +74,9 @@ CASES = [(1, 8, 1, 1, False), (2, 4, 4, 1, False), (16, 64, 4, 2, False), (33, 5
          (3000, 640, 8, 1, False), (700, 384, 6, 2, False), (700, 512, 6, 2, True), (1200, 260, 6, 2, True),
          # every number of 128-expert chunks, odd sizes that end early in the last one
          (90, 257, 4, 2, True), (400, 259, 4, 1, False), (300, 385, 4, 2, True), (310, 513, 4, 2, False),
-         (40, 641, 8, 3, True), (320, 642, 8, 3, True), (330, 769, 8, 1, True), (340, 897, 16, 2, False)]
+         (40, 641, 8, 3, True), (320, 642, 8, 3, True), (330, 769, 8, 1, True), (340, 897, 16, 2, False),
+         # the largest batch of one launch, and over its limits of logits and of counts
+         (256, 512, 8, 4, True), (256, 516, 8, 4, True), (17, 798, 2, 8, False)]
 
 
 @pytest.mark.parametrize("T,E,k,S,mask", CASES)
