@@ -82,6 +82,10 @@ __device__ __forceinline__ int2 sequence_range(const RouterBatch& b, int s) {
   return make_int2(a, min(max(__ldg(b.seq + s + 1), a), b.T));
 }
 
+// End of a run of up to n tokens from `first` <= T on.  T may be 2^31 - 1, so here and below
+// the distance to the end is what is compared: a token number past the end could wrap.
+__device__ __forceinline__ int run_end(int first, int n, int T) { return first + min(n, T - first); }
+
 // The last sequence that begins at or before token t (0 where none does).
 __device__ __forceinline__ int sequence_of(const RouterBatch& b, int t) {
   if (!b.seq) return 0;
@@ -102,11 +106,11 @@ count_kernel(const RouterBatch b, int per_cta, int32_t* __restrict__ counts,
   __syncthreads();
   bool waited = false;
   const int first = (int)min((long long)blockIdx.x * per_cta, (long long)b.T);
-  const int last = min(first + per_cta, b.T);
+  const int last = run_end(first, per_cta, b.T);
   // the slice's choices and masks on their way while the sequence is looked up
   for (long long i = (long long)first * b.k + threadIdx.x * 32; i < (long long)last * b.k; i += kCountThreads * 32)
     asm volatile("prefetch.global.L2 [%0];" ::"l"(b.ids + i));
-  if (b.mask && first + threadIdx.x * 128 < last)
+  if (b.mask && (int)threadIdx.x * 128 < last - first)
     asm volatile("prefetch.global.L2 [%0];" ::"l"(b.mask + first + threadIdx.x * 128));
   for (int t0 = first; t0 < last;) {
     const int s = sequence_of(b, t0);
@@ -134,8 +138,8 @@ count_kernel(const RouterBatch b, int per_cta, int32_t* __restrict__ counts,
         if (keep[j] && (unsigned)id[j] < (unsigned)b.E) atomicAdd(&hist[id[j]], 1);
     }
     if (b.mask) {
-      for (int t = t0 + threadIdx.x; t < t1; t += kCountThreads)
-        if (__ldg(b.mask + t)) atomicAdd(&hist[b.E], 1);
+      for (int i = threadIdx.x; i < t1 - t0; i += kCountThreads)
+        if (__ldg(b.mask + t0 + i)) atomicAdd(&hist[b.E], 1);
     } else if (threadIdx.x == 0) {
       hist[b.E] = t1 - t0;
     }
@@ -261,7 +265,7 @@ struct SequenceWalk {
   }
   __device__ __forceinline__ void masks(const RouterBatch& b, int t, int lane) {
     base = t;
-    keep = b.mask ? __ballot_sync(kFull, t + lane < b.T && __ldg(b.mask + t + lane) != 0) : kFull;
+    keep = b.mask ? __ballot_sync(kFull, lane < b.T - t && __ldg(b.mask + t + lane) != 0) : kFull;
   }
 
   // Moves to token t; whether it counts.  (kShared: counts and tokens are in shared memory.)
@@ -269,7 +273,7 @@ struct SequenceWalk {
   __device__ __forceinline__ bool at(const RouterBatch& b, const int32_t* counts,
                                      const int32_t* tokens, int t, int lane) {
     if (t >= end && s + 1 < b.S) find(b, t);
-    if (t >= base + 32) masks(b, t, lane);
+    if (t - base >= 32) masks(b, t, lane);
     if (t < begin || t >= end || !(keep >> (t - base) & 1u)) return false;
     if (fresh) load<kShared>(b, counts, tokens, lane);
     return true;
@@ -364,11 +368,11 @@ loss_kernel(const RouterBatch b, float alpha, const int32_t* __restrict__ counts
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   pdl_trigger();
   const long long w = (long long)blockIdx.x * kWarps + warp;
-  const int t0 = (int)min(w * per_warp, (long long)b.T), t1 = min(t0 + per_warp, b.T);
+  const int t0 = (int)min(w * per_warp, (long long)b.T), t1 = run_end(t0, per_warp, b.T);
   RowRing<kNI, kVec> ring(ring_smem, warp, lane);
   // the logits are complete (see the counts); the counts are not
   for (int i = 0; i < kSlots; ++i) {
-    if (t0 + i < t1) ring.fetch(i, b.logits + (long long)(t0 + i) * b.E, b.E, lane);
+    if (i < t1 - t0) ring.fetch(i, b.logits + (long long)(t0 + i) * b.E, b.E, lane);
     ring.commit();
   }
   SequenceWalk<kNI, kVec> q;
@@ -386,7 +390,7 @@ loss_kernel(const RouterBatch b, float alpha, const int32_t* __restrict__ counts
       else if (!(zd.x == 0.0f)) total += zd.x;      // NaN logits stay NaN
     }
     // refilled once its row is used
-    if (t + kSlots < t1) ring.fetch(slot, b.logits + (long long)(t + kSlots) * b.E, b.E, lane);
+    if (t1 - t > kSlots) ring.fetch(slot, b.logits + (long long)(t + kSlots) * b.E, b.E, lane);
     ring.commit();
     slot = slot + 1 == kSlots ? 0 : slot + 1;
   }
@@ -453,7 +457,7 @@ small_loss_kernel(const RouterBatch b, float alpha, int32_t* __restrict__ counts
   const int t0 = min(w * per_warp, b.T), t1 = min(t0 + per_warp, b.T);
   RowRing<kNI, kVec> ring(ring_smem, warp, lane);
   for (int i = 0; i < kSlots; ++i) {
-    if (t0 + i < t1) ring.fetch(i, b.logits + (long long)(t0 + i) * b.E, b.E, lane);
+    if (i < t1 - t0) ring.fetch(i, b.logits + (long long)(t0 + i) * b.E, b.E, lane);
     ring.commit();
   }
   SequenceWalk<kNI, kVec> q;
@@ -493,7 +497,7 @@ small_loss_kernel(const RouterBatch b, float alpha, int32_t* __restrict__ counts
       if (zd.x > 0.0f) sum += q.part * (q.unit * zd.y / zd.x);
       else if (!(zd.x == 0.0f)) sum += zd.x;
     }
-    if (t + kSlots < t1) ring.fetch(slot, b.logits + (long long)(t + kSlots) * b.E, b.E, lane);
+    if (t1 - t > kSlots) ring.fetch(slot, b.logits + (long long)(t + kSlots) * b.E, b.E, lane);
     ring.commit();
     slot = slot + 1 == kSlots ? 0 : slot + 1;
   }
@@ -533,36 +537,37 @@ backward_kernel(const RouterBatch b, const BackwardArgs a) {
   pdl_trigger();
   pdl_wait();
   const long long w = (long long)blockIdx.x * kWarps + warp;
-  const int t0 = (int)min(w * a.per_warp, (long long)b.T), t1 = min(t0 + a.per_warp, b.T);
+  const int t0 = (int)min(w * a.per_warp, (long long)b.T), t1 = run_end(t0, a.per_warp, b.T);
   const float gl = a.grad_loss ? a.alpha * __ldg(a.grad_loss) : 0.0f;
   SequenceWalk<kNI, kVec> q;
   RowRing<kNI, kVec> ring(ring_smem, warp, lane);
   if (t0 < t1 && a.grad_loss) {
     q.start(b, t0, lane);
     for (int i = 0; i < kSlots; ++i) {
-      if (t0 + i < t1) ring.fetch(i, b.logits + (long long)(t0 + i) * b.E, b.E, lane);
+      if (i < t1 - t0) ring.fetch(i, b.logits + (long long)(t0 + i) * b.E, b.E, lane);
       ring.commit();
     }
   }
   // the j-th chosen expert of a token and its gradient are lane j's; they are loaded
   // a token ahead, as is the expert's logit where the row itself is not read
-  auto choice = [&](int t, int& id, float& g) {
+  auto choice = [&](int t, int ahead, int& id, float& g) {      // of token t + ahead
     id = -1;
     g = 0.0f;
-    if (a.grad_w && t < t1 && lane < b.k) {
-      id = __ldg(b.ids + (long long)t * b.k + lane);
-      g = __ldg(a.grad_w + (long long)t * b.k + lane);
+    if (a.grad_w && t1 - t > ahead && lane < b.k) {
+      id = __ldg(b.ids + (long long)(t + ahead) * b.k + lane);
+      g = __ldg(a.grad_w + (long long)(t + ahead) * b.k + lane);
     }
   };
-  auto logit = [&](int t, int id) {
-    return !a.grad_loss && (unsigned)id < (unsigned)b.E ? __ldg(b.logits + (long long)t * b.E + id)
-                                                       : -INFINITY;
+  auto logit = [&](int t, int ahead, int id) {                  // (no id behind the last token)
+    return !a.grad_loss && (unsigned)id < (unsigned)b.E
+               ? __ldg(b.logits + (long long)(t + ahead) * b.E + id)
+               : -INFINITY;
   };
   int id1, id2;
   float g1, g2, l1;
-  choice(t0, id1, g1);
-  choice(t0 + 1, id2, g2);
-  l1 = logit(t0, id1);
+  choice(t0, 0, id1, g1);
+  choice(t0, 1, id2, g2);
+  l1 = logit(t0, 0, id1);
   int slot = 0;
   for (int t = t0; t < t1; ++t) {
     const long long row = (long long)t * b.E;
@@ -571,8 +576,8 @@ backward_kernel(const RouterBatch b, const BackwardArgs a) {
     float g = g1, l = l1;
     id1 = id2;
     g1 = g2;
-    l1 = logit(t + 1, id1);
-    choice(t + 2, id2, g2);
+    l1 = logit(t, 1, id1);
+    choice(t, 2, id2, g2);
     if ((unsigned)id >= (unsigned)b.E) {       // no choice of this lane's, or a dropped one
       id = -1;
       g = 0.0f;
@@ -646,7 +651,7 @@ backward_kernel(const RouterBatch b, const BackwardArgs a) {
     }
     // the slot is refilled once all of the row's uses are over
     if (a.grad_loss) {
-      if (t + kSlots < t1) ring.fetch(slot, b.logits + row + (long long)kSlots * b.E, b.E, lane);
+      if (t1 - t > kSlots) ring.fetch(slot, b.logits + row + (long long)kSlots * b.E, b.E, lane);
       ring.commit();
     }
     slot = slot + 1 == kSlots ? 0 : slot + 1;

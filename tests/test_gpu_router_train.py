@@ -224,3 +224,43 @@ def test_graph_replay_and_autograd_beside_it():
         assert torch.equal(loss, want[0]) and torch.equal(grad, want[1])
     eager.backward()
     assert logits.grad is not None
+
+
+def test_largest_batch():
+    # T * topk = 2^31 - 1: the ends of the last warps' and CTAs' runs, and the tokens that are
+    # looked ahead for, lie past 2^31
+    if torch.cuda.mem_get_info()[0] < 64 << 30:
+        pytest.skip("needs 64 GB")
+    T, tail = 2 ** 31 - 1, 1000
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    l = torch.empty((T, 1), device="cuda").uniform_(-3, 3, generator=gen)
+    gw = torch.empty((T, 1), device="cuda").uniform_(0.5, 1, generator=gen)
+    ids = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    m = torch.ones(T, dtype=torch.uint8, device="cuda")
+    m[5::1 << 20] = 0
+    m[-7:-3] = 0
+    seq = dev(np.array([0, T - tail, T], np.int32))
+    loss, cnt, tok = (torch.full(s, -7, dtype=t, device="cuda") for s, t in (
+        ((1,), torch.float32), ((2, 1), torch.int32), ((2,), torch.int32)))
+    ws = torch.empty(lm.moe_balance_loss_workspace_bytes(T, 1, 2), dtype=torch.uint8, device="cuda")
+    lm.moe_balance_loss(l, ids, 0.5, loss, cnt, tok, ws, token_mask=m, seq_offsets=seq)
+    n = [int(m[:T - tail].sum(dtype=torch.int64)), int(m[T - tail:].sum(dtype=torch.int64))]
+    assert tok.tolist() == n and cnt.flatten().tolist() == n
+    # one expert: each sequence's share of the loss is alpha / 2; a warp's run is summed up in fp32
+    run = T / (16 * torch.cuda.get_device_properties(0).multi_processor_count)
+    assert abs(float(loss) - 0.5) <= 0.5 * ((run + 100) * U + 2.0 ** -16)
+    grad = torch.full((T + GUARD,), 5.0, device="cuda")
+    lm.moe_router_backward(l, ids, grad[:T].view(T, 1), grad_topk_weights=gw, renormalize=0,
+                           routed_scaling_factor=2.0, grad_loss=torch.ones(1, device="cuda"), expert_counts=cnt,
+                           seq_tokens=tok, alpha=0.5, token_mask=m, seq_offsets=seq)
+    for a in range(0, T, 1 << 28):
+        b = min(a + (1 << 28), T)
+        s = torch.sigmoid(l[a:b, 0].double())
+        want = 2.0 * gw[a:b, 0] * s * (1 - s)
+        # the weights' part; the balance loss of one expert has gradient 0 (f - mean f)
+        bound = backward_tolerance(np.array([3.0]), 1, 1) * (2.0 * gw[a:b, 0] * s + 0.5 / tail)
+        assert bool(((grad[a:b].double() - want).abs() <= bound).all()), a
+        del s, want, bound
+    assert bool((grad[T:] == 5.0).all())
+    del l, gw, ids, m, grad
+    torch.cuda.empty_cache()
