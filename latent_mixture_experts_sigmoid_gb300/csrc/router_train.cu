@@ -378,7 +378,15 @@ loss_kernel(const RouterBatch b, float alpha, const int32_t* __restrict__ counts
   SequenceWalk<kNI, kVec> q;
   if (t0 < t1) q.start(b, t0, lane);
   pdl_wait();
-  float total = 0.0f;
+  // A warp's run may have hundreds of thousands of tokens (2^31 - 1 of them: 883012 on 152 SMs),
+  // whose terms are about equal: in one fp32 sum each would lose the same part (50 million
+  // tokens: 1.4e-4 of the loss).  `lost` holds what the last addition rounded off.
+  float total = 0.0f, lost = 0.0f;
+  auto add = [&](float term) {
+    const float x = term - lost, sum = total + x;
+    lost = (sum - total) - x;
+    total = sum;
+  };
   int slot = 0;
   for (int t = t0; t < t1; ++t) {
     f32x2 v[kNI][2];
@@ -386,8 +394,8 @@ loss_kernel(const RouterBatch b, float alpha, const int32_t* __restrict__ counts
     if (q.at(b, counts, tokens, t, lane)) {
       bool tiny;
       const float2 zd = row_sums<kNI, kVec>(v, q.c, ring, slot, b.E, lane, &tiny);
-      if (zd.x > 0.0f) total += q.part * (q.unit * zd.y / zd.x);
-      else if (!(zd.x == 0.0f)) total += zd.x;      // NaN logits stay NaN
+      if (zd.x > 0.0f) add(q.part * (q.unit * zd.y / zd.x));
+      else if (!(zd.x == 0.0f)) add(zd.x);          // NaN logits stay NaN
     }
     // refilled once its row is used
     if (t1 - t > kSlots) ring.fetch(slot, b.logits + (long long)(t + kSlots) * b.E, b.E, lane);

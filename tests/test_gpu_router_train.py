@@ -264,3 +264,18 @@ def test_largest_batch():
     assert bool((grad[T:] == 5.0).all())
     del l, gw, ids, m, grad
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("T,S", [(3 << 24, 1), ((1 << 25) + 77, 3)])
+def test_loss_of_many_tokens(T, S):
+    # one expert, chosen by every token: the loss is alpha exactly.  The bound has no term that
+    # grows with T: the sigmoids, a term's factors, two roundings of a compensated sum, the
+    # CTA's eight and the last CTA's sums (loss_tolerance's others)
+    l = torch.empty((T, 1), device="cuda").uniform_(-3, 3)
+    ids = torch.zeros((T, 1), dtype=torch.int32, device="cuda")
+    cuts = dev(np.array([0, T // 5, T // 2, T] if S == 3 else [0, T], np.int32))
+    loss, cnt, tok = torch.empty(1, device="cuda"), *(torch.empty(S, dtype=torch.int32, device="cuda") for _ in "ab")
+    ws = torch.empty(lm.moe_balance_loss_workspace_bytes(T, 1, S), dtype=torch.uint8, device="cuda")
+    lm.moe_balance_loss(l, ids, 0.25, loss, cnt, tok, ws, seq_offsets=cuts)
+    assert int(tok.sum()) == T and torch.equal(cnt, tok)
+    assert abs(float(loss) - 0.25) <= 0.25 * (2 * (3 + 8 + 1 / 32 + 5 + 2) + 2 + 8 + 32 + 8) * U
