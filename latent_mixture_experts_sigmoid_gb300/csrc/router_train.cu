@@ -41,8 +41,19 @@ constexpr float kLog2e = 1.4426950408889634f;
 // exp(l) to 2^-39, and shares are taken from exp(l - max l), which cannot underflow.
 constexpr float kTinySum = 9.094947017729282e-13f;   // 2^-40
 
-__device__ __forceinline__ float sigmoid_f(float l) {
-  return rcp_fast(1.0f + ex2_fast(-kLog2e * l));
+// {s, 1 - s} of a logit.  With e = exp(-|l|) the smaller of the two is e / (1 + e), the larger
+// 1 / (1 + e): neither is the difference of the other from 1, which a rounded s near 1 would
+// leave nothing of (1 - s at l = 12: 1 % off, from l = 17 on 0).
+__device__ __forceinline__ float2 sigmoid_f(float l) {
+  const float e = ex2_fast(-kLog2e * fabsf(l)), r = rcp_fast(1.0f + e), u = e * r;
+  return l > 0.0f ? make_float2(r, u) : make_float2(u, r);
+}
+
+// min(x, 127), NaN staying NaN (as it would not in fminf)
+__device__ __forceinline__ float most_127(float x) {
+  float y;
+  asm("min.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(127.0f));
+  return y;
 }
 
 __device__ __forceinline__ float warp_sum(float v) {
@@ -308,23 +319,27 @@ struct SequenceWalk {
   }
 };
 
-// The row of a slot -> its sigmoids; returns {Z, sum_e c s}.  Where Z would underflow the
-// row becomes exp(l - max l) instead (see kTinySum), `tiny` set.  Pairs of experts go
-// through the packed fp32 operations: 4 instructions an expert.
-template <int kNI, bool kVec>
+// The row of a slot -> {Z, sum_e c s}.  kKeep: `s` becomes s (1 - s), otherwise s.  1 - s is
+// e s with e = exp(-l), without a difference (see sigmoid_f); e ends at 2^127, where the
+// reciprocal of 1 + e is 0 already, so that e s is 0 and not NaN.  Where Z would underflow, s is
+// exp(l - max l) instead (see kTinySum) and 1 - s is 1.  Pairs of experts go through the
+// packed fp32 operations: 4 instructions an expert, 6 with kKeep.
+template <bool kKeep, int kNI, bool kVec>
 __device__ __forceinline__ float2 row_sums(f32x2 (&s)[kNI][2], const f32x2 (&c)[kNI][2],
-                                           const RowRing<kNI, kVec>& ring, int slot, int E, int lane,
-                                           bool* tiny) {
+                                           const RowRing<kNI, kVec>& ring, int slot, int E, int lane) {
   ring.read(s, slot, E, lane);
   f32x2 z2 = 0ull, dot2 = 0ull;
 #pragma unroll
   for (int i = 0; i < kNI; ++i)
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
-      const f32x2 e = LMOE_F2_APPLY(ex2_fast, f2_mul(s[i][j], f2_splat(-kLog2e)));
-      s[i][j] = LMOE_F2_APPLY(rcp_fast, f2_add(e, f2_splat(1.0f)));
-      z2 = f2_add(z2, s[i][j]);
-      dot2 = f2_fma(c[i][j], s[i][j], dot2);
+      f32x2 x = f2_mul(s[i][j], f2_splat(-kLog2e));
+      if (kKeep) x = LMOE_F2_APPLY(most_127, x);
+      const f32x2 e = LMOE_F2_APPLY(ex2_fast, x);
+      const f32x2 v = LMOE_F2_APPLY(rcp_fast, f2_add(e, f2_splat(1.0f)));
+      z2 = f2_add(z2, v);
+      dot2 = f2_fma(c[i][j], v, dot2);
+      s[i][j] = kKeep ? f2_mul(f2_mul(e, v), v) : v;
     }
   float z = f2_lo(z2) + f2_hi(z2), dot = f2_lo(dot2) + f2_hi(dot2);
 #pragma unroll
@@ -332,8 +347,7 @@ __device__ __forceinline__ float2 row_sums(f32x2 (&s)[kNI][2], const f32x2 (&c)[
     z += __shfl_xor_sync(kFull, z, o);
     dot += __shfl_xor_sync(kFull, dot, o);
   }
-  *tiny = z < kTinySum;
-  if (*tiny) {
+  if (z < kTinySum) {
     ring.read(s, slot, E, lane);
     float m = -INFINITY;
 #pragma unroll
@@ -392,8 +406,7 @@ loss_kernel(const RouterBatch b, float alpha, const int32_t* __restrict__ counts
     f32x2 v[kNI][2];
     ring.wait_oldest();
     if (q.at(b, counts, tokens, t, lane)) {
-      bool tiny;
-      const float2 zd = row_sums<kNI, kVec>(v, q.c, ring, slot, b.E, lane, &tiny);
+      const float2 zd = row_sums<false, kNI, kVec>(v, q.c, ring, slot, b.E, lane);
       if (zd.x > 0.0f) add(q.part * (q.unit * zd.y / zd.x));
       else if (!(zd.x == 0.0f)) add(zd.x);          // NaN logits stay NaN
     }
@@ -500,8 +513,7 @@ small_loss_kernel(const RouterBatch b, float alpha, int32_t* __restrict__ counts
     f32x2 v[kNI][2];
     ring.wait_oldest();
     if (q.template at<true>(b, total, total + n, t, lane)) {
-      bool tiny;
-      const float2 zd = row_sums<kNI, kVec>(v, q.c, ring, slot, b.E, lane, &tiny);
+      const float2 zd = row_sums<false, kNI, kVec>(v, q.c, ring, slot, b.E, lane);
       if (zd.x > 0.0f) sum += q.part * (q.unit * zd.y / zd.x);
       else if (!(zd.x == 0.0f)) sum += zd.x;
     }
@@ -592,13 +604,12 @@ backward_kernel(const RouterBatch b, const BackwardArgs a) {
     }
     // 1. the balance loss's gradient: coef (c - mean) s (1 - s)
     float coef = 0.0f, mean = 0.0f;
-    bool tiny = false;
     if (a.grad_loss) {
       ring.wait_oldest();
       __syncwarp();                            // the whole row has landed
       if (id >= 0) l = *ring.place(slot, id, lane);
       if (q.at(b, a.counts, a.tokens, t, lane)) {
-        const float2 zd = row_sums<kNI, kVec>(v, q.c, ring, slot, b.E, lane, &tiny);
+        const float2 zd = row_sums<true, kNI, kVec>(v, q.c, ring, slot, b.E, lane);
         if (!(zd.x == 0.0f)) {
           coef = gl * q.part * q.unit / zd.x;
           mean = zd.y / zd.x;
@@ -608,7 +619,8 @@ backward_kernel(const RouterBatch b, const BackwardArgs a) {
     // 2. the weights' gradient: lane j puts the j-th chosen expert's in its place
     // of the slot, whose row has been used
     if (a.grad_w) {
-      const float s = sigmoid_f(l);
+      const float2 sc = sigmoid_f(l);          // s, 1 - s
+      const float s = sc.x;
       float d = a.rsf * g * s;
       if (a.renorm) {
         float p = s, z = warp_sum(s);
@@ -623,12 +635,11 @@ backward_kernel(const RouterBatch b, const BackwardArgs a) {
       __syncwarp();                            // every lane has its logit
       ring.clear(slot);
       __syncwarp();
-      if (id >= 0) *ring.place(slot, id, lane) = d * (1.0f - s);
+      if (id >= 0) *ring.place(slot, id, lane) = d * sc.y;
       __syncwarp();
     }
-    // coef (c - mean) s (1 - s), with 1 - s = 1 where the row holds exponentials
+    // coef (c - mean) s (1 - s)
     const f32x2 scale = f2_splat(coef), shift = f2_splat(-coef * mean);
-    const f32x2 minus = f2_splat(tiny ? 0.0f : -1.0f);
 #pragma unroll
     for (int i = 0; i < kNI; ++i) {
       f32x2 o[2] = {0ull, 0ull};
@@ -639,10 +650,7 @@ backward_kernel(const RouterBatch b, const BackwardArgs a) {
       }
       if (coef != 0.0f) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const f32x2 s = v[i][j];
-          o[j] = f2_fma(f2_fma(q.c[i][j], scale, shift), f2_fma(f2_mul(s, minus), s, s), o[j]);
-        }
+        for (int j = 0; j < 2; ++j) o[j] = f2_fma(f2_fma(q.c[i][j], scale, shift), v[i][j], o[j]);
       }
       const float4 r = make_float4(f2_lo(o[0]), f2_hi(o[0]), f2_lo(o[1]), f2_hi(o[1]));
       if (kVec) {

@@ -279,3 +279,29 @@ def test_loss_of_many_tokens(T, S):
     lm.moe_balance_loss(l, ids, 0.25, loss, cnt, tok, ws, seq_offsets=cuts)
     assert int(tok.sum()) == T and torch.equal(cnt, tok)
     assert abs(float(loss) - 0.25) <= 0.25 * (2 * (3 + 8 + 1 / 32 + 5 + 2) + 2 + 8 + 32 + 8) * U
+
+
+@pytest.mark.parametrize("renorm", [0, 1])
+@pytest.mark.parametrize("parts", ["weights", "loss", "both"])
+@pytest.mark.parametrize("E", [8, 96, 257, 896])
+def test_gradient_of_confident_experts(E, parts, renorm):
+    # logits of 6 to 40 beside ordinary ones: s (1 - s) is exp(-l) there, and the bound has the
+    # factor 1 - s (1 / (1 + exp(l))) that the other tests' leaves out
+    g = np.random.default_rng(E)
+    T, k = 50, 4
+    l, ids, seq, m = batch(T, E, k, 3, 17, True)
+    high = g.random((T, E)) < 0.5
+    l[high] = g.uniform(6, 40, int(high.sum())).astype(np.float32)
+    l[:8] = np.linspace(6, 40, 8, dtype=np.float32)[:, None]          # whole rows of one logit
+    gw = g.standard_normal((T, k)).astype(np.float32) if parts != "loss" else None
+    gl = -1.5 if parts != "weights" else None
+    got = check_backward(l, ids, seq, m, gw, renorm, 2.5, gl, 0.5)
+    c, n = R.counts(ids, E, seq, m)
+    ref, mag = R.router_backward(l, ids, gw, renorm, 2.5, gl, c, n, 0.5, seq, m)
+    l64 = l.astype(np.float64)
+    # (the reference's own 1 - s, a difference of float64s, is 2^-53 off and as much of mag)
+    # backward_tolerance counts s, Z, the dot product and Z again; here 1 - s and the product too
+    tol = backward_tolerance(l, E, k) + (float(l.max()) + 8 + 2) * U
+    bound = (tol / (1.0 + np.exp(l64)) + 2.0 ** -52) * mag + 1e-37
+    assert np.all(np.abs(got - ref) <= bound), (float((np.abs(got - ref) / bound).max()),
+                                                np.argwhere(np.abs(got - ref) > bound)[:3])
