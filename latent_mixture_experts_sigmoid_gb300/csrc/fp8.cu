@@ -732,7 +732,7 @@ cudaError_t launch_form(const Fp8Gemm& g, int splits, cudaStream_t s) {
   p.feat = g.feat;
   p.nkb = fp8_blocks(g.K);
   p.groups = g.groups;
-  p.nfeat = kSitu ? g.feat / 2 / 128 : (g.feat + kBN - 1) / kBN;
+  p.nfeat = kSitu ? g.feat / 2 / 128 : ceil_div(g.feat, kBN);
   p.stages = kRingBytes / kStage;
   p.ws_rows = fp8_blocks(g.feat);
   p.rows = g.rows;
@@ -789,11 +789,11 @@ DenseForm dense_form(long long T, int N, int nkb, int nsm) {
   const double rows = T < BM ? (double)T : (double)BM;
   const auto waves = [](long long n, int slots) { return (double)((n + slots - 1) / slots); };
   DenseForm best{true, true, 1};
-  double least = waves((T + 255) / 256 * ((N + 255) / 256), nsm / 2) * (nkb * 900.0 + 5700) + kLaunch;
+  double least = waves((T + 255) / 256 * ceil_div(N, 256), nsm / 2) * (nkb * 900.0 + 5700) + kLaunch;
   for (int wide = 0; wide < 2; ++wide) {
     const int bn = wide ? 256 : 128;
     const double block = (wide ? 700 : 350) + 2.3 * rows;
-    const long long tiles = tok * ((N + bn - 1) / bn);
+    const long long tiles = tok * ceil_div(N, bn);
     for (int c = 1; c <= kMaxSplits && c <= nkb; c *= 2) {
       // clusters of four that fit at once: 32 of 152 / 4
       const int slots = c == 1 ? nsm : c == 2 ? nsm / 2 : nsm * 32 / 152;

@@ -227,7 +227,7 @@ fp8_stream_kernel(const __grid_constant__ CUtensorMap tmW, const __grid_constant
   if (kMode == kDense || (kMode == kGateUp && !p.beside)) pdl_wait();
   pdl_trigger();
   const int feats = kMode == kGateUp ? kRows / 2 : kRows;
-  const int nfb = kMode == kDense ? (p.feat + kRows - 1) / kRows : p.feat / kRows;
+  const int nfb = kMode == kDense ? (p.feat - 1) / kRows + 1 : p.feat / kRows;
   int units = nfb;
   if (kMode == kDense) units *= (p.rows + kTok - 1) / kTok;
   else units *= build_list<kThreads>(p, list, warp_sum);
@@ -499,7 +499,7 @@ cudaError_t launch_stream(const Fp8Gemm& g, cudaStream_t s) {
       cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
   if (e != cudaSuccess) return e;
   // units: feature blocks of the experts that may have rows, or of the token blocks
-  const long long blocks = (g.feat + kRows - 1) / kRows;
+  const long long blocks = ceil_div(g.feat, kRows);
   const long long units = blocks * (kMode == kDense ? (g.rows + kTok - 1) / kTok
                                                     : g.rows < g.groups ? g.rows : g.groups);
   const int grid = units < num_sms() ? (int)units : num_sms();

@@ -154,6 +154,33 @@ def test_linear_16_byte_alignment(T, N, K):
     np.testing.assert_array_equal(scales.cpu().numpy(), want_s)
 
 
+@pytest.mark.parametrize("T", [1, 17])
+def test_linear_most_features(T):
+    # N = 2^31 - 8, the most that the argument holds: a stream and a tensor-core form; all of the
+    # weights' rows but a few are zeros
+    N, K = 2 ** 31 - 8, 16
+    if torch.cuda.mem_get_info()[0] < 1.3 * (N * K + 2 * T * N) + (8 << 30):
+        pytest.skip("needs %d GB" % (1.3 * (N * K + 2 * T * N) / 2 ** 30 + 8))
+    from tests.gpu_util import host_bits
+    g = np.random.default_rng(T)
+    x, xs = codes_of(g, T, K, 1)
+    rows = np.array([0, 1, 130, 12345678, N // 2, N - 300, N - 129, N - 8, N - 1])
+    wr, _ = F.quantize(O.f64_to_bf16_bits(g.standard_normal((len(rows), K)) + 3), 1)
+    at = dev(rows)
+    w = torch.zeros((N, K), dtype=torch.uint8, device="cuda")
+    w[at] = dev(wr)
+    ws = torch.full((F.blocks(N), 1), 0.5, device="cuda")
+    out = torch.full((T, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    lm.lmoe_linear_fp8(dev(x), dev(xs), w, ws, out)
+    got = O.bf16_to_f64(host_bits(out[:, at]))
+    assert lm.lmoe_device_error() == 0
+    ref, mag = F.linear(x, xs, wr, np.full((1, 1), 0.5, np.float32))
+    assert_close(got, ref, mag, K)
+    assert [int(torch.count_nonzero(o)) for o in out] == [int(np.count_nonzero(r)) for r in got]
+    del w, ws, out
+    torch.cuda.empty_cache()
+
+
 def test_linear_every_code():
     # every finite e4m3 code as an operand, one product a row: exact but for the bf16 rounding
     from tests.gpu_util import host_bits
