@@ -29,7 +29,7 @@
  *     workspace.  The enqueued work can be captured in a CUDA graph.
  *   - On a validation error nothing is launched and a negative lmoe_status is
  *     returned.  A zero-sized problem (T == 0, N == 0, E == 0) returns LMOE_OK
- *     and launches nothing.
+ *     and launches nothing (moe_balance_loss sets its outputs to 0).
  *   - Weights (the members of lmoe_weights, the `w` of lmoe_linear and the
  *     e_score_correction_bias of moe_route) are read-only model parameters.
  *     Kernels launch with programmatic dependent launch and may start reading
@@ -458,7 +458,9 @@ int latent_moe_launch_count_fp8(const lmoe_dims* dims, int has_shared_expert);
 /* row are, the token adds 0.  NaN logits give a NaN loss.  Sums are fp32 in a */
 /* fixed order: repeated calls give the same bits.                           */
 /* Limits: those of moe_route on E and topk, T * topk <= 2^31 - 1,            */
-/* 1 <= S <= 65536, alpha finite.  T == 0 writes nothing.                     */
+/* 1 <= S <= 65536, alpha finite.  T == 0: loss, expert_counts and seq_tokens  */
+/* become 0 where they are memory of the current device; nothing else is      */
+/* looked at.                                                                 */
 /* ------------------------------------------------------------------------ */
 size_t moe_balance_loss_workspace_bytes(int T, int E, int S);
 int moe_balance_loss(const float* router_logits, const int32_t* topk_ids,

@@ -1291,7 +1291,19 @@ int moe_balance_loss(const float* router_logits, const int32_t* topk_ids,
                      void* workspace, size_t workspace_bytes, void* stream) {
   const int v = validate_router(T, E, topk, S, alpha);
   if (v != LMOE_OK) return v;
-  if (T == 0) return LMOE_OK;
+  if (T == 0) {
+    // an empty batch (a rank without tokens): 0, not what an earlier call left there
+    const struct {
+      void* p;
+      size_t bytes;
+    } outs[] = {{loss, sizeof(float)},
+                {expert_counts, (size_t)S * E * sizeof(int32_t)},
+                {seq_tokens, (size_t)S * sizeof(int32_t)}};
+    for (const auto& o : outs)
+      if (o.p && on_current_device({o.p}))
+        LMOE_TRY(cudaMemsetAsync(o.p, 0, o.bytes, (cudaStream_t)stream));
+    return LMOE_OK;
+  }
   if (!router_logits || !topk_ids || !loss || !expert_counts || !seq_tokens ||
       (!seq_offsets && S != 1))
     return LMOE_ERR_NULL;

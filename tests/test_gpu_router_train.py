@@ -305,3 +305,38 @@ def test_gradient_of_confident_experts(E, parts, renorm):
     bound = (tol / (1.0 + np.exp(l64)) + 2.0 ** -52) * mag + 1e-37
     assert np.all(np.abs(got - ref) <= bound), (float((np.abs(got - ref) / bound).max()),
                                                 np.argwhere(np.abs(got - ref) > bound)[:3])
+
+
+@pytest.mark.parametrize("S", [1, 3])
+def test_empty_batch(S):
+    # no tokens: loss and counts are 0, not what an earlier batch left there, on the call's stream
+    # and in a graph; the gradient has no element to write
+    E = 40
+    loss, lbuf = guarded((1,), torch.float32, -7.0)
+    cnt, cbuf = guarded((S, E), torch.int32, -7)
+    tok, tbuf = guarded((S,), torch.int32, -7)
+    l, ids = torch.empty((0, E), device="cuda"), torch.empty((0, 4), dtype=torch.int32, device="cuda")
+    seq = None if S == 1 else torch.zeros(S + 1, dtype=torch.int32, device="cuda")
+    ws = torch.empty(lm.moe_balance_loss_workspace_bytes(0, E, S), dtype=torch.uint8, device="cuda")
+    s = torch.cuda.Stream()
+    torch.cuda.synchronize()
+
+    def call():
+        lm.moe_balance_loss(l, ids, 0.25, loss, cnt, tok, ws, seq_offsets=seq, stream=s)
+
+    call()
+    s.synchronize()
+    g = torch.cuda.CUDAGraph()
+    for replay in (False, True):
+        if replay:
+            with torch.cuda.graph(g, stream=s):
+                call()
+            loss.fill_(-7), cnt.fill_(-7), tok.fill_(-7)
+            torch.cuda.synchronize()
+            g.replay()
+            torch.cuda.synchronize()
+        assert float(loss) == 0.0 and int(cnt.abs().sum()) == 0 and int(tok.abs().sum()) == 0
+        for b in (lbuf, cbuf, tbuf):
+            assert bool((b[-GUARD:] == -7).all())
+    lm.moe_router_backward(l, ids, torch.empty((0, E), device="cuda"), grad_loss=torch.ones(1, device="cuda"),
+                           expert_counts=cnt, seq_tokens=tok, alpha=0.25, seq_offsets=seq)
