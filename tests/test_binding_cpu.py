@@ -53,3 +53,17 @@ def test_weight_sizes_follow_the_dims():
     small = dataclasses.replace(d, inter=64)
     with pytest.raises(ValueError):
         lm.make_weights({"w13": torch.zeros(3, dtype=torch.bfloat16)}, small)
+
+
+def test_addresses_take_the_short_way(monkeypatch):
+    # raw addresses pass through at once: not by way of a failed tensor query and the checks
+    # that tell errors apart
+    from latent_mixture_experts_sigmoid_gb300 import _binding as b
+
+    def refuse(*a):
+        raise AssertionError("an address went the long way")
+
+    monkeypatch.setattr(b, "_dev_slow", refuse)
+    assert b._dev(4096, "x", torch.float32, 1) == 4096
+    assert b._dev(0, "x", (torch.bfloat16, torch.int16), 1) == 0
+    assert b._dev(None, "x", torch.float32, 1) is None
