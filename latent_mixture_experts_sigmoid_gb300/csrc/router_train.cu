@@ -675,11 +675,12 @@ backward_kernel(const RouterBatch b, const BackwardArgs a) {
 }
 
 // Tokens a warp takes and CTAs of the token kernels: two CTAs an SM at the most.
+constexpr int kCtasPerSm = 2;
 struct TokenGrid {
   int per_warp, ctas;
 };
 TokenGrid token_grid(int T) {
-  const long long warps = 2ll * num_sms() * kWarps;
+  const long long warps = (long long)kCtasPerSm * num_sms() * kWarps;
   TokenGrid g;
   g.per_warp = (int)((T + warps - 1) / warps);
   g.ctas = ceil_div(ceil_div(T, g.per_warp), kWarps);
@@ -722,9 +723,10 @@ cudaError_t launch_ring(void (*kernel)(KArgs...), int ctas, int ni, int cluster,
 
 }  // namespace
 
-// the ticket, then a partial sum per CTA of the loss kernel
+// the ticket, then a partial sum per CTA of the loss kernel: room for the most CTAs of any T,
+// so that the workspace of the largest batch serves smaller ones (their CTAs may be more)
 size_t balance_workspace_bytes(int T) {
-  const size_t n = 256 + (T > 0 ? (size_t)token_grid(T).ctas * 4 : 0);
+  const size_t n = 256 + (T > 0 ? (size_t)kCtasPerSm * num_sms() * 4 : 0);
   return (n + 255) & ~size_t(255);
 }
 

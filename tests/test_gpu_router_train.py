@@ -340,3 +340,16 @@ def test_empty_batch(S):
             assert bool((b[-GUARD:] == -7).all())
     lm.moe_router_backward(l, ids, torch.empty((0, E), device="cuda"), grad_loss=torch.ones(1, device="cuda"),
                            expert_counts=cnt, seq_tokens=tok, alpha=0.25, seq_offsets=seq)
+
+
+def test_workspace_of_a_larger_batch():
+    # one workspace for a batch of 5000 tokens, then smaller ones with more CTAs and with fewer
+    E, k, big = 96, 4, 5000
+    ws = torch.empty(lm.moe_balance_loss_workspace_bytes(big, E, 1), dtype=torch.uint8, device="cuda")
+    for T in (big, 4864, 3000, 2433, 2432, 300, 256, 5):
+        l, ids, _, m = batch(T, E, k, 1, T, True)
+        want, _, _ = run_loss(l, ids, None, m, 0.25)
+        loss, cnt = torch.empty(1, device="cuda"), torch.empty((1, E), dtype=torch.int32, device="cuda")
+        tok = torch.empty(1, dtype=torch.int32, device="cuda")
+        lm.moe_balance_loss(dev(l), dev(ids), 0.25, loss, cnt, tok, ws, token_mask=dev(m))
+        assert torch.equal(loss, want)

@@ -1,0 +1,25 @@
+"""Workspace sizes never fall as a batch grows: a buffer for the largest batch serves every
+smaller one."""
+import pytest
+
+lm = pytest.importorskip("latent_mixture_experts_sigmoid_gb300")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib():
+    from latent_mixture_experts_sigmoid_gb300 import build
+    build.build()
+    lm.load_library()
+
+
+def assert_rising(sizes):
+    falls = [(n, a, b) for (_, a), (n, b) in zip(sizes[:-1], sizes[1:]) if b < a]
+    assert not falls, falls[:5]
+
+
+LARGE = [3000, 4096, 9999, 16384, 65536, 1 << 20, 1 << 24]
+
+
+@pytest.mark.parametrize("E,S", [(1, 1), (64, 4), (896, 40)])
+def test_balance_loss(E, S):
+    assert_rising([(T, lm.moe_balance_loss_workspace_bytes(T, E, S)) for T in [*range(0, 8000), *LARGE]])
