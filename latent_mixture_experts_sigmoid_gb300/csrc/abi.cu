@@ -562,16 +562,24 @@ cudaError_t experts_fp8(const lmoe_fp8_experts& w, const uint8_t* x, const float
   return cudaSuccess;
 }
 
-// Workspace of lmoe_experts_fp8 (base NULL: its size).
-size_t carve_fp8_act(long long rows, int d, const Fp8Plan& plan, char* base, Fp8Act* act) {
+// Workspace of lmoe_experts_fp8 (base NULL: its size).  Whatever the call's own plan, the fp32
+// values have room for the most rows, up to `rows`, of a call with light experts (the calls with
+// heavy ones are those of more rows): the size does not fall as the rows grow, and the
+// workspace of the largest call serves smaller ones.
+size_t carve_fp8_act(long long rows, int E, int d, char* base, Fp8Act* act) {
   Carver c;
   c.base = base;
   Fp8Act a{};
-  if (plan.heavy) {
+  if (fp8_plan(rows, E, rows).heavy) {
     a.codes = c.take<uint8_t>((size_t)rows * d);
     a.scales = c.take<float>((size_t)rows * (d / kFp8Block));
   }
-  if (plan.light) a.values = c.take<float>((size_t)rows * d);
+  long long light = 0;
+  for (long long hi = rows; light < hi;) {
+    const long long mid = light + (hi - light + 1) / 2;
+    if (fp8_plan(mid, E, mid).light) light = mid; else hi = mid - 1;
+  }
+  a.values = c.take<float>((size_t)light * d);
   if (act) *act = a;
   return ((c.off + 255) & ~size_t(255)) + 256;
 }
@@ -1229,7 +1237,7 @@ size_t lmoe_experts_fp8_workspace_bytes(int64_t rows, int E, int latent, int int
   if (rows < 0 || rows > kMaxFp8Rows || E < 1 || E > 1024 || latent <= 0 || latent % kFp8Block ||
       latent > kMaxFp8Dim || inter <= 0 || inter % kFp8Block || inter > kMaxFp8Dim)
     return 0;
-  return carve_fp8_act(rows, inter, fp8_plan(rows, E, rows), nullptr, nullptr);
+  return carve_fp8_act(rows, E, inter, nullptr, nullptr);
 }
 
 int lmoe_experts_fp8(const lmoe_fp8_experts* experts, const uint8_t* x, const float* xs,
@@ -1253,7 +1261,7 @@ int lmoe_experts_fp8(const lmoe_fp8_experts* experts, const uint8_t* x, const fl
     return LMOE_ERR_DEVICE;
   const Fp8Plan plan = fp8_plan(rows, E, rows);
   Fp8Act act;
-  carve_fp8_act(rows, inter, plan, static_cast<char*>(workspace), &act);
+  carve_fp8_act(rows, E, inter, static_cast<char*>(workspace), &act);
   for (int stage = 1; stage <= 2; ++stage)
     LMOE_TRY(experts_fp8(*experts, x, xs, expert_offsets, act, y, rows, E, latent, inter, beta,
                          linear_beta, plan, stage, (cudaStream_t)stream));

@@ -357,6 +357,31 @@ def test_experts_rows_outside_stay_untouched():
         np.testing.assert_array_equal(got, want)
 
 
+@pytest.mark.parametrize("E,sizes", [(300, (1000, 400, 151, 150, 129, 128, 40, 1)),
+                                     (16, (400, 129, 128, 9, 8)), (2, (300, 17, 16, 8))])
+def test_experts_in_the_workspace_of_a_larger_call(E, sizes):
+    # one workspace, of the largest call, over the changes of kernel from call to call
+    L = d = 128
+    g = np.random.default_rng(E)
+    Q = expert_weights(g, E, L, d)
+    qd = {k: dev(v) for k, v in Q.items()}
+    ws = torch.empty(lm.lmoe_experts_fp8_workspace_bytes(sizes[0], E, L, d), dtype=torch.uint8, device="cuda")
+    for R in sizes:
+        off = np.concatenate([[0], np.cumsum(np.bincount(g.integers(0, E, R), minlength=E))]).astype(np.int32)
+        x, xs = codes_of(g, R, L, 1)
+        got = []
+        for w in (ws, torch.empty(lm.lmoe_experts_fp8_workspace_bytes(R, E, L, d), dtype=torch.uint8, device="cuda")):
+            y, buf = guarded((R, L), torch.bfloat16, 7.0)
+            lm.lmoe_experts_fp8(qd, dev(x), dev(xs), dev(off), y, w, inter=d, beta=BETA, linear_beta=LBETA)
+            assert bool((buf[-GUARD:] == 7.0).all())
+            got.append(y)
+        assert torch.equal(got[0], got[1])
+        yr, _, _ = F.experts(x, xs, off, Q, d, BETA, LBETA)
+        y = got[0].double().cpu().numpy()
+        # (a code of the activations may round the other way: a step of 2^-3 of one of 128 terms)
+        assert np.linalg.norm(y - yr) <= 0.02 * np.linalg.norm(yr)
+
+
 # --- the layer --------------------------------------------------------------------
 
 

@@ -23,3 +23,10 @@ LARGE = [3000, 4096, 9999, 16384, 65536, 1 << 20, 1 << 24]
 @pytest.mark.parametrize("E,S", [(1, 1), (64, 4), (896, 40)])
 def test_balance_loss(E, S):
     assert_rising([(T, lm.moe_balance_loss_workspace_bytes(T, E, S)) for T in [*range(0, 8000), *LARGE]])
+
+
+@pytest.mark.parametrize("inter", [128, 512])
+@pytest.mark.parametrize("E", [1, 2, 7, 8, 15, 16, 17, 64, 255, 256, 257, 300, 896, 1024])
+def test_experts_fp8(E, inter):
+    counts = sorted({*range(0, 2500), 8 * E, 8 * E + 1, *LARGE, 1 << 27})
+    assert_rising([(n, lm.lmoe_experts_fp8_workspace_bytes(n, E, 256, inter)) for n in counts])
