@@ -424,8 +424,12 @@ int lmoe_experts_fp8(const lmoe_fp8_experts* experts, const uint8_t* x, const fl
 /* The layer forward with e4m3 routed experts: latent_moe_forward with        */
 /* weights->w13 and weights->w2 unused (may be NULL), the expert-major rows   */
 /* of Z quantised per 128 columns and the experts run as lmoe_experts_fp8.   */
-/* Everything else, the workspace offsets among it, is latent_moe_forward's  */
-/* (entries A, G and act of the workspace hold no data above 128 tokens).    */
+/* Everything else, the workspace offsets among it, is latent_moe_forward's, */
+/* but entries G and act of the workspace hold the experts' own activations  */
+/* and not bf16, as A does above 128 tokens.  The workspace's size does not  */
+/* fall as T grows: that of the largest batch serves smaller ones (the size  */
+/* of latent_moe_forward's and latent_moe_forward_mxfp4's falls from 128 to   */
+/* 129 tokens, behind which it has no split-K partials).                       */
 /* Limits: those of latent_moe_forward, inter % 128 == 0, inter <= 8192 and   */
 /* T * topk <= 2^27.  The four expert pointers are required (LMOE_ERR_NULL),  */
 /* 16-byte aligned (LMOE_ERR_ALIGN) device memory (LMOE_ERR_DEVICE).         */

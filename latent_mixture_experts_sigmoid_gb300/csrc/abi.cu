@@ -139,7 +139,8 @@ struct Ws {
   // MXFP4 forward at decode sizes with heavy slots: the light experts' list
   // and count, the heavy slots' group tables
   int32_t *light, *n_light, *h_expert, *h_count, *h_offset, *h_prefix;
-  // e4m3 forward: expert-major rows and activations, codes and scales
+  // e4m3 forward: expert-major rows and activations, codes and scales (mostly in the
+  // room of A, G and act)
   uint8_t *A8, *act8;
   float *A8s, *act8s, *act8f;
 };
@@ -247,15 +248,35 @@ size_t carve(const lmoe_dims& d, char* base, Ws* ws, Experts form = Experts::kBf
     w.Wd13 = w.Wd2 = nullptr;
   }
   if (form == Experts::kFp8) {
-    w.A8 = c.take<uint8_t>(T * k * L);
-    w.A8s = c.take<float>(T * k * (L / kFp8Block));
-    const Fp8Plan fp = fp8_plan((long long)(T * k), d.num_experts, d.T);
-    w.act8 = fp.heavy ? c.take<uint8_t>(T * k * dI) : nullptr;
-    w.act8s = fp.heavy ? c.take<float>(T * k * (dI / kFp8Block)) : nullptr;
-    w.act8f = fp.light ? c.take<float>(T * k * dI) : nullptr;
+    // The activations take the room of the bf16 forward's, which this one does not write: fp32
+    // values that of G (4 bytes a feature both), codes and scales that of act (1 + 1/32 of 2).
+    // So do, above decode sizes, the expert-major rows that of A; at decode sizes A holds
+    // the rows that they are quantised from.
+    static_assert(kFp8Block * 1 + sizeof(float) <= kFp8Block * sizeof(uint16_t), "codes, scale <= bf16");
+    if (d.T <= kDecodeMaxT) {
+      w.A8 = c.take<uint8_t>(T * k * L);
+      w.A8s = c.take<float>(T * k * (L / kFp8Block));
+    } else if (base) {
+      w.A8 = reinterpret_cast<uint8_t*>(w.A);
+      w.A8s = reinterpret_cast<float*>(w.A8 + T * k * L);
+    }
+    if (base) {
+      w.act8f = reinterpret_cast<float*>(w.G);
+      w.act8 = reinterpret_cast<uint8_t*>(w.act);
+      w.act8s = reinterpret_cast<float*>(w.act8 + T * k * dI);
+    }
   }
   if (ws) *ws = w;
-  return (c.off + 255) & ~size_t(255);
+  size_t bytes = (c.off + 255) & ~size_t(255);
+  if (form == Experts::kFp8 && d.T > kDecodeMaxT) {
+    // no less than at decode sizes with their split-K partials: the workspace of the largest
+    // batch serves smaller ones
+    lmoe_dims small = d;
+    small.T = kDecodeMaxT;
+    const size_t least = carve(small, nullptr, nullptr, form);
+    if (least > bytes) bytes = least;
+  }
+  return bytes;
 }
 
 int validate_dims(const lmoe_dims* d) {

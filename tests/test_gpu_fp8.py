@@ -472,3 +472,28 @@ def test_layer_in_a_graph_and_launch_count():
         g.replay()
         torch.cuda.synchronize()
         np.testing.assert_array_equal(host_bits(out), want)
+
+
+@pytest.mark.parametrize("E,topk", [(64, 4), (896, 4), (8, 8)])
+def test_layer_in_the_workspace_of_a_larger_batch(E, topk):
+    # one workspace, of the largest batch, against one of the batch's own size, over the changes
+    # between the decode form, the streaming and the tensor-core kernels
+    from tests.gpu_util import DEV, weights_to_device, dev_bf16, dev_f32
+    base = dataclasses.replace(W.TINY, T=400, num_experts=E, topk=topk)
+    wts = W.layer_weights(base, E)
+    q = {k: dev(v) for k, v in quantized_experts(wts).items()}
+    wdev = weights_to_device(dict(wts, w13=None, w2=None))
+    ws = torch.full((lm.latent_moe_workspace_bytes_fp8(base),), 0xFF, dtype=torch.uint8, device=DEV)
+    torch.cuda.synchronize()
+    for T in (400, 129, 128, 112, 33, 32, 9, 1, 300):
+        d = dataclasses.replace(base, T=T)
+        x, lg = dev_bf16(W.hidden_states(d, T)), dev_f32(W.router_logits(T, E, T))
+        got = []
+        for w in (ws, torch.full((lm.latent_moe_workspace_bytes_fp8(d),), 0xFF, dtype=torch.uint8, device=DEV)):
+            out, buf = guarded((T, d.hidden), torch.bfloat16, 7.0)
+            n = w.numel()
+            lm.latent_moe_forward_fp8(d, wdev, q, x, lg, out, w, workspace_bytes=n)
+            assert bool((buf[-GUARD:] == 7.0).all())
+            got.append(out)
+        assert lm.lmoe_device_error() == 0
+        assert torch.equal(got[0], got[1]) and bool(torch.isfinite(got[0].float()).all())

@@ -1,6 +1,10 @@
 """Workspace sizes never fall as a batch grows: a buffer for the largest batch serves every
 smaller one."""
+import dataclasses
+
 import pytest
+
+import workloads as W
 
 lm = pytest.importorskip("latent_mixture_experts_sigmoid_gb300")
 
@@ -30,3 +34,15 @@ def test_balance_loss(E, S):
 def test_experts_fp8(E, inter):
     counts = sorted({*range(0, 2500), 8 * E, 8 * E + 1, *LARGE, 1 << 27})
     assert_rising([(n, lm.lmoe_experts_fp8_workspace_bytes(n, E, 256, inter)) for n in counts])
+
+
+@pytest.mark.parametrize("E,topk", [(64, 4), (896, 16), (896, 1), (8, 8), (1024, 4)])
+def test_layer_fp8(E, topk):
+    sizes = []
+    for T in [*range(0, 1200), 2048, 4096, 8192]:
+        d = dataclasses.replace(W.TINY, T=T, num_experts=E, topk=topk)
+        sizes.append((T, lm.latent_moe_workspace_bytes_fp8(d)))
+        # above decode sizes the e4m3 rows and activations have the room of the bf16 ones
+        if T > 128:
+            assert sizes[-1][1] == max(lm.latent_moe_workspace_bytes(d), sizes[128][1])
+    assert_rising(sizes)
