@@ -28,3 +28,16 @@ def test_example_trains_the_router(cuda_ok):
     # alpha is the loss of an even load; without its gradient the load drifts apart
     free, _, _ = _main(steps=12, alpha=0.0)
     assert history[-1][2] <= free[-1][2] and losses[0] > 0
+
+
+def test_example_balances_the_load(cuda_ok):
+    # the loss over alpha is 1 for an even load and more for any other.  A run whose alpha is too
+    # small to act measures the same loss: its load drifts apart, while the balance gradient's
+    # does not.  Without that gradient both runs would be the same but for rounding.
+    small = 2.0 ** -20
+    held, free = _main(steps=12, alpha=0.2)[0], _main(steps=12, alpha=small)[0]
+    first, last, drifted = held[0][1] / 0.2 - 1, held[-1][1] / 0.2 - 1, free[-1][1] / small - 1
+    assert abs(first - (free[0][1] / small - 1)) <= 2.0 ** -20      # the same first step
+    assert drifted > 1.2 * first > 0
+    assert last < 0.8 * drifted
+    assert held[-1][2] < free[-1][2]
