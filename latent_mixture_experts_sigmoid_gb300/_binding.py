@@ -199,7 +199,7 @@ def _dev(t, name: str, dtypes, numel: int) -> int | None:
     access it as the C ABI describes: a contiguous tensor on the current CUDA
     device, of one of `dtypes`, holding at least `numel` elements.  None and raw
     integer addresses pass through unchecked (the caller vouches for them)."""
-    if t is None or isinstance(t, int):
+    if t is None or type(t) is int:
         return t
     try:
         # one pass of cheap queries; whatever fails it is told apart below
@@ -213,6 +213,8 @@ def _dev(t, name: str, dtypes, numel: int) -> int | None:
 
 def _dev_slow(t, name: str, dtypes, numel: int) -> int:
     """_dev's checks one by one, for the error that names what is wrong."""
+    if isinstance(t, int):
+        return t
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name}: expected a torch tensor, an address or None")
     if not t.is_cuda:
