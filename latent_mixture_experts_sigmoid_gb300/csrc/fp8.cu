@@ -17,7 +17,6 @@
 // is one scalar per thread and 128 columns.
 #include <cuda.h>
 
-#include <mutex>
 #include <type_traits>
 
 #include "fp8.cuh"
@@ -186,8 +185,8 @@ quantize_scatter_kernel(const uint16_t* __restrict__ Z, const int32_t* __restric
 // The wide tile (kNH = 2) halves the token bytes a product reads and the barriers.  SituGLU,
 // four special functions an output, costs a tile another 4500 cycles, in which the tensor core
 // runs two K blocks ahead and the ring fills.
-// 65536 rows over 896 experts, latent 2048, inter 512: first product 362 us (1.84 GB, 5.1 TB/s),
-// second 198 us (1.13 GB, 5.7 TB/s).
+// 65536 rows over 806 of 896 experts, latent 2048, inter 512: first product 362 us (1.84 GB,
+// 5.1 TB/s), second 198 us (1.13 GB, 5.7 TB/s).
 // Every wait is bounded: on expiry the code goes to the device error word, the
 // CTA drains its copies and MMAs, frees its TMEM and returns.
 // ---------------------------------------------------------------------------

@@ -18,11 +18,13 @@
 // bring them (lane c of a row's four has bytes 16 c .. 16 c + 15 of each half): the
 // same for both operands, so it drops out of the sum.
 //
-// Bound by the weights' bytes once there are enough of them: 128 rows over 103 of 896 experts,
-// latent 2048, inter 512, both products 57.8 us (379 MB, 6.6 TB/s).  A dense product of a few
-// microseconds is its launch, one memory latency and its bytes: [1, 7168] x [2048, 7168] 4.8 us
-// (14.7 MB, 2.2 us at full rate), 9.5 on the tensor-core kernel with its K split four ways;
-// [8, 7168] x [8192, 7168] 13.7 us (58.8 MB, 4.3 TB/s), 15.4 there.
+// Bound by the weights' bytes once there are enough of them: 128 rows over 96 of 896 experts
+// (the mean of four batches), latent 2048, inter 512, both products 55.5 us (303 MB, 5.5 TB/s;
+// 45 us at the copy bandwidth, the rest is mostly the two launches' ends and first loads).  A
+// dense product of a few microseconds is its launch, one memory latency and its bytes:
+// [1, 7168] x [2048, 7168] 5.5 us, 5.0 with its weights in L2 (14.7 MB, 2.2 us at full rate), 9.5
+// on the tensor-core kernel with its K split four ways; [8, 7168] x [8192, 7168] 13.7 us
+// (58.8 MB, 4.3 TB/s), 15.4 there.
 #include <cuda.h>
 
 #include "fp8.cuh"

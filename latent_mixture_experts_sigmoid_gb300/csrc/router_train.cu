@@ -19,11 +19,11 @@
 // sequence's counts stay in registers from token to token.  Every sum has a
 // fixed order, so results repeat to the bit (the counts are sums of integers).
 //
-// 16384 tokens, 896 experts, 16 choices, 4 sequences: loss 19 us (60 MB, 8.8 us at full
+// 16384 tokens, 896 experts, 16 choices, 4 sequences: loss 19.4 us (60 MB, 8.8 us at full
 // rate), of which the counts, which the token pass must have first, take about 5; gradient
-// 24 us (120 MB, 4.9 TB/s).  What bounds the token kernels is not the bandwidth but the
-// instructions and latencies of a row on its warp, 16 warps an SM (gradient: 1.8
-// instructions a cycle, some 650 a token; 24 warps with fewer registers each were slower).
+// 24.3 us (120 MB, 4.9 TB/s).  What bounds the token kernels is not the bandwidth but the
+// latencies of a row on its warp, 16 warps an SM (gradient: 685 instructions a token, 1.95
+// of 4 a cycle; 24 warps with fewer registers each were slower).
 // 256 tokens of 64 experts: loss 5 us, gradient 2.9 us, launches and one chain of latencies.
 #include "lmoe_internal.cuh"
 #include "router_train.cuh"
@@ -182,7 +182,7 @@ __device__ __forceinline__ int expert_of(int i, int j, int lane) {
 // Every lane copies and reads its own experts only, so that its own copies'
 // completion is all there is to wait for.  kSlots rows are on their way per warp:
 // 16 warps an SM and a latency of about 1.5 us need two rows each at full
-// bandwidth (16384 x 896: two slots 24.2 us for the gradient, three 24.9, four 25.7; with a
+// bandwidth (16384 x 896: two slots 24.3 us for the gradient, three 24.8, four 25.6; with a
 // row ahead in registers instead 37).
 constexpr int kSlots = 2;
 

@@ -53,15 +53,15 @@ __device__ __forceinline__ bool mbar_try_wait_ns(uint32_t bar, uint32_t parity, 
   return ok != 0;
 }
 
-// 32 bytes (32-byte aligned) as one store: a whole sector.  Where a warp's lanes write a row
-// each, a store costs its 32 lines whatever its width.
-// 32 bytes at once, 32-byte aligned
+// 32 bytes (32-byte aligned) at once
 __device__ __forceinline__ void ld_global32(const void* p, uint32_t (&w)[8]) {
   asm volatile("ld.global.v8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]),
                  "=r"(w[7])
                : "l"(p));
 }
+// ... as one store: a whole sector.  Where a warp's lanes write a row each, a store costs its 32
+// lines whatever its width.
 __device__ __forceinline__ void st_global32(void* p, const uint32_t (&w)[8]) {
   asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]),
                "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
@@ -185,8 +185,6 @@ __device__ __forceinline__ void tmem_ld64(uint32_t taddr, uint32_t (&r)[64]) {
       : "r"(taddr));
 }
 
-// Waits for this thread's TMEM loads.  The registers pass through the wait, so
-// that no use of them can be scheduled ahead of it.
 // Waits for this thread's TMEM loads.  The registers pass through the wait, so
 // that no use of them can be scheduled ahead of it.
 __device__ __forceinline__ void tmem_wait_ld64(uint32_t (&r)[64]) {
