@@ -414,7 +414,8 @@ typedef struct lmoe_fp8_experts {
 /* inter % 128 == 0, latent and inter <= 8192, 0 <= rows <= 2^27.             */
 /* The workspace (lmoe_experts_fp8_workspace_bytes, 256-byte aligned) holds  */
 /* act (of experts with few rows in fp32: their second product quantises     */
-/* it).  Weights, scales and offsets are read in stream order.     */
+/* it); its size does not fall as rows grow: that of the largest call serves */
+/* smaller ones.  Weights, scales and offsets are read in stream order.       */
 size_t lmoe_experts_fp8_workspace_bytes(int64_t rows, int E, int latent, int inter);
 int lmoe_experts_fp8(const lmoe_fp8_experts* experts, const uint8_t* x, const float* xs,
                      const int32_t* expert_offsets, lmoe_bf16* y, int64_t rows, int E, int latent,
@@ -464,7 +465,7 @@ int latent_moe_launch_count_fp8(const lmoe_dims* dims, int has_shared_expert);
 /* Limits: those of moe_route on E and topk, T * topk <= 2^31 - 1,            */
 /* 1 <= S <= 65536, alpha finite.  T == 0: loss, expert_counts and seq_tokens  */
 /* become 0 where they are memory of the current device; nothing else is      */
-/* looked at.                                                                 */
+/* looked at.  The workspace's size does not fall as T grows.                 */
 /* ------------------------------------------------------------------------ */
 size_t moe_balance_loss_workspace_bytes(int T, int E, int S);
 int moe_balance_loss(const float* router_logits, const int32_t* topk_ids,
