@@ -29,7 +29,9 @@
  *     workspace.  The enqueued work can be captured in a CUDA graph.
  *   - On a validation error nothing is launched and a negative lmoe_status is
  *     returned.  A zero-sized problem (T == 0, N == 0, E == 0) returns LMOE_OK
- *     and launches nothing (moe_balance_loss sets its outputs to 0).
+ *     and launches nothing (moe_balance_loss and the weight gradients of
+ *     lmoe_rms_norm_backward and lmoe_grouped_linear_backward_w set their
+ *     outputs).
  *   - Weights (the members of lmoe_weights, the `w` of lmoe_linear and the
  *     e_score_correction_bias of moe_route) are read-only model parameters.
  *     Kernels launch with programmatic dependent launch and may start reading
@@ -493,6 +495,89 @@ int moe_router_backward(const float* router_logits, const int32_t* topk_ids,
                         const int32_t* expert_counts, const int32_t* seq_tokens, float alpha,
                         const uint8_t* token_mask, const int32_t* seq_offsets, int T, int E,
                         int topk, int S, float* grad_logits, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* Residual addition and RMSNorm in front of the layer, in one pass.          */
+/*                                                                            */
+/*   h[t,:]   = x[t,:] + residual[t,:]      (fp32; residual NULL: h = x)       */
+/*   y[t,:]   = h[t,:] / sqrt(mean(h[t,:]^2) + rms_eps) * norm_w   (fp32)      */
+/*   residual_out = bf16(h)  if not NULL;   out = bf16(y)  if not NULL         */
+/*   codes, scales = the rule of lmoe_quantize_fp8 (block_rows = 1) on y, if   */
+/*                   not NULL: the token rows of lmoe_linear_fp8 and           */
+/*                   lmoe_experts_fp8                                          */
+/* x, residual, residual_out, out [T, H] bf16; norm_w [H] bf16 or NULL (ones); */
+/* codes [T, H] e4m3, scales [T, ceil(H/128)] fp32, both or neither.  At least */
+/* one of out and codes (LMOE_ERR_NULL).  y is taken from the unrounded h and  */
+/* rounded once in each of its outputs.  residual_out and out may be x or      */
+/* residual (in place); otherwise outputs do not overlap anything.  Squares    */
+/* that leave the range of fp32 are handled (the row is scaled first); an      */
+/* infinity or NaN in a row stays in its row: 0 beside infinities, NaN in      */
+/* their place, and NaN throughout beside a NaN.  With rms_eps = 0 a row of    */
+/* zeros is NaN.                                                              */
+/* Requires 8 <= H <= 16384, H % 8 == 0 (H % 16 == 0 with codes), T >= 0,      */
+/* rms_eps finite and >= 0 (LMOE_ERR_DIM).  norm_w is read in stream order.    */
+/* ------------------------------------------------------------------------ */
+int lmoe_rms_norm(const lmoe_bf16* x, const lmoe_bf16* residual, const lmoe_bf16* norm_w,
+                  float rms_eps, lmoe_bf16* residual_out, lmoe_bf16* out, uint8_t* codes,
+                  float* scales, int T, int H, void* stream);
+
+/* Its gradient, from the h that the forward left in residual_out (or x):     */
+/*   r = 1 / sqrt(mean(h^2) + rms_eps);  n = h r;  g = grad_out * norm_w       */
+/*   grad_h      = bf16( grad_residual + r (g - n mean(g n)) )                */
+/*                 (of x and of residual alike)                               */
+/*   grad_norm_w = sum over t of grad_out[t,:] n[t,:]       (fp32)             */
+/* grad_out (of out; of the codes' values where those were used), h, grad_h    */
+/* [T, H] bf16; grad_residual [T, H] bf16 (the gradient that reaches           */
+/* residual_out from elsewhere) or NULL (zeros); grad_norm_w [H] fp32 or NULL  */
+/* (not computed; no workspace is needed then).  grad_h may be grad_out, h or  */
+/* grad_residual.  Sums are fp32 in a fixed order: repeated calls give the     */
+/* same bits.  Limits of lmoe_rms_norm; H % 8 == 0.  T == 0: grad_norm_w       */
+/* becomes 0 where it is memory of the current device.  The workspace          */
+/* (256-byte aligned) does not fall as T grows.                               */
+size_t lmoe_rms_norm_backward_workspace_bytes(int T, int H);
+int lmoe_rms_norm_backward(const lmoe_bf16* grad_out, const lmoe_bf16* h, const lmoe_bf16* norm_w,
+                           const lmoe_bf16* grad_residual, float rms_eps, lmoe_bf16* grad_h,
+                           float* grad_norm_w, int T, int H, void* workspace,
+                           size_t workspace_bytes, void* stream);
+
+/* The gradient of situ_and_mul: grad_in [N, 2d] of in [N, 2d] and grad_out   */
+/* [N, d], all bf16 (grad_in may be in).  Requires d % 8 == 0, N * d <= 2^40;  */
+/* beta <= 0 -> LMOE_ERR_BETA.                                                */
+int situ_and_mul_backward(const lmoe_bf16* in, const lmoe_bf16* grad_out, lmoe_bf16* grad_in,
+                          int64_t N, int d, float beta, float linear_beta, void* stream);
+
+/* ------------------------------------------------------------------------ */
+/* bf16 products of token rows grouped by expert, and their gradients.        */
+/*                                                                            */
+/* Expert e owns rows expert_offsets[e] .. expert_offsets[e+1] - 1 of the row  */
+/* matrices; expert_offsets [E+1] int32 on the device, ascending, within       */
+/* [0, rows] (entries outside are clamped on the device).  A row that no       */
+/* expert owns is neither read nor written.  w, grad_w [E, N, K] (lmoe_weights */
+/* w13: N = 2 inter, K = latent; w2: N = latent, K = inter).                   */
+/*   lmoe_grouped_linear:            out[r,:]    = bf16( W_e x[r,:] )          */
+/*   lmoe_grouped_linear_backward_x: grad_x[r,:] = bf16( W_e^T grad_out[r,:] ) */
+/*   lmoe_grouped_linear_backward_w: grad_w[e]   = sum over the rows r of e of */
+/*                                   grad_out[r,:] x[r,:]^T  (+ add[e])        */
+/* x, grad_x [rows, K], out, grad_out [rows, N] and w bf16.  grad_w is fp32     */
+/* (grad_w) or bf16 (grad_w_bf16), one of them, the other NULL; add [E, N, K]  */
+/* fp32 or NULL, with grad_w only (LMOE_ERR_NULL otherwise), may be grad_w     */
+/* itself (a gradient summed over micro-batches).  Every element of grad_w is  */
+/* written, add or 0 for experts without rows (also with rows == 0).           */
+/* Products are summed on the tensor cores in fp32 and rounded once; repeated  */
+/* calls give the same bits.  A NaN or infinity in a row reaches that row of   */
+/* out and grad_x, and the gradients of its expert's weights, alone.           */
+/* Requires 1 <= E <= 1024, N % 8 == 0, K % 8 == 0, 8 <= N, K <= 65536,         */
+/* 0 <= rows <= 2^27.  No workspace.  Everything is read in stream order.      */
+/* ------------------------------------------------------------------------ */
+int lmoe_grouped_linear(const lmoe_bf16* x, const lmoe_bf16* w, const int32_t* expert_offsets,
+                        lmoe_bf16* out, int64_t rows, int E, int N, int K, void* stream);
+int lmoe_grouped_linear_backward_x(const lmoe_bf16* grad_out, const lmoe_bf16* w,
+                                   const int32_t* expert_offsets, lmoe_bf16* grad_x, int64_t rows,
+                                   int E, int N, int K, void* stream);
+int lmoe_grouped_linear_backward_w(const lmoe_bf16* grad_out, const lmoe_bf16* x,
+                                   const int32_t* expert_offsets, const float* add, float* grad_w,
+                                   lmoe_bf16* grad_w_bf16, int64_t rows, int E, int N, int K,
+                                   void* stream);
 
 /* The layer forward without a caller workspace.  The pages have no          */
 /* counterpart to this entry point; it exists for callers that cannot         */

@@ -15,5 +15,7 @@ from ._binding import (  # noqa: F401
     LmoeFp8Experts, make_fp8_experts, lmoe_quantize_fp8, lmoe_linear_fp8, lmoe_experts_fp8,
     lmoe_experts_fp8_workspace_bytes, latent_moe_workspace_bytes_fp8, latent_moe_forward_fp8,
     latent_moe_launch_count_fp8, moe_balance_loss, moe_balance_loss_workspace_bytes,
-    moe_router_backward,
+    moe_router_backward, lmoe_rms_norm, lmoe_rms_norm_backward,
+    lmoe_rms_norm_backward_workspace_bytes, situ_and_mul_backward, lmoe_grouped_linear,
+    lmoe_grouped_linear_backward_x, lmoe_grouped_linear_backward_w,
 )

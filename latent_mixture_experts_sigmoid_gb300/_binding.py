@@ -37,7 +37,10 @@ ABI_FUNCTIONS = ("moe_route", "situ_and_mul", "masked_situ_and_mul", "latent_moe
                  "lmoe_quantize_fp8", "lmoe_linear_fp8", "lmoe_experts_fp8",
                  "lmoe_experts_fp8_workspace_bytes", "latent_moe_workspace_bytes_fp8",
                  "latent_moe_forward_fp8", "latent_moe_launch_count_fp8",
-                 "moe_balance_loss", "moe_balance_loss_workspace_bytes", "moe_router_backward")
+                 "moe_balance_loss", "moe_balance_loss_workspace_bytes", "moe_router_backward",
+                 "lmoe_rms_norm", "lmoe_rms_norm_backward", "lmoe_rms_norm_backward_workspace_bytes",
+                 "situ_and_mul_backward", "lmoe_grouped_linear", "lmoe_grouped_linear_backward_x",
+                 "lmoe_grouped_linear_backward_w")
 
 
 class LmoeError(RuntimeError):
@@ -175,6 +178,19 @@ def load_library(path: str | None = None) -> ctypes.CDLL:
     lib.moe_router_backward.argtypes = [vp, vp, vp, i32, f32, vp, vp, vp, f32, vp, vp, i32, i32,
                                         i32, i32, vp, vp]
     lib.moe_router_backward.restype = i32
+    lib.lmoe_rms_norm.argtypes = [vp, vp, vp, f32, vp, vp, vp, vp, i32, i32, vp]
+    lib.lmoe_rms_norm.restype = i32
+    lib.lmoe_rms_norm_backward_workspace_bytes.argtypes = [i32, i32]
+    lib.lmoe_rms_norm_backward_workspace_bytes.restype = ctypes.c_size_t
+    lib.lmoe_rms_norm_backward.argtypes = [vp, vp, vp, vp, f32, vp, vp, i32, i32, vp, ctypes.c_size_t, vp]
+    lib.lmoe_rms_norm_backward.restype = i32
+    lib.situ_and_mul_backward.argtypes = [vp, vp, vp, i64, i32, f32, f32, vp]
+    lib.situ_and_mul_backward.restype = i32
+    for name in ("lmoe_grouped_linear", "lmoe_grouped_linear_backward_x"):
+        getattr(lib, name).argtypes = [vp, vp, vp, vp, i64, i32, i32, i32, vp]
+        getattr(lib, name).restype = i32
+    lib.lmoe_grouped_linear_backward_w.argtypes = [vp, vp, vp, vp, vp, vp, i64, i32, i32, i32, vp]
+    lib.lmoe_grouped_linear_backward_w.restype = i32
     _lib = lib
     return lib
 
@@ -730,3 +746,101 @@ def moe_router_backward(router_logits, topk_ids, grad_logits, grad_topk_weights=
         _dev(seq_tokens, "seq_tokens", torch.int32, S), float(alpha), mask, seq, T, E, k, S,
         _dev(grad_logits, "grad_logits", torch.float32, T * E), _stream(stream))
     _check(st, "moe_router_backward")
+
+
+# --- residual + RMSNorm ------------------------------------------------------------
+
+
+def lmoe_rms_norm(x, norm_w, rms_eps: float, out=None, codes=None, scales=None, residual=None,
+                  residual_out=None, stream=None, T: int | None = None, H: int | None = None):
+    """RMSNorm of h = x (+ residual) [T, H]: out bf16, e4m3 codes [T, H] with scales
+    [T, ceil(H/128)], residual_out = bf16(h); outputs that are None are not written (out or
+    codes is needed).  norm_w [H] bf16, None: ones."""
+    if T is None:
+        H = x.shape[-1]
+        T = x.numel() // H
+    T, H = int(T), int(H)
+    st = load_library().lmoe_rms_norm(
+        _dev(x, "x", _BF16, T * H), _dev(residual, "residual", _BF16, T * H),
+        _dev(norm_w, "norm_w", _BF16, H), float(rms_eps),
+        _dev(residual_out, "residual_out", _BF16, T * H), _dev(out, "out", _BF16, T * H),
+        _dev(codes, "codes", _E4M3, T * H), _dev(scales, "scales", torch.float32, T * _blocks(H)),
+        T, H, _stream(stream))
+    _check(st, "lmoe_rms_norm")
+
+
+def lmoe_rms_norm_backward_workspace_bytes(T: int, H: int) -> int:
+    return int(load_library().lmoe_rms_norm_backward_workspace_bytes(int(T), int(H)))
+
+
+def lmoe_rms_norm_backward(grad_out, h, norm_w, rms_eps: float, grad_h, grad_norm_w=None,
+                           grad_residual=None, workspace=None, stream=None, T: int | None = None,
+                           H: int | None = None):
+    """The gradient of lmoe_rms_norm: grad_h [T, H] bf16 (of x and residual alike, with
+    grad_residual added) and, unless None, grad_norm_w [H] fp32 (through the workspace)."""
+    if T is None:
+        H = h.shape[-1]
+        T = h.numel() // H
+    T, H = int(T), int(H)
+    wsp, wsn = _workspace(workspace, None)
+    st = load_library().lmoe_rms_norm_backward(
+        _dev(grad_out, "grad_out", _BF16, T * H), _dev(h, "h", _BF16, T * H),
+        _dev(norm_w, "norm_w", _BF16, H), _dev(grad_residual, "grad_residual", _BF16, T * H),
+        float(rms_eps), _dev(grad_h, "grad_h", _BF16, T * H),
+        _dev(grad_norm_w, "grad_norm_w", torch.float32, H), T, H, wsp, wsn, _stream(stream))
+    _check(st, "lmoe_rms_norm_backward")
+
+
+def situ_and_mul_backward(inp, grad_out, grad_in, beta: float, linear_beta: float, stream=None,
+                          N: int | None = None, d: int | None = None):
+    """The gradient of situ_and_mul: grad_in [N, 2d] of inp [N, 2d] and grad_out [N, d]."""
+    if N is None:
+        d = inp.shape[-1] // 2
+        N = inp.numel() // (2 * d)
+    N, d = int(N), int(d)
+    st = load_library().situ_and_mul_backward(
+        _dev(inp, "input", _BF16, N * 2 * d), _dev(grad_out, "grad_out", _BF16, N * d),
+        _dev(grad_in, "grad_in", _BF16, N * 2 * d), N, d, float(beta), float(linear_beta),
+        _stream(stream))
+    _check(st, "situ_and_mul_backward")
+
+
+# --- bf16 products grouped by expert -----------------------------------------------
+
+
+def lmoe_grouped_linear(x, w, expert_offsets, out, stream=None, shape: tuple | None = None):
+    """out [rows, N] = x [rows, K] @ w[e]^T for the rows of each expert e (expert_offsets[e] ..
+    expert_offsets[e+1]); w [E, N, K].  shape (rows, E, N, K) for raw addresses."""
+    R, E, N, K = (int(v) for v in (shape if shape is not None else (x.shape[0], *w.shape)))
+    st = load_library().lmoe_grouped_linear(
+        _dev(x, "x", _BF16, R * K), _dev(w, "w", _BF16, E * N * K),
+        _dev(expert_offsets, "expert_offsets", torch.int32, E + 1), _dev(out, "out", _BF16, R * N),
+        R, E, N, K, _stream(stream))
+    _check(st, "lmoe_grouped_linear")
+
+
+def lmoe_grouped_linear_backward_x(grad_out, w, expert_offsets, grad_x, stream=None,
+                                   shape: tuple | None = None):
+    """grad_x [rows, K] = grad_out [rows, N] @ w[e] for the rows of each expert e."""
+    R, E, N, K = (int(v) for v in (shape if shape is not None else (grad_out.shape[0], *w.shape)))
+    st = load_library().lmoe_grouped_linear_backward_x(
+        _dev(grad_out, "grad_out", _BF16, R * N), _dev(w, "w", _BF16, E * N * K),
+        _dev(expert_offsets, "expert_offsets", torch.int32, E + 1),
+        _dev(grad_x, "grad_x", _BF16, R * K), R, E, N, K, _stream(stream))
+    _check(st, "lmoe_grouped_linear_backward_x")
+
+
+def lmoe_grouped_linear_backward_w(grad_out, x, expert_offsets, grad_w, add=None, stream=None,
+                                   shape: tuple | None = None):
+    """grad_w[e] [N, K] = grad_out^T @ x over the rows of expert e (+ add[e]), fp32 or bf16 by
+    grad_w's dtype; add fp32, with an fp32 grad_w only (it may be grad_w).  Raw addresses: shape
+    (rows, E, N, K), grad_w is fp32 then."""
+    R, E, N, K = (int(v) for v in (shape if shape is not None else (x.shape[0], *grad_w.shape)))
+    half = getattr(grad_w, "dtype", torch.float32) in _BF16
+    out = _dev(grad_w, "grad_w", _BF16 if half else torch.float32, E * N * K)
+    st = load_library().lmoe_grouped_linear_backward_w(
+        _dev(grad_out, "grad_out", _BF16, R * N), _dev(x, "x", _BF16, R * K),
+        _dev(expert_offsets, "expert_offsets", torch.int32, E + 1),
+        _dev(add, "add", torch.float32, E * N * K), None if half else out, out if half else None,
+        R, E, N, K, _stream(stream))
+    _check(st, "lmoe_grouped_linear_backward_w")

@@ -40,9 +40,11 @@
 
 #include "fp8.cuh"
 #include "gemm_tc.cuh"
+#include "grouped.cuh"
 #include "lmoe_internal.cuh"
 #include "moe_data.cuh"
 #include "mxfp4.cuh"
+#include "norm.cuh"
 #include "router_train.cuh"
 
 namespace lmoe {
@@ -611,6 +613,19 @@ int validate_router(int T, int E, int topk, int S, float alpha) {
   if ((long long)T * topk > 2147483647ll || S < 1 || S > 65536 || !isfinite(alpha))
     return LMOE_ERR_DIM;
   return LMOE_OK;
+}
+
+// The checks of the norm's and of the grouped products' entry points that need no pointer.
+int validate_norm(int T, int H, float eps) {
+  return T < 0 || H < 8 || H % 8 || H > kMaxNormDim || !isfinite(eps) || eps < 0.0f ? LMOE_ERR_DIM
+                                                                                    : LMOE_OK;
+}
+
+int validate_grouped(int64_t rows, int E, int N, int K) {
+  return rows < 0 || rows > kMaxGroupedRows || E < 1 || E > 1024 || N < 8 || N % 8 ||
+                 N > kMaxGroupedDim || K < 8 || K % 8 || K > kMaxGroupedDim
+             ? LMOE_ERR_DIM
+             : LMOE_OK;
 }
 
 #define LMOE_TRY(x)                                  \
@@ -1377,6 +1392,125 @@ int moe_router_backward(const float* router_logits, const int32_t* topk_ids,
   LMOE_TRY(launch_router_backward(b, grad_topk_weights, renormalize, routed_scaling_factor,
                                   grad_loss, expert_counts, seq_tokens, alpha, grad_logits,
                                   (cudaStream_t)stream));
+  return LMOE_OK;
+}
+
+int lmoe_rms_norm(const lmoe_bf16* x, const lmoe_bf16* residual, const lmoe_bf16* norm_w,
+                  float rms_eps, lmoe_bf16* residual_out, lmoe_bf16* out, uint8_t* codes,
+                  float* scales, int T, int H, void* stream) {
+  const int v = validate_norm(T, H, rms_eps);
+  if (v != LMOE_OK) return v;
+  if (codes && H % 16) return LMOE_ERR_DIM;
+  if (T == 0) return LMOE_OK;
+  if (!x || (!out && !codes) || (codes == nullptr) != (scales == nullptr)) return LMOE_ERR_NULL;
+  const void* ptrs[] = {x, residual, norm_w, residual_out, out, codes, scales};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return LMOE_ERR_ALIGN;
+  if (!on_current_device({x, residual, norm_w, residual_out, out, codes, scales}))
+    return LMOE_ERR_DEVICE;
+  const NormForward n{x, residual, norm_w, residual_out, out, codes, scales, T, H, rms_eps};
+  LMOE_TRY(launch_norm(n, (cudaStream_t)stream));
+  return LMOE_OK;
+}
+
+size_t lmoe_rms_norm_backward_workspace_bytes(int T, int H) {
+  return validate_norm(T, H, 0.0f) == LMOE_OK ? norm_backward_workspace_bytes(T, H) : 0;
+}
+
+int lmoe_rms_norm_backward(const lmoe_bf16* grad_out, const lmoe_bf16* h, const lmoe_bf16* norm_w,
+                           const lmoe_bf16* grad_residual, float rms_eps, lmoe_bf16* grad_h,
+                           float* grad_norm_w, int T, int H, void* workspace,
+                           size_t workspace_bytes, void* stream) {
+  const int v = validate_norm(T, H, rms_eps);
+  if (v != LMOE_OK) return v;
+  if (T == 0) {
+    // an empty batch (a rank without tokens): 0, not what an earlier call left there
+    if (grad_norm_w && on_current_device({grad_norm_w}))
+      LMOE_TRY(cudaMemsetAsync(grad_norm_w, 0, (size_t)H * sizeof(float), (cudaStream_t)stream));
+    return LMOE_OK;
+  }
+  if (!grad_out || !h || !grad_h) return LMOE_ERR_NULL;
+  const void* ptrs[] = {grad_out, h, norm_w, grad_residual, grad_h, grad_norm_w};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return LMOE_ERR_ALIGN;
+  if (grad_norm_w && (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u) ||
+                      workspace_bytes < norm_backward_workspace_bytes(T, H)))
+    return LMOE_ERR_WORKSPACE;
+  if (!on_current_device({grad_out, h, norm_w, grad_residual, grad_h, grad_norm_w,
+                          grad_norm_w ? workspace : nullptr}))
+    return LMOE_ERR_DEVICE;
+  const NormBackward n{grad_out, h, norm_w, grad_residual, grad_h, grad_norm_w,
+                       static_cast<float*>(workspace), T, H, rms_eps};
+  LMOE_TRY(launch_norm_backward(n, (cudaStream_t)stream));
+  return LMOE_OK;
+}
+
+int situ_and_mul_backward(const lmoe_bf16* in, const lmoe_bf16* grad_out, lmoe_bf16* grad_in,
+                          int64_t N, int d, float beta, float linear_beta, void* stream) {
+  if (!finite_pos(beta)) return LMOE_ERR_BETA;
+  if (N < 0 || d <= 0 || d % 8 || !isfinite(linear_beta) || N > (1ll << 40) / d) return LMOE_ERR_DIM;
+  if (N == 0) return LMOE_OK;
+  if (!in || !grad_out || !grad_in) return LMOE_ERR_NULL;
+  if (!aligned16(in) || !aligned16(grad_out) || !aligned16(grad_in)) return LMOE_ERR_ALIGN;
+  if (!on_current_device({in, grad_out, grad_in})) return LMOE_ERR_DEVICE;
+  LMOE_TRY(launch_situ_backward(in, grad_out, grad_in, N, d, beta, linear_beta, (cudaStream_t)stream));
+  return LMOE_OK;
+}
+
+// lmoe_grouped_linear and its gradient to the rows
+static int grouped_rows(const lmoe_bf16* rows_in, const lmoe_bf16* w, const int32_t* expert_offsets,
+                        lmoe_bf16* rows_out, int64_t rows, int E, int N, int K, bool backward,
+                        void* stream) {
+  const int v = validate_grouped(rows, E, N, K);
+  if (v != LMOE_OK) return v;
+  if (rows == 0) return LMOE_OK;
+  if (!rows_in || !w || !expert_offsets || !rows_out) return LMOE_ERR_NULL;
+  if (!aligned16(rows_in) || !aligned16(w) || !aligned16(expert_offsets) || !aligned16(rows_out))
+    return LMOE_ERR_ALIGN;
+  if (!on_current_device({rows_in, w, expert_offsets, rows_out})) return LMOE_ERR_DEVICE;
+  const GroupedLinear g{rows_in, w, expert_offsets, rows_out, rows, E, N, K};
+  LMOE_TRY(launch_grouped_linear(g, backward, (cudaStream_t)stream));
+  return LMOE_OK;
+}
+
+int lmoe_grouped_linear(const lmoe_bf16* x, const lmoe_bf16* w, const int32_t* expert_offsets,
+                        lmoe_bf16* out, int64_t rows, int E, int N, int K, void* stream) {
+  return grouped_rows(x, w, expert_offsets, out, rows, E, N, K, false, stream);
+}
+
+int lmoe_grouped_linear_backward_x(const lmoe_bf16* grad_out, const lmoe_bf16* w,
+                                   const int32_t* expert_offsets, lmoe_bf16* grad_x, int64_t rows,
+                                   int E, int N, int K, void* stream) {
+  return grouped_rows(grad_out, w, expert_offsets, grad_x, rows, E, N, K, true, stream);
+}
+
+int lmoe_grouped_linear_backward_w(const lmoe_bf16* grad_out, const lmoe_bf16* x,
+                                   const int32_t* expert_offsets, const float* add, float* grad_w,
+                                   lmoe_bf16* grad_w_bf16, int64_t rows, int E, int N, int K,
+                                   void* stream) {
+  const int v = validate_grouped(rows, E, N, K);
+  if (v != LMOE_OK) return v;
+  if ((grad_w == nullptr) == (grad_w_bf16 == nullptr) || (add && !grad_w)) return LMOE_ERR_NULL;
+  if (rows > 0 && (!grad_out || !x || !expert_offsets)) return LMOE_ERR_NULL;
+  const void* ptrs[] = {grad_out, x, expert_offsets, add, grad_w, grad_w_bf16};
+  for (const void* p : ptrs)
+    if (p && !aligned16(p)) return LMOE_ERR_ALIGN;
+  if (rows == 0) {
+    // no rows at all (a rank without tokens): 0, or the gradient so far
+    if (!on_current_device({add, grad_w, grad_w_bf16})) return LMOE_ERR_DEVICE;
+    const size_t n = (size_t)E * N * K;
+    if (!add)
+      LMOE_TRY(cudaMemsetAsync(grad_w ? (void*)grad_w : grad_w_bf16, 0,
+                               n * (grad_w ? sizeof(float) : sizeof(lmoe_bf16)), (cudaStream_t)stream));
+    else if (add != grad_w)
+      LMOE_TRY(cudaMemcpyAsync(grad_w, add, n * sizeof(float), cudaMemcpyDeviceToDevice,
+                               (cudaStream_t)stream));
+    return LMOE_OK;
+  }
+  if (!on_current_device({grad_out, x, expert_offsets, add, grad_w, grad_w_bf16}))
+    return LMOE_ERR_DEVICE;
+  const GroupedWeightGrad g{grad_out, x, expert_offsets, add, grad_w, grad_w_bf16, rows, E, N, K};
+  LMOE_TRY(launch_grouped_weight_grad(g, (cudaStream_t)stream));
   return LMOE_OK;
 }
 

@@ -216,5 +216,8 @@ cudaError_t launch_situ(const uint16_t* in, uint16_t* out, long long N, int d, f
                         float lbeta, cudaStream_t s);
 cudaError_t launch_masked_situ(const uint16_t* in, uint16_t* out, const int32_t* counts, int E,
                                int T_max, int d, float beta, float lbeta, cudaStream_t s);
+// grad_in [N, 2d] of in [N, 2d] and grad_out [N, d]; N * d / 8 < 2^39
+cudaError_t launch_situ_backward(const uint16_t* in, const uint16_t* grad_out, uint16_t* grad_in,
+                                 long long N, int d, float beta, float lbeta, cudaStream_t s);
 
 }  // namespace lmoe

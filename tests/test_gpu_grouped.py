@@ -1,0 +1,343 @@
+"""GPU parity of the products grouped by expert and of their gradients against float64.
+
+Tolerance.  The tensor cores add up products in fp32: one rounding (of 2^-23 at most, the
+hardware truncates) a step of 16 terms and one for the rows' own sums, so that a sum of n
+terms is off by at most (n / 16 + 32) 2^-23 of the sum of their magnitudes; then one rounding
+of the output: bf16 2^-8, fp32 2^-24 (twice with an addend)."""
+import threading
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import training_oracle as O
+
+pytestmark = pytest.mark.gpu
+lm = pytest.importorskip("latent_mixture_experts_sigmoid_gb300")
+BF16 = torch.finfo(torch.bfloat16).eps / 2
+NAN = float("nan")
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _lib(cuda_ok):
+    lm.load_library()
+
+
+@pytest.fixture(autouse=True)
+def _no_device_error():
+    yield
+    assert lm.lmoe_device_error() == 0
+
+
+def f64(t):
+    return t.detach().double().cpu().numpy()
+
+
+def rand(shape, seed, std=1.0):
+    g = torch.Generator().manual_seed(seed)
+    return (std * torch.randn(shape, generator=g)).to(torch.bfloat16).to("cuda")
+
+
+def slack(n):
+    return (n / 16 + 32) * 2.0 ** -23
+
+
+def offsets(counts, first=0):
+    return torch.tensor(np.concatenate([[first], first + np.cumsum(counts)]), dtype=torch.int32, device="cuda")
+
+
+LEAD, TRAIL = 3, 5          # rows before the first and behind the last expert's
+
+# rows of each expert
+COUNTS = {
+    "one row": [1],
+    "empty": [0, 0, 0],
+    "borders": [0, 1, 15, 16, 17, 31, 32, 33, 0, 63, 64, 65, 127, 128, 129, 0],
+    "more borders": [255, 256, 257, 0, 0, 1, 600],
+    "many small": [(7 * i) % 5 for i in range(200)],
+    "one of many": [0] * 99 + [90] + [0] * 100,
+    "large": [1500],
+}
+DIMS = [(8, 8), (64, 64), (256, 128), (136, 200), (120, 264), (1024, 512), (384, 1032)]
+FEW = [("borders", 256, 128), ("borders", 136, 200), ("more borders", 1032, 72), ("many small", 520, 136), ("large", 264, 520)]
+CASES = [(c, n, k) for c in COUNTS for n, k in DIMS if COUNTS[c] != [1500] or n * k < 1 << 18]
+
+
+def make(name, N, K, seed=0):
+    counts = COUNTS[name]
+    R = sum(counts) + LEAD + TRAIL
+    off = offsets(counts, LEAD)
+    x, dy = rand((R, K), seed), rand((R, N), seed + 1, 1e-2)
+    w = rand((len(counts), N, K), seed + 2, 0.05)
+    # what belongs to nobody must not be looked at
+    for t in (x, dy):
+        t[:LEAD] = NAN
+        t[R - TRAIL:] = NAN
+    return off, x, dy, w, R
+
+
+def owned(counts):
+    return slice(LEAD, LEAD + sum(counts))
+
+
+def check_rows(call, ref_fn, rows_in, w, off, counts, terms, out_dim):
+    R = rows_in.shape[0]
+    buf = torch.full((R * out_dim + 64,), 7.0, dtype=torch.bfloat16, device="cuda")
+    out = buf[:R * out_dim].view(R, out_dim)
+    call(rows_in, w, off, out)
+    own = owned(counts)
+    o, wi, xi = f64(off), f64(w), f64(rows_in)
+    xi[:LEAD] = xi[R - TRAIL:] = 0
+    ref = ref_fn(xi, wi, o, np.zeros((R, out_dim)))
+    mag = ref_fn(np.abs(xi), np.abs(wi), o, np.zeros((R, out_dim)))
+    err, bound = np.abs(f64(out) - ref)[own], (BF16 * np.abs(ref) + slack(terms) * mag)[own]
+    assert np.all(err <= bound * (1 + 2 ** -7)), (float(np.nanmax(err / bound)), np.argwhere(~(err <= bound))[:5])
+    assert bool((buf[-64:] == 7.0).all()) and bool((out[:LEAD] == 7.0).all()) and bool((out[R - TRAIL:] == 7.0).all())
+    again = torch.full_like(out, 7.0)
+    call(rows_in, w, off, again)
+    assert torch.equal(again, out)
+
+
+@pytest.mark.parametrize("name,N,K", CASES)
+def test_forward(name, N, K):
+    off, x, dy, w, R = make(name, N, K)
+    check_rows(lm.lmoe_grouped_linear, O.grouped_linear, x, w, off, COUNTS[name], K, N)
+
+
+@pytest.mark.parametrize("name,N,K", CASES)
+def test_backward_x(name, N, K):
+    off, x, dy, w, R = make(name, N, K)
+    check_rows(lm.lmoe_grouped_linear_backward_x, O.grouped_linear_backward_x, dy, w, off, COUNTS[name], N, K)
+
+
+@pytest.mark.parametrize("form", ["fp32", "add", "in place", "bf16"])
+@pytest.mark.parametrize("name,N,K", CASES)
+def test_backward_w(name, N, K, form):
+    if form in ("add", "in place") and (name, N, K) not in FEW:
+        pytest.skip("the addend at a few sizes")
+    off, x, dy, w, R = make(name, N, K)
+    E, counts = w.shape[0], COUNTS[name]
+    dt = torch.bfloat16 if form == "bf16" else torch.float32
+    buf = torch.full((E * N * K + 64,), 7.0, dtype=dt, device="cuda")
+    dw = buf[:E * N * K].view(E, N, K)
+    add = None
+    if form == "add":
+        add = torch.randn((E, N, K), generator=torch.Generator().manual_seed(3)).to("cuda")
+    elif form == "in place":
+        dw.copy_(torch.randn((E, N, K), generator=torch.Generator().manual_seed(3)))
+        add = dw
+    before = None if add is None else f64(add)
+    lm.lmoe_grouped_linear_backward_w(dy, x, off, dw, add=add)
+    xi, di = f64(x), f64(dy)
+    for a in (xi, di):
+        a[:LEAD] = a[R - TRAIL:] = 0
+    ref = O.grouped_linear_backward_w(di, xi, f64(off), before)
+    mag = O.grouped_linear_backward_w(np.abs(di), np.abs(xi), f64(off))
+    n = np.array(counts)[:, None, None]
+    if form == "bf16":
+        bound = BF16 * np.abs(ref) * (1 + 2 ** -7) + slack(n) * mag
+    else:
+        bound = 2.0 ** -23 * np.abs(ref) + slack(n) * mag + (0 if before is None else 2.0 ** -23 * np.abs(before))
+    err = np.abs(f64(dw) - ref)
+    assert np.all(err <= bound), (float(np.nanmax(err - bound)), np.argwhere(~(err <= bound))[:5])
+    assert bool((buf[-64:] == 7.0).all())
+    assert not f64(dw)[np.array(counts) == 0].any() or before is not None
+    if form in ("fp32", "bf16"):
+        again = torch.full_like(dw, 7.0)
+        lm.lmoe_grouped_linear_backward_w(dy, x, off, again)
+        assert torch.equal(again, dw)
+
+
+def test_clamped_offsets():
+    # entries outside [0, rows] and descending ones lead nowhere outside the buffers
+    R, N, K = 40, 64, 64
+    x, w = rand((R, K), 0), rand((3, N, K), 1)
+    out = torch.full((R, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    off = torch.tensor([-100, 10, 5, 2 ** 31 - 1], dtype=torch.int32, device="cuda")
+    lm.lmoe_grouped_linear(x, w, off, out)
+    ref = O.grouped_linear(f64(x)[5:], f64(w)[2:], [0, 35], np.zeros((35, N)))
+    assert np.allclose(f64(out)[10:], ref[5:], rtol=2 ** -7, atol=1e-2)     # rows 5 .. 9 are two experts'
+    ref = O.grouped_linear(f64(x)[:5], f64(w)[:1], [0, 5], np.zeros((5, N)))
+    assert np.allclose(f64(out)[:5], ref, rtol=2 ** -7, atol=1e-2)
+    dw = torch.full((3, N, K), 7.0, device="cuda")
+    lm.lmoe_grouped_linear_backward_w(x, x, off, dw)
+    assert bool(torch.isfinite(dw).all()) and not dw[1].any()
+
+
+@pytest.mark.parametrize("value", [NAN, float("inf"), -float("inf")])
+def test_specials_stay_with_their_rows(value):
+    counts, N, K = [20, 70, 9, 33], 136, 200
+    off, R = offsets(counts), sum(counts)
+    x, dy, w = rand((R, K), 0), rand((R, N), 1), rand((4, N, K), 2)
+    y, dx, dw = (torch.empty(s, dtype=d, device="cuda") for s, d in
+                 (((R, N), torch.bfloat16), ((R, K), torch.bfloat16), ((4, N, K), torch.float32)))
+
+    def run():
+        lm.lmoe_grouped_linear(x, w, off, y)
+        lm.lmoe_grouped_linear_backward_x(dy, w, off, dx)
+        lm.lmoe_grouped_linear_backward_w(dy, x, off, dw)
+        return y.clone(), dx.clone(), dw.clone()
+
+    want = run()
+    row = 20 + 70 - 1                                  # the last of expert 1: next to expert 2's in a tile
+    x[row] = value
+    dy[row] = value
+    got = run()
+    keep = [i for i in range(R) if i != row]
+    assert torch.equal(got[0][keep], want[0][keep]) and torch.equal(got[1][keep], want[1][keep])
+    assert torch.equal(got[2][[0, 2, 3]], want[2][[0, 2, 3]])
+    assert not torch.isfinite(got[0][row].float()).any() and not torch.isfinite(got[2][1]).any()
+    # weights: of one expert
+    x[row], dy[row] = 1.0, 1.0
+    w[1] = value
+    lm.lmoe_grouped_linear(x, w, off, y)
+    lm.lmoe_grouped_linear_backward_x(dy, w, off, dx)
+    others = [i for i in range(R) if not 20 <= i < 90]
+    assert torch.equal(y[others], want[0][others]) and torch.equal(dx[others], want[1][others])
+
+
+def test_far_rows_and_experts():
+    # element offsets past 2^31: the last rows of a long batch, the last of many experts
+    K, N = 2048, 72
+    R = 2 ** 20 + 100
+    x = torch.empty((R, K), dtype=torch.bfloat16, device="cuda")
+    tail = rand((200, K), 0)
+    x[-200:] = tail
+    off = torch.tensor([R - 190, R - 150, R - 3], dtype=torch.int32, device="cuda")
+    w = rand((2, N, K), 1, 0.05)
+    out = torch.empty((R, N), dtype=torch.bfloat16, device="cuda")
+    lm.lmoe_grouped_linear(x, w, off, out)
+    rel = torch.tensor([0, 40, 187], dtype=torch.int32, device="cuda")
+    small = torch.empty((187, N), dtype=torch.bfloat16, device="cuda")
+    lm.lmoe_grouped_linear(tail[10:197].contiguous(), w, rel, small)
+    assert torch.equal(out[R - 190:R - 3], small)
+    dy = torch.empty((R, N), dtype=torch.bfloat16, device="cuda")
+    dy[-200:] = rand((200, N), 2)
+    dx, dw, dws = torch.empty_like(x), torch.empty((2, N, K), device="cuda"), torch.empty((2, N, K), device="cuda")
+    lm.lmoe_grouped_linear_backward_x(dy, w, off, dx)
+    lm.lmoe_grouped_linear_backward_w(dy, x, off, dw)
+    sx = torch.empty((187, K), dtype=torch.bfloat16, device="cuda")
+    part = dy[R - 190:R - 3].contiguous()
+    lm.lmoe_grouped_linear_backward_x(part, w, rel, sx)
+    lm.lmoe_grouped_linear_backward_w(part, tail[10:197].contiguous(), rel, dws)
+    assert torch.equal(dx[R - 190:R - 3], sx) and torch.equal(dw, dws)
+    del x, dx, dy, out
+    E, N, K = 1024, 1032, 2088                          # 2.2e9 weights
+    w = torch.zeros((E, N, K), dtype=torch.bfloat16, device="cuda")
+    w[-2:] = rand((2, N, K), 3, 0.05)
+    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    off[-2], off[-1] = 30, 70
+    x, out, sm = rand((70, K), 4), torch.empty((70, N), dtype=torch.bfloat16, device="cuda"), None
+    lm.lmoe_grouped_linear(x, w, off, out)
+    sm = torch.empty_like(out)
+    lm.lmoe_grouped_linear(x, w[-2:].contiguous(), torch.tensor([0, 30, 70], dtype=torch.int32, device="cuda"), sm)
+    assert torch.equal(out, sm)
+    dw = torch.full((E, N, K), 7.0, dtype=torch.bfloat16, device="cuda")
+    lm.lmoe_grouped_linear_backward_w(out, x, off, dw)
+    dws = torch.empty((2, N, K), dtype=torch.bfloat16, device="cuda")
+    lm.lmoe_grouped_linear_backward_w(out, x, torch.tensor([0, 30, 70], dtype=torch.int32, device="cuda"), dws)
+    assert torch.equal(dw[-2:], dws) and not dw[:-2].any()
+
+
+def test_no_rows():
+    w, off = rand((3, 64, 64), 0), torch.zeros(4, dtype=torch.int32, device="cuda")
+    e = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")
+    lm.lmoe_grouped_linear(e, w, off, e)
+    lm.lmoe_grouped_linear_backward_x(e, w, off, e)
+    for dt in (torch.float32, torch.bfloat16):
+        dw = torch.full((3, 64, 64), 7.0, dtype=dt, device="cuda")
+        lm.lmoe_grouped_linear_backward_w(e, e, off, dw)
+        assert not dw.any()
+    add = torch.randn((3, 64, 64), device="cuda")
+    dw = torch.full((3, 64, 64), 7.0, device="cuda")
+    lm.lmoe_grouped_linear_backward_w(e, e, off, dw, add=add)
+    assert torch.equal(dw, add)
+
+
+def test_against_differences():
+    # the loss sum(c * y) along directions of x and w: y is bilinear, so its float64 twin's
+    # difference is exact up to cancellation
+    counts, N, K = [5, 0, 40], 64, 72
+    off, R = offsets(counts), 45
+    x, c, w = rand((R, K), 0), rand((R, N), 1), rand((3, N, K), 2)
+    dx, dw = torch.empty_like(x), torch.empty((3, N, K), device="cuda")
+    lm.lmoe_grouped_linear_backward_x(c, w, off, dx)
+    lm.lmoe_grouped_linear_backward_w(c, x, off, dw)
+    g = np.random.default_rng(0)
+    for _ in range(4):
+        a, b = g.standard_normal((R, K)), g.standard_normal((3, N, K))
+
+        def loss(t):
+            return (f64(c) * O.grouped_linear(f64(x) + t * a, f64(w) + t * b, f64(off), np.zeros((R, N)))).sum()
+
+        diff = (loss(1e-4) - loss(-1e-4)) / 2e-4
+        room = 2 * BF16 * np.abs(f64(dx) * a).sum() + 1e-4 * np.abs(f64(dw) * b).sum() + 1e-3
+        assert abs((f64(dx) * a).sum() + (f64(dw) * b).sum() - diff) <= room
+
+
+def test_captured_replayed_and_beside_another_stream():
+    counts, N, K = [30, 0, 300, 77, 5, 128], 256, 320
+    off, R = offsets(counts), sum(counts)
+    x, dy, w = rand((R, K), 0), rand((R, N), 1), rand((6, N, K), 2)
+
+    def outputs():
+        return (torch.empty((R, N), dtype=torch.bfloat16, device="cuda"),
+                torch.empty((R, K), dtype=torch.bfloat16, device="cuda"), torch.empty((6, N, K), device="cuda"))
+
+    def run(o, stream=None):
+        lm.lmoe_grouped_linear(x, w, off, o[0], stream=stream)
+        lm.lmoe_grouped_linear_backward_x(dy, w, off, o[1], stream=stream)
+        lm.lmoe_grouped_linear_backward_w(dy, x, off, o[2], stream=stream)
+
+    want, a, b = outputs(), outputs(), outputs()
+    run(want)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        run(a)
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            run(a)
+    for t in a:
+        t.zero_()
+    torch.cuda.synchronize()
+    other = torch.cuda.Stream()
+    for _ in range(20):
+        graph.replay()
+        run(b, stream=other)
+    torch.cuda.synchronize()
+    assert all(torch.equal(p, q) and torch.equal(r, q) for p, q, r in zip(a, want, b))
+    results = []
+
+    def thread():
+        s = torch.cuda.Stream()
+        o = outputs()
+        torch.cuda.synchronize()
+        for _ in range(20):
+            run(o, stream=s)
+        s.synchronize()
+        results.append(all(torch.equal(p, q) for p, q in zip(o, want)))
+
+    ts = [threading.Thread(target=thread) for _ in range(2)]
+    for t in ts:
+        t.start()
+    for t in ts:
+        t.join()
+    assert results == [True, True]
+
+
+def test_weights_written_just_before():
+    # in stream order: a call before this one may have written the weights and the offsets
+    counts, N, K = [60, 4, 100], 128, 256
+    R = sum(counts)
+    x, w = rand((R, K), 0), rand((3, N, K), 1)
+    off = offsets(counts)
+    want, got = (torch.empty((R, N), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    lm.lmoe_grouped_linear(x, w, off, want)
+    for _ in range(10):
+        w2, off2 = torch.full_like(w, NAN), torch.zeros_like(off)
+        w2.copy_(w)
+        off2.copy_(off)
+        lm.lmoe_grouped_linear(x, w2, off2, got)
+        assert torch.equal(got, want)
