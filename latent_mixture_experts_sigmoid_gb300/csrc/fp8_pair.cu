@@ -70,36 +70,6 @@ __device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volati
   return false;
 }
 
-__device__ __forceinline__ uint32_t cluster_addr(uint32_t addr, uint32_t rank) {
-  uint32_t a;
-  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(addr), "r"(rank));
-  return a;
-}
-
-// A box into this CTA's shared memory, its bytes on a barrier of either CTA of the pair.
-__device__ __forceinline__ void tma_load_pair(const CUtensorMap* map, uint32_t dst, uint32_t cluster_bar,
-                                              int c0, int c1) {
-  asm volatile(
-      "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.cta_group::2"
-      " [%0], [%1, {%3, %4}], [%2];" ::"r"(dst),
-      "l"(reinterpret_cast<uint64_t>(map)), "r"(cluster_bar), "r"(c0), "r"(c1)
-      : "memory");
-}
-
-// (relaxed: see mbar_arrive_relaxed)
-__device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.relaxed.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
-               : "memory");
-}
-
-// Arrive on the barrier at `bar`'s offset in both CTAs once the pair's MMAs so far are done.
-__device__ __forceinline__ void commit_both(uint32_t bar) {
-  asm volatile(
-      "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64"
-      " [%0], %1;" ::"r"(bar), "h"((uint16_t)3)
-      : "memory");
-}
-
 __device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
                                          uint32_t accumulate) {
   asm volatile(

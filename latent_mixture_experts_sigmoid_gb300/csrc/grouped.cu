@@ -1,97 +1,636 @@
-// bf16 products of rows grouped by expert and their gradients:
+// bf16 products of rows grouped by expert and their gradients, on pairs of SMs:
 //   forward   out[r] = W_e x[r]
 //   backward  grad_x[r] = W_e^T grad_out[r],   grad_W_e = sum over r of grad_out[r] x[r]^T
-// for the rows r of expert e, offsets[e] .. offsets[e+1] - 1; products summed in fp32 and rounded
-// once.
+// for the rows r of expert e, offsets[e] .. offsets[e+1] - 1; products summed in fp32 on the
+// tensor cores and rounded once.
 //
-// The simplest form: a CTA a 64 x 64 tile, operands through shared memory, fp32 FMAs.
+// One kernel in three modes.  The two CTAs of a cluster compute a tile of 256 x N (tcgen05
+// cta_group::2); each brings in its own 128 rows of the M side and half of the N side, and the
+// tensor cores of both read both halves.
+//   forward   M: rows of W (K-major),     N: token rows (K-major),      summed over K
+//   rows      M: columns of W (M-major),  N: token rows (K-major),      summed over W's rows
+//   weights   M: columns of grad_out,     N: columns of x (both M/N-major),  summed over tokens
+// With the weights on the M side a tile's cost follows the number of an expert's rows in steps
+// of 32, where 128 or 256 rows on the M side would pay for all of them; the columns of other
+// experts' rows behind the last are not stored.  The major-ness is a bit of the MMA's operand
+// descriptors: nothing is transposed in memory.
+//
+// Where the token rows are the sum's index (weights), the last block of 64 reaches into the next
+// expert's rows.  Its bytes go to a barrier of the CTA's own first; a warp sets the rows behind the
+// last to zero and passes the block on.  (Both operands': 0 times another expert's NaN is NaN.)
+//
+//   warp 0      TMA producer of this CTA's halves; their bytes count on the leader's (rank 0's)
+//               barrier
+//   warp 1      allocates TMEM; in the leader one thread issues the MMAs of both CTAs, and its
+//               commits arrive in both
+//   warp 2      (weights) the zeros in the last blocks
+//   warps 4..11 read a finished tile from TMEM (warp w: the 32 M rows of lane quarter w % 4, half of
+//               the columns) and write it: token rows with two features a thread and store,
+//               gradients of weights through shared memory and bulk tensor stores
+// Two accumulators of 256 columns: a tile's output runs beside the next one's sums.
+// Every wait is bounded; neither CTA leaves or frees its TMEM before both are done.
+#include <cuda.h>
+
+#include <mutex>
+
 #include "grouped.cuh"
+#include "tc_ptx.cuh"
 
 namespace lmoe {
 namespace {
 
-constexpr int kT = 64, kD = 16, kThreads = 256;
+enum : int { kForward = 0, kRows = 1, kWeights = 2 };          // modes
+enum : int { kErrProducer = 1, kErrMmaFull = 2, kErrMmaTmem = 3, kErrEpilogue = 4,
+             kErrDrain = 5, kErrDone = 6 };                     // device error word codes
 
-// sum over k < depth of A(m, k) B(n, k), A(m, k) at a[m am + k ak]; the caller's thread gets rows
-// 4 ty .. and columns 4 tx .. of the tile
-__device__ void tile_product(const uint16_t* a, long long am, long long ak, int mv, const uint16_t* b,
-                             long long bn, long long bk, int nv, int depth, float (&acc)[4][4]) {
-  __shared__ float as[kD][kT + 1], bs[kD][kT + 1];
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) acc[i][j] = 0.0f;
-  for (int k0 = 0; k0 < depth; k0 += kD) {
-    __syncthreads();
-    for (int i = threadIdx.x; i < kT * kD; i += kThreads) {
-      const int k = i % kD, m = i / kD;
-      const bool in = k0 + k < depth;
-      as[k][m] = in && m < mv ? __uint_as_float((uint32_t)a[m * am + (k0 + k) * ak] << 16) : 0.0f;
-      bs[k][m] = in && m < nv ? __uint_as_float((uint32_t)b[m * bn + (k0 + k) * bk] << 16) : 0.0f;
+constexpr int kEpiWarp0 = 4, kEpiWarps = 8;
+constexpr int kThreads = (kEpiWarp0 + kEpiWarps) * 32;
+constexpr int kHalf = 128;                          // M rows of one CTA
+constexpr int kTile = 2 * kHalf;
+constexpr int kBK = 64;                             // a K block: 128 bytes
+constexpr uint32_t kChunk = kBK * 128;              // 64 M or N columns of a block, K rows of 128 bytes
+constexpr uint32_t kABytes = kHalf * kBK * 2;
+constexpr int kAcc = 2;                             // TMEM accumulators of 256 columns
+constexpr int kMaxStages = 12;
+constexpr int kMaxGroups = 1024;
+constexpr uint32_t kStageBox = 32 * 128;            // the epilogue's box of a gradient of weights
+
+struct Params {
+  int E, mdim, depth, ncols;     // M side's extent; terms of a sum and (weights) N side's extent
+  int mtiles, ntiles;            // tiles of a group, ntiles: weights only
+  int nt, part;                  // most token rows of a tile; rows of a partial box
+  int stages;
+  uint32_t stage_bytes;
+  long long R;
+  const int32_t* offsets;
+  uint16_t* out;                 // forward, rows
+  const float* add;              // weights
+  int* err;
+};
+
+// A bounded wait: each further try suspends the thread for about a microsecond at most,
+// 2^21 of them (about two seconds) end it.
+__device__ __forceinline__ bool wait_phase(uint32_t bar, uint32_t parity, volatile int* abort_flag,
+                                           int* err, int code) {
+  if (mbar_try_wait(bar, parity)) return true;
+  for (int n = 0; n < (1 << 21); ++n) {
+    if (mbar_try_wait_ns(bar, parity, 1000u)) return true;
+    if (*abort_flag) return false;
+  }
+  atomicCAS(err, 0, code);
+  *abort_flag = 1;
+  return false;
+}
+
+// kind::f16, bf16 operands, fp32 sums, M = 256
+__device__ __forceinline__ void mma_pair(uint32_t d_tmem, uint64_t a, uint64_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::2.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+      "l"(a), "l"(b), "r"(idesc), "r"(accumulate)
+      : "memory");
+}
+
+// Operand descriptors, both with the 128-byte swizzle.  K-major: rows of 64 K elements, groups of
+// eight rows 1024 bytes apart.  M/N-major: a row is one K index of 64 M or N elements, groups of
+// eight K 1024 bytes apart, the next 64 elements kChunk further.
+template <bool kMajorK>
+__device__ __forceinline__ uint64_t sdesc(uint32_t saddr) {
+  return (uint64_t)((saddr & 0x3FFFFu) >> 4) | (uint64_t)(kMajorK ? 1 : kChunk >> 4) << 16 |
+         (uint64_t)(1024 >> 4) << 32 | (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+// 16 K further: 32 bytes in a row, or 16 rows
+template <bool kMajorK>
+constexpr uint64_t kStep = (kMajorK ? 32 : 16 * 128) >> 4;
+
+template <int kMode>
+__device__ __forceinline__ uint32_t idesc(int n) {
+  return (1u << 4) | (1u << 7) | (1u << 10) | ((kMode == kForward ? 0u : 1u) << 15) |
+         ((kMode == kWeights ? 1u : 0u) << 16) | ((uint32_t)(n >> 3) << 17) |
+         ((uint32_t)(kTile >> 4) << 24);
+}
+
+// forward, rows: token tiles before each expert [E + 1], its first row and the one behind its
+// last [E], in shared memory.
+struct Groups {
+  int* prefix;
+  int2* rows;
+};
+
+// One tile of the walk.
+struct Tile {
+  int group, m0;      // first M row
+  int row0;           // token rows: the first and how many (weights: the group's)
+  int rows;
+  int n0, n;          // N side: first column (weights), the MMA's N
+};
+
+__device__ __forceinline__ int2 group_rows(const Params& p, int e) {
+  const int R = (int)p.R;
+  const int a = min(max(__ldg(p.offsets + e), 0), R);
+  return make_int2(a, min(max(__ldg(p.offsets + e + 1), a), R));
+}
+
+// forward, rows: tiles of an expert's token rows, the M tile changing fastest.  weights: an
+// expert's M x N tiles.
+template <int kMode>
+__device__ __forceinline__ Tile tile_of(const Params& p, const Groups& t, int u) {
+  Tile x;
+  if constexpr (kMode == kWeights) {
+    const int per = p.mtiles * p.ntiles;
+    x.group = u / per;
+    const int rem = u - x.group * per, m = rem / p.ntiles;
+    x.m0 = m * kTile;
+    x.n0 = (rem - m * p.ntiles) * kTile;
+    x.n = p.ncols - x.n0 > kHalf ? kTile : kHalf;
+    const int2 r = group_rows(p, x.group);
+    x.row0 = r.x;
+    x.rows = r.y - r.x;
+  } else {
+    const int i = u / p.mtiles;
+    x.m0 = (u - i * p.mtiles) * kTile;
+    int lo = 0, hi = p.E - 1;      // the last group whose prefix is <= i
+    while (lo < hi) {
+      const int mid = (lo + hi + 1) >> 1;
+      if (t.prefix[mid] <= i) lo = mid; else hi = mid - 1;
     }
-    __syncthreads();
-    for (int k = 0; k < kD; ++k)
-      for (int i = 0; i < 4; ++i)
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(as[k][4 * ty + i], bs[k][4 * tx + j], acc[i][j]);
+    x.group = lo;
+    const int2 r = t.rows[lo];
+    x.row0 = r.x + (i - t.prefix[lo]) * p.nt;
+    x.rows = min(p.nt, r.y - x.row0);
+    x.n0 = 0;
+    x.n = (x.rows + 31) & ~31;
+  }
+  return x;
+}
+
+// The table of the groups, by all threads of the CTA.
+__device__ void build_groups(const Params& p, const Groups& t, int* warp_sum) {
+  constexpr int kPer = (kMaxGroups + kThreads - 1) / kThreads;
+  const int g0 = threadIdx.x * kPer;
+  int tiles[kPer], sum = 0;
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    tiles[i] = 0;
+    if (g0 + i < p.E) {
+      const int2 r = group_rows(p, g0 + i);
+      t.rows[g0 + i] = r;
+      tiles[i] = (r.y - r.x + p.nt - 1) / p.nt;
+    }
+    sum += tiles[i];
+  }
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  int incl = sum;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int v = __shfl_up_sync(0xFFFFFFFFu, incl, o);
+    if (lane >= o) incl += v;
+  }
+  if (lane == 31) warp_sum[warp] = incl;
+  __syncthreads();
+  int run = incl - sum;
+  for (int w = 0; w < warp; ++w) run += warp_sum[w];
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    if (g0 + i <= p.E) t.prefix[g0 + i] = run;
+    run += tiles[i];
   }
 }
 
-__device__ __forceinline__ int2 group_rows(const int32_t* offsets, int e, long long R) {
-  const int a = min(max(__ldg(offsets + e), 0), (int)R);
-  return make_int2(a, min(max(__ldg(offsets + e + 1), a), (int)R));
+// forward, rows: 32 token columns of TMEM lane = feature f into the rows of out.  Neighbouring
+// lanes swap halves, so that each stores two features of every second row.
+__device__ __forceinline__ void store_rows(const Params& p, const uint32_t (&v)[32], int row0, int valid,
+                                           int f, int lane) {
+  uint16_t* at = p.out + (long long)(row0 + (lane & 1)) * p.mdim + (f & ~1);
+  const bool in = f < p.mdim;                        // (mdim is even: both of a pair, or none)
+#pragma unroll
+  for (int j = 0; j < 32; j += 2) {
+    const uint32_t own = pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
+    const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
+    // even lane: row j, features f, f + 1 = own low, other low; odd: row j + 1, other high, own high
+    const uint32_t two = lane & 1 ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
+    if (in && j + (lane & 1) < valid) *reinterpret_cast<uint32_t*>(at + (long long)j * p.mdim) = two;
+  }
 }
 
-__global__ void __launch_bounds__(kThreads)
-linear_kernel(GroupedLinear p, bool backward) {
+// kOut (weights): 0 fp32, 1 bf16, 2 fp32 with an addend
+template <int kMode, int kOut>
+__global__ void __launch_bounds__(kThreads, 1)
+grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
+               const __grid_constant__ CUtensorMap tmAp, const __grid_constant__ CUtensorMap tmBp,
+               const __grid_constant__ CUtensorMap tmO, const Params p) {
+  constexpr bool kAK = kMode == kForward, kBK_ = kMode != kWeights;   // K-major operands
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
+                                             ~uintptr_t(1023));
+  uint8_t* boxes = smem + (size_t)p.stages * p.stage_bytes;           // (weights)
+  uint64_t* bars = reinterpret_cast<uint64_t*>(boxes + (kMode == kWeights ? kEpiWarps * 2 * kStageBox : 0));
+  constexpr int kFull = 0, kEmpty = kMaxStages, kTfull = 2 * kMaxStages, kTempty = kTfull + kAcc,
+                kDone = kTempty + kAcc, kLast = kDone + 1, kBars = kLast + kMaxStages;
+  uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + kBars);
+  volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
+  int* warp_sum = reinterpret_cast<int*>(tmem_holder + 2);
+  const Groups groups{warp_sum + kThreads / 32 + 2 * p.E, reinterpret_cast<int2*>(warp_sum + kThreads / 32)};
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint32_t bar0 = smem_u32(bars);
+  auto bar_at = [&](int i) { return bar0 + 8u * (uint32_t)i; };
+  const uint32_t rank = cluster_rank();
+
   pdl_trigger();
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < p.stages; ++i) {
+      mbar_init(bar_at(kFull + i), kMode == kWeights ? 2 : 1);   // (a last block: both CTAs' warps 2)
+      mbar_init(bar_at(kEmpty + i), 1);
+      mbar_init(bar_at(kLast + i), 1);
+    }
+    for (int i = 0; i < kAcc; ++i) {
+      mbar_init(bar_at(kTfull + i), 1);
+      mbar_init(bar_at(kTempty + i), 2 * kEpiWarps);             // (the leader's: both CTAs' epilogues)
+    }
+    mbar_init(bar_at(kDone), 1);
+    *abort_flag = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+  }
+  if (warp == 1) {
+    asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(
+                     smem_u32(tmem_holder)), "r"(512u)
+                 : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;" ::: "memory");
+  }
   pdl_wait();
-  const int e = blockIdx.y, in = backward ? p.N : p.K, out = backward ? p.K : p.N;
-  const int2 r = group_rows(p.offsets, e, p.R);
-  const int c0 = blockIdx.x * kT;
-  const uint16_t* w = p.w + (long long)e * p.N * p.K + (long long)c0 * (backward ? 1 : p.K);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  for (long long r0 = r.x; r0 < r.y; r0 += kT) {
-    float acc[4][4];
-    tile_product(p.rows_in + r0 * in, in, 1, (int)min((long long)kT, r.y - r0), w,
-                 backward ? 1 : p.K, backward ? p.K : 1, out - c0, in, acc);
-    for (int i = 0; i < 4; ++i)
-      for (int j = 0; j < 4; ++j) {
-        const long long row = r0 + 4 * ty + i;
-        const int c = c0 + 4 * tx + j;
-        if (row < r.y && c < out) p.rows_out[row * out + c] = to_bf16(acc[i][j]);
+  int U;
+  if constexpr (kMode == kWeights) {
+    U = p.E * p.mtiles * p.ntiles;
+  } else {
+    build_groups(p, groups, warp_sum);
+  }
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();      // both CTAs' barriers are there before any copy or commit reaches them
+  tc_fence_after();
+  // (offsets that do not ascend may count rows more than once: the walk ends somewhere)
+  if constexpr (kMode != kWeights) U = (int)min((long long)groups.prefix[p.E] * p.mtiles, 1ll << 30);
+  const uint32_t tmem_base = *tmem_holder;
+  const int u0 = (int)(blockIdx.x >> 1), ustep = (int)(gridDim.x >> 1);
+  const int nkb_rows = (p.depth + kBK - 1) / kBK;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      // ---------------- TMA producer ----------------
+      int s = 0;
+      uint32_t ph = 0, it = 0;
+      bool ok = true;
+      for (int u = u0; u < U && ok; u += ustep) {
+        const Tile x = tile_of<kMode>(p, groups, u);
+        const int m = x.m0 + (int)rank * kHalf, half = x.n >> 1;
+        const int nkb = kMode == kWeights ? (x.rows + kBK - 1) / kBK : nkb_rows;
+        // token rows: one box of all, or as many partial ones as this CTA's half takes
+        const bool whole = x.n == p.nt;
+        const int nbox = whole ? 1 : (half + p.part - 1) / p.part;
+        const int brows = whole ? p.nt >> 1 : p.part;
+        const int tok = x.row0 + (int)rank * half;
+        const int nchunk = x.n >> 7;                 // (weights: 64 columns each)
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          if (!wait_phase(bar_at(kEmpty + s), ph ^ 1u, abort_flag, p.err, kErrProducer)) { ok = false; break; }
+          const uint32_t at = smem_u32(smem) + (uint32_t)s * p.stage_bytes, bt = at + kABytes;
+          const int k = kb * kBK;
+          const int left = x.rows - k;               // (weights)
+          if (kMode == kWeights && left < kBK) {
+            const int n16 = (left + 15) >> 4;
+            const uint32_t bar = bar_at(kLast + s);
+            mbar_arrive_expect_tx(bar, (uint32_t)((2 + nchunk) * n16) * 2048u);
+            for (int c = 0; c < 2; ++c)
+              for (int i = 0; i < n16; ++i)
+                tma_load_2d(&tmAp, at + c * kChunk + i * 2048u, bar, m + c * 64, x.row0 + k + i * 16);
+            for (int c = 0; c < nchunk; ++c)
+              for (int i = 0; i < n16; ++i)
+                tma_load_2d(&tmBp, bt + c * kChunk + i * 2048u, bar, x.n0 + (int)rank * half + c * 64,
+                            x.row0 + k + i * 16);
+          } else {
+            const uint32_t bar = cluster_addr(bar_at(kFull + s), 0);
+            if (rank == 0) {
+              const uint32_t bytes = kMode == kWeights ? (uint32_t)(2 + nchunk) * kChunk
+                                                       : kABytes + (uint32_t)(nbox * brows) * 128u;
+              if constexpr (kMode == kWeights) mbar_arrive(bar_at(kFull + s));
+              mbar_arrive_expect_tx(bar_at(kFull + s), 2 * bytes);
+            }
+            if constexpr (kMode == kForward) {
+              tma_load_pair_3d(&tmA, at, bar, k, m, x.group);
+            } else if constexpr (kMode == kRows) {
+              tma_load_pair_3d(&tmA, at, bar, m, k, x.group);
+              tma_load_pair_3d(&tmA, at + kChunk, bar, m + 64, k, x.group);
+            } else {
+              tma_load_pair(&tmA, at, bar, m, x.row0 + k);
+              tma_load_pair(&tmA, at + kChunk, bar, m + 64, x.row0 + k);
+            }
+            if constexpr (kMode == kWeights) {
+              for (int c = 0; c < nchunk; ++c)
+                tma_load_pair(&tmB, bt + c * kChunk, bar, x.n0 + (int)rank * half + c * 64, x.row0 + k);
+            } else {
+              const CUtensorMap* map = whole ? &tmB : &tmBp;
+              for (int i = 0; i < nbox; ++i)
+                tma_load_pair(map, bt + (uint32_t)(i * brows) * 128u, bar, k, tok + i * brows);
+            }
+          }
+          if (++s == p.stages) { s = 0; ph ^= 1u; }
+        }
       }
+      // the leader: every copy of the pair has landed before the CTAs exit
+      if (rank == 0)
+        for (uint32_t j = it > (uint32_t)p.stages ? it - p.stages : 0u; j < it; ++j) {
+          volatile int never = 0;
+          if (!wait_phase(bar_at(kFull + (int)(j % p.stages)), (j / p.stages) & 1u, &never, p.err, kErrDrain))
+            break;
+        }
+    }
+  } else if (warp == 1) {
+    if (lane == 0 && rank == 0) {
+      // ---------------- MMA issuer of the pair ----------------
+      const uint64_t a0 = sdesc<kAK>(smem_u32(smem)), b0 = sdesc<kBK_>(smem_u32(smem) + kABytes);
+      int s = 0;
+      uint32_t ph = 0, acc = 0, aph = 0;
+      bool ok = true;
+      for (int u = u0; u < U && ok; u += ustep) {
+        const Tile x = tile_of<kMode>(p, groups, u);
+        const int depth = kMode == kWeights ? x.rows : p.depth;
+        if (depth == 0) continue;                    // (an expert without rows: the epilogue writes zeros)
+        if (!wait_phase(bar_at(kTempty + (int)acc), aph ^ 1u, abort_flag, p.err, kErrMmaTmem)) break;
+        tc_fence_after();
+        const uint32_t id = idesc<kMode>(x.n);
+        for (int k = 0; k < depth; k += kBK) {
+          if (!wait_phase(bar_at(kFull + s), ph, abort_flag, p.err, kErrMmaFull)) { ok = false; break; }
+          if constexpr (kMode == kWeights)
+            if (depth - k < kBK) fence_acquire_cluster();      // the zeros of both CTAs' warps 2
+          tc_fence_after();
+          const uint64_t da = a0 + (uint64_t)s * (p.stage_bytes >> 4), db = b0 + (uint64_t)s * (p.stage_bytes >> 4);
+          const int steps = min(kBK / 16, (depth - k + 15) >> 4);
+          for (int j = 0; j < steps; ++j)
+            mma_pair(tmem_base + acc * kTile, da + j * kStep<kAK>, db + j * kStep<kBK_>, id, k + j ? 1u : 0u);
+          commit_both(bar_at(kEmpty + s));
+          if (++s == p.stages) { s = 0; ph ^= 1u; }
+        }
+        if (!ok) break;
+        commit_both(bar_at(kTfull + (int)acc));
+        if (++acc == kAcc) { acc = 0; aph ^= 1u; }
+      }
+      // every MMA this thread issued has completed before TMEM is freed
+      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                       bar_at(kDone))
+                   : "memory");
+      volatile int never = 0;
+      wait_phase(bar_at(kDone), 0u, &never, p.err, kErrDone);
+    }
+  } else if (warp == 2) {
+    if constexpr (kMode == kWeights) {
+      // ---------------- zeros behind an expert's last row ----------------
+      uint32_t it = 0, lph = 0;                      // lph: a stage's phase of kLast, a bit each
+      for (int u = u0; u < U; u += ustep) {
+        const Tile x = tile_of<kMode>(p, groups, u);
+        it += (uint32_t)(x.rows + kBK - 1) / kBK;
+        const int left = x.rows & (kBK - 1);
+        if (left == 0) continue;
+        const int s = (int)((it - 1) % (uint32_t)p.stages);
+        if (!__all_sync(0xFFFFFFFFu, wait_phase(bar_at(kLast + s), (lph >> s) & 1u, abort_flag, p.err, kErrProducer))) break;
+        lph ^= 1u << s;
+        const int z = -left & 15, nchunk = 2 + (x.n >> 7);       // rows up to the next 16; 64 columns each
+        uint8_t* at = smem + (size_t)s * p.stage_bytes + left * 128;
+        for (int i = lane; i < z * 8 * nchunk; i += 32) {
+          const int c = i / (z * 8);
+          *reinterpret_cast<uint4*>(at + c * kChunk + (i - c * z * 8) * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster_release(cluster_addr(bar_at(kFull + s), 0));
+      }
+    }
+  } else if (warp >= kEpiWarp0) {
+    // ---------------- epilogue ----------------
+    const int q = warp & 3;                      // TMEM lane quarter this warp may access
+    const int h = (warp - kEpiWarp0) >> 2;
+    const uint32_t tempty = cluster_addr(bar_at(kTempty), 0);
+    const uint32_t tmem = tmem_base + ((uint32_t)(q * 32) << 16);
+    uint32_t acc = 0, aph = 0;
+    int box = 0;
+    bool ok = true;
+    for (int u = u0; u < U && ok; u += ustep) {
+      const Tile x = tile_of<kMode>(p, groups, u);
+      const bool zero = kMode == kWeights && x.rows == 0;
+      const int m = x.m0 + (int)rank * kHalf + q * 32;           // first M row of the warp
+      if (!zero) {
+        // (a wait's outcome is one for the warp, whose lanes meet again below)
+        ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kTfull + (int)acc), aph, abort_flag, p.err, kErrEpilogue));
+        if (!ok) break;
+        tc_fence_after();
+      }
+      if constexpr (kMode != kWeights) {
+        for (int c = h * 32; c < x.rows; c += 64) {
+          uint32_t v[32];
+          tmem_ld32(tmem + acc * kTile + c, v);
+          tmem_wait_ld32(v);
+          store_rows(p, v, x.row0 + c, x.rows - c, m + lane, lane);
+        }
+      } else {
+        constexpr int kCols = kOut == 1 ? 64 : 32;               // columns of a box
+        const int c1 = (h + 1) * (x.n >> 1);
+        for (int c = h * (x.n >> 1); c < c1; c += kCols) {
+          const int col = x.n0 + c;
+          const bool in = m < p.mdim && col < p.ncols;
+          uint8_t* dst = boxes + ((warp - kEpiWarp0) * 2 + box) * kStageBox;
+          box ^= 1;
+          uint32_t w[32];
+          if constexpr (kOut == 1) {
+            uint32_t v[64];
+            if (!zero) {
+              tmem_ld64(tmem + acc * kTile + c, v);
+              tmem_wait_ld64(v);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j)
+              w[j] = zero ? 0u : pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
+          } else {
+            if (!zero) {
+              tmem_ld32(tmem + acc * kTile + c, w);
+              tmem_wait_ld32(w);
+            }
+#pragma unroll
+            for (int j = 0; j < 32; ++j) w[j] = zero ? 0u : w[j];
+            if constexpr (kOut == 2) {
+              if (m + lane < p.mdim) {
+                const float* a = p.add + ((long long)x.group * p.mdim + m + lane) * p.ncols + col;
+#pragma unroll
+                for (int j = 0; j < 32; j += 4)
+                  if (col + j < p.ncols) {                       // (ncols % 8 == 0)
+                    const float4 f = *reinterpret_cast<const float4*>(a + j);
+                    w[j] = __float_as_uint(__uint_as_float(w[j]) + f.x);
+                    w[j + 1] = __float_as_uint(__uint_as_float(w[j + 1]) + f.y);
+                    w[j + 2] = __float_as_uint(__uint_as_float(w[j + 2]) + f.z);
+                    w[j + 3] = __float_as_uint(__uint_as_float(w[j + 3]) + f.w);
+                  }
+              }
+            }
+          }
+          if (lane == 0) bulk_wait_read_but_one();               // the box's last store has read it
+          __syncwarp();
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<uint4*>(dst + lane * 128 + ((j ^ (lane & 7)) << 4)) =
+                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            if (in) tma_store_3d(&tmO, smem_u32(dst), col, m, x.group);
+            bulk_commit();
+          }
+        }
+      }
+      if (!zero) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive_cluster(tempty + 8u * acc);
+        if (++acc == kAcc) { acc = 0; aph ^= 1u; }
+      }
+    }
+    if (kMode == kWeights && lane == 0) bulk_wait_all();
   }
+
+  tc_fence_before();
+  __syncthreads();
+  cluster_sync();      // the pair's MMAs and commits are done with both CTAs
+  if (warp == 1) {
+    __syncwarp();
+    tc_fence_after();
+    asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem_base), "r"(512u)
+                 : "memory");
+  }
+  cluster_sync();
 }
 
-__global__ void __launch_bounds__(kThreads)
-weight_grad_kernel(GroupedWeightGrad p) {
-  pdl_trigger();
-  pdl_wait();
-  const int e = blockIdx.z, n0 = blockIdx.y * kT, k0 = blockIdx.x * kT;
-  const int2 r = group_rows(p.offsets, e, p.R);
-  const int tx = threadIdx.x & 15, ty = threadIdx.x >> 4;
-  float acc[4][4];
-  tile_product(p.dy + (long long)r.x * p.N + n0, 1, p.N, p.N - n0, p.x + (long long)r.x * p.K + k0, 1,
-               p.K, p.K - k0, r.y - r.x, acc);
-  for (int i = 0; i < 4; ++i)
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + 4 * ty + i, k = k0 + 4 * tx + j;
-      if (n >= p.N || k >= p.K) continue;
-      const long long at = ((long long)e * p.N + n) * p.K + k;
-      if (p.dw) p.dw[at] = p.add ? p.add[at] + acc[i][j] : acc[i][j];
-      else p.dw_bf16[at] = to_bf16(acc[i][j]);
-    }
+typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*,
+                                  const cuuint64_t*, const cuuint64_t*, const cuuint32_t*,
+                                  const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
+                                  CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+// [groups, rows, cols] in boxes of box_rows rows of 128 bytes, 128-byte swizzle; elements outside
+// read as zeros and are not written
+bool make_map(CUtensorMap* m, const void* base, bool fp32, long long groups, long long rows, int cols,
+              int box_rows) {
+  const EncodeTiledFn enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
+  if (!enc) return false;
+  const cuuint64_t size = fp32 ? 4 : 2;
+  cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)groups};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * size, (cuuint64_t)cols * size * (cuuint64_t)rows};
+  cuuint32_t box[3] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows, 1};
+  cuuint32_t estr[3] = {1, 1, 1};
+  return enc(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
+             groups ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
+             CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+             CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+constexpr size_t kMaxSmem = 227 * 1024;
+
+// shared memory of a launch but for its stages
+constexpr size_t other_smem(int mode, int E) {
+  return 1024 + (mode == kWeights ? (size_t)kEpiWarps * 2 * kStageBox : 0) +
+         (3 * kMaxStages + 2 * kAcc + 1) * 8 + 8 + (kThreads / 32) * 4 +
+         (mode == kWeights ? 0 : (size_t)(3 * E + 1) * 4) + 16;
+}
+
+// Pairs that fit on the current device at once (pairs share a GPC), 0 on failure.
+template <int kMode, int kOut>
+int pairs_resident() {
+  static int cache[64] = {};
+  static std::mutex mu;
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  if (cache[dev]) return cache[dev];
+  auto* kern = grouped_kernel<kMode, kOut>;
+  if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) != cudaSuccess)
+    return 0;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(2 * num_sms());
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = kMaxSmem;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = 2;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  int n = 0;
+  if (cudaOccupancyMaxActiveClusters(&n, kern, &cfg) != cudaSuccess) return 0;
+  return cache[dev] = n;
+}
+
+struct Maps {
+  CUtensorMap a, b, ap, bp, o;
+};
+
+template <int kMode, int kOut>
+cudaError_t launch(const Maps& m, Params& p, long long units, cudaStream_t s) {
+  const int pairs = pairs_resident<kMode, kOut>();
+  if (pairs < 1) return cudaErrorInvalidConfiguration;
+  p.err = device_error_word();
+  if (!p.err) return cudaErrorInvalidValue;
+  const size_t other = other_smem(kMode, p.E);
+  p.stages = (int)((kMaxSmem - other) / p.stage_bytes);
+  if (p.stages > kMaxStages) p.stages = kMaxStages;
+  return launch_k_cluster(grouped_kernel<kMode, kOut>, dim3(2 * (unsigned)(units < pairs ? units : pairs)),
+                          dim3(kThreads), other + (size_t)p.stages * p.stage_bytes, s, 2, m.a, m.b, m.ap,
+                          m.bp, m.o, p);
 }
 
 }  // namespace
 
 cudaError_t launch_grouped_linear(const GroupedLinear& g, bool backward, cudaStream_t s) {
-  return launch_k(linear_kernel, dim3(ceil_div(backward ? g.K : g.N, kT), g.E), dim3(kThreads), 0, s, g,
-                  backward);
+  Params p{};
+  p.E = g.E;
+  p.mdim = backward ? g.K : g.N;
+  p.depth = backward ? g.N : g.K;
+  p.mtiles = ceil_div(p.mdim, kTile);
+  p.nt = g.R <= 8ll * g.E ? 32 : g.R <= 32ll * g.E ? 128 : 256;
+  p.part = p.nt >= 64 ? 32 : 16;
+  p.stage_bytes = kABytes + (uint32_t)p.nt * 64;
+  p.R = g.R;
+  p.offsets = g.offsets;
+  p.out = g.rows_out;
+  Maps m;
+  if (!make_map(&m.a, g.w, false, g.E, g.N, g.K, backward ? kBK : kHalf) ||
+      !make_map(&m.b, g.rows_in, false, 0, g.R, p.depth, p.nt / 2) ||
+      !make_map(&m.bp, g.rows_in, false, 0, g.R, p.depth, p.part))
+    return cudaErrorInvalidValue;
+  m.ap = m.a;
+  m.o = m.a;
+  // token tiles: one a started nt rows and expert at most
+  const long long units = (g.R / p.nt + (g.R < g.E ? g.R : g.E)) * p.mtiles;
+  return backward ? launch<kRows, 0>(m, p, units, s) : launch<kForward, 0>(m, p, units, s);
 }
 
 cudaError_t launch_grouped_weight_grad(const GroupedWeightGrad& g, cudaStream_t s) {
-  return launch_k(weight_grad_kernel, dim3(ceil_div(g.K, kT), ceil_div(g.N, kT), g.E), dim3(kThreads), 0,
-                  s, g);
+  Params p{};
+  p.E = g.E;
+  p.mdim = g.N;
+  p.ncols = g.K;
+  p.mtiles = ceil_div(g.N, kTile);
+  p.ntiles = ceil_div(g.K, kTile);
+  p.stage_bytes = 2 * kABytes;
+  p.R = g.R;
+  p.offsets = g.offsets;
+  p.add = g.add;
+  Maps m;
+  const bool fp32 = g.dw != nullptr;
+  if (!make_map(&m.a, g.dy, false, 0, g.R, g.N, kBK) || !make_map(&m.ap, g.dy, false, 0, g.R, g.N, 16) ||
+      !make_map(&m.b, g.x, false, 0, g.R, g.K, kBK) || !make_map(&m.bp, g.x, false, 0, g.R, g.K, 16) ||
+      !make_map(&m.o, fp32 ? (const void*)g.dw : g.dw_bf16, fp32, g.E, g.N, g.K, 32))
+    return cudaErrorInvalidValue;
+  const long long units = (long long)p.E * p.mtiles * p.ntiles;
+  if (!fp32) return launch<kWeights, 1>(m, p, units, s);
+  return p.add ? launch<kWeights, 2>(m, p, units, s) : launch<kWeights, 0>(m, p, units, s);
 }
 
 }  // namespace lmoe
