@@ -347,8 +347,10 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         }
     }
   } else if (warp == 1) {
-    if (lane == 0 && rank == 0) {
+    if (rank == 0) {
       // ---------------- MMA issuer of the pair ----------------
+      // The warp runs the loop as one and a lane of it issues: an MMA's operands go through
+      // registers of the warp, which a branch of one lane fills at about 130 cycles an MMA.
       const uint64_t a0 = sdesc<kAK>(smem_u32(smem)), b0 = sdesc<kBK_>(smem_u32(smem) + kABytes);
       int s = 0;
       uint32_t ph = 0, acc = 0, aph = 0;
@@ -357,29 +359,39 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const Tile x = tile_of<kMode>(p, groups, u);
         const int depth = kMode == kWeights ? x.rows : p.depth;
         if (depth == 0) continue;                    // (an expert without rows: the epilogue writes zeros)
-        if (!wait_phase(bar_at(kTempty + (int)acc), aph ^ 1u, abort_flag, p.err, kErrMmaTmem)) break;
+        ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kTempty + (int)acc), aph ^ 1u, abort_flag, p.err, kErrMmaTmem));
+        if (!ok) break;
         tc_fence_after();
-        const uint32_t id = idesc<kMode>(x.n);
+        const uint32_t id = idesc<kMode>(x.n), d = tmem_base + acc * kTile;
         for (int k = 0; k < depth; k += kBK) {
-          if (!wait_phase(bar_at(kFull + s), ph, abort_flag, p.err, kErrMmaFull)) { ok = false; break; }
+          ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kFull + s), ph, abort_flag, p.err, kErrMmaFull));
+          if (!ok) break;
           if constexpr (kMode == kWeights)
             if (depth - k < kBK) fence_acquire_cluster();      // the zeros of both CTAs' warps 2
           tc_fence_after();
           const uint64_t da = a0 + (uint64_t)s * (p.stage_bytes >> 4), db = b0 + (uint64_t)s * (p.stage_bytes >> 4);
-          const int steps = min(kBK / 16, (depth - k + 15) >> 4);
-          for (int j = 0; j < steps; ++j)
-            mma_pair(tmem_base + acc * kTile, da + j * kStep<kAK>, db + j * kStep<kBK_>, id, k + j ? 1u : 0u);
-          commit_both(bar_at(kEmpty + s));
+          if (elect_one()) {
+#pragma unroll
+            for (int j = 0; j < kBK / 16; ++j)
+              // (weights: not past the zeros; the others' blocks are whole or filled up with zeros)
+              if (kMode != kWeights || k + 16 * j < depth)
+                mma_pair(d, da + j * kStep<kAK>, db + j * kStep<kBK_>, id, j ? 1u : (uint32_t)(k != 0));
+            commit_both(bar_at(kEmpty + s));
+          }
+          __syncwarp();
           if (++s == p.stages) { s = 0; ph ^= 1u; }
         }
         if (!ok) break;
-        commit_both(bar_at(kTfull + (int)acc));
+        if (elect_one()) commit_both(bar_at(kTfull + (int)acc));
+        __syncwarp();
         if (++acc == kAcc) { acc = 0; aph ^= 1u; }
       }
-      // every MMA this thread issued has completed before TMEM is freed
-      asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                       bar_at(kDone))
-                   : "memory");
+      // every MMA the lane issued has completed before TMEM is freed
+      if (elect_one())
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                         bar_at(kDone))
+                     : "memory");
+      __syncwarp();
       volatile int never = 0;
       wait_phase(bar_at(kDone), 0u, &never, p.err, kErrDone);
     }
