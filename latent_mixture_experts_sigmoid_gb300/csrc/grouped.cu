@@ -278,26 +278,29 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int nkb_rows = (p.depth + kBK - 1) / kBK;
 
   if (warp == 0) {
-    if (lane == 0) {
-      // ---------------- TMA producer ----------------
-      int s = 0;
-      uint32_t ph = 0, it = 0;
-      bool ok = true;
-      for (int u = u0; u < U && ok; u += ustep) {
-        const Tile x = tile_of<kMode>(p, groups, u);
-        const int m = x.m0 + (int)rank * kHalf, half = x.n >> 1;
-        const int nkb = kMode == kWeights ? (x.rows + kBK - 1) / kBK : nkb_rows;
-        // token rows: one box of all, or as many partial ones as this CTA's half takes
-        const bool whole = x.n == p.nt;
-        const int nbox = whole ? 1 : (half + p.part - 1) / p.part;
-        const int brows = whole ? p.nt >> 1 : p.part;
-        const int tok = x.row0 + (int)rank * half;
-        const int nchunk = x.n >> 7;                 // (weights: 64 columns each)
-        for (int kb = 0; kb < nkb; ++kb, ++it) {
-          if (!wait_phase(bar_at(kEmpty + s), ph ^ 1u, abort_flag, p.err, kErrProducer)) { ok = false; break; }
-          const uint32_t at = smem_u32(smem) + (uint32_t)s * p.stage_bytes, bt = at + kABytes;
-          const int k = kb * kBK;
-          const int left = x.rows - k;               // (weights)
+    // ---------------- TMA producer ----------------
+    // (the warp runs as one and a lane issues, as in the MMA warp)
+    int s = 0;
+    uint32_t ph = 0, it = 0;
+    bool ok = true;
+    for (int u = u0; u < U && ok; u += ustep) {
+      const Tile x = tile_of<kMode>(p, groups, u);
+      const int m = x.m0 + (int)rank * kHalf, half = x.n >> 1;
+      const int nkb = kMode == kWeights ? (x.rows + kBK - 1) / kBK : nkb_rows;
+      // token rows: one box of all, or as many partial ones as this CTA's half takes
+      const bool whole = x.n == p.nt;
+      const int nbox = whole ? 1 : (half + p.part - 1) / p.part;
+      const int brows = whole ? p.nt >> 1 : p.part;
+      const int tok = x.row0 + (int)rank * half;
+      const int nchunk = x.n >> 7;                   // (weights: 64 columns each)
+      const int n0 = x.n0 + (int)rank * half;
+      for (int kb = 0; kb < nkb; ++kb, ++it) {
+        ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kEmpty + s), ph ^ 1u, abort_flag, p.err, kErrProducer));
+        if (!ok) break;
+        const uint32_t at = smem_u32(smem) + (uint32_t)s * p.stage_bytes, bt = at + kABytes;
+        const int k = kb * kBK;
+        const int left = x.rows - k;                 // (weights)
+        if (elect_one()) {
           if (kMode == kWeights && left < kBK) {
             const int n16 = (left + 15) >> 4;
             const uint32_t bar = bar_at(kLast + s);
@@ -307,8 +310,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                 tma_load_2d(&tmAp, at + c * kChunk + i * 2048u, bar, m + c * 64, x.row0 + k + i * 16);
             for (int c = 0; c < nchunk; ++c)
               for (int i = 0; i < n16; ++i)
-                tma_load_2d(&tmBp, bt + c * kChunk + i * 2048u, bar, x.n0 + (int)rank * half + c * 64,
-                            x.row0 + k + i * 16);
+                tma_load_2d(&tmBp, bt + c * kChunk + i * 2048u, bar, n0 + c * 64, x.row0 + k + i * 16);
           } else {
             const uint32_t bar = cluster_addr(bar_at(kFull + s), 0);
             if (rank == 0) {
@@ -327,25 +329,27 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
               tma_load_pair(&tmA, at + kChunk, bar, m + 64, x.row0 + k);
             }
             if constexpr (kMode == kWeights) {
-              for (int c = 0; c < nchunk; ++c)
-                tma_load_pair(&tmB, bt + c * kChunk, bar, x.n0 + (int)rank * half + c * 64, x.row0 + k);
+              tma_load_pair(&tmB, bt, bar, n0, x.row0 + k);
+              if (nchunk > 1) tma_load_pair(&tmB, bt + kChunk, bar, n0 + 64, x.row0 + k);
+            } else if (whole) {
+              tma_load_pair(&tmB, bt, bar, k, tok);
             } else {
-              const CUtensorMap* map = whole ? &tmB : &tmBp;
               for (int i = 0; i < nbox; ++i)
-                tma_load_pair(map, bt + (uint32_t)(i * brows) * 128u, bar, k, tok + i * brows);
+                tma_load_pair(&tmBp, bt + (uint32_t)(i * brows) * 128u, bar, k, tok + i * brows);
             }
           }
-          if (++s == p.stages) { s = 0; ph ^= 1u; }
         }
+        __syncwarp();
+        if (++s == p.stages) { s = 0; ph ^= 1u; }
       }
-      // the leader: every copy of the pair has landed before the CTAs exit
-      if (rank == 0)
-        for (uint32_t j = it > (uint32_t)p.stages ? it - p.stages : 0u; j < it; ++j) {
-          volatile int never = 0;
-          if (!wait_phase(bar_at(kFull + (int)(j % p.stages)), (j / p.stages) & 1u, &never, p.err, kErrDrain))
-            break;
-        }
     }
+    // the leader: every copy of the pair has landed before the CTAs exit
+    if (rank == 0)
+      for (uint32_t j = it > (uint32_t)p.stages ? it - p.stages : 0u; j < it; ++j) {
+        volatile int never = 0;
+        if (!wait_phase(bar_at(kFull + (int)(j % p.stages)), (j / p.stages) & 1u, &never, p.err, kErrDrain))
+          break;
+      }
   } else if (warp == 1) {
     if (rank == 0) {
       // ---------------- MMA issuer of the pair ----------------
