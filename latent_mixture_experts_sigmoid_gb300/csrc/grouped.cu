@@ -215,6 +215,21 @@ __device__ __forceinline__ void store_rows(const Params& p, const uint32_t (&v)[
   }
 }
 
+// weights: the addend of a box at row m, column col: 128 bytes of a row by eight lanes, four rows a load
+__device__ __forceinline__ void load_addend(const Params& p, const Tile& x, int m, int col, int lane,
+                                            uint4 (&add)[8]) {
+  const int r = m + (lane >> 3), c = col + (lane & 7) * 4;       // (ncols % 8 == 0)
+  const float* at = p.add + ((long long)x.group * p.mdim + r) * p.ncols + c;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    add[i] = make_uint4(0, 0, 0, 0);
+    if (r + i * 4 < p.mdim && c < p.ncols)
+      asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                   : "=r"(add[i].x), "=r"(add[i].y), "=r"(add[i].z), "=r"(add[i].w)
+                   : "l"(at + (long long)i * 4 * p.ncols));
+  }
+}
+
 // kOut (weights): 0 fp32, 1 bf16, 2 fp32 with an addend
 template <int kMode, int kOut>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -226,7 +241,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
   uint8_t* boxes = smem + (size_t)p.stages * p.stage_bytes;           // (weights)
-  uint64_t* bars = reinterpret_cast<uint64_t*>(boxes + (kMode == kWeights ? kEpiWarps * 2 * kStageBox : 0));
+  uint64_t* bars = reinterpret_cast<uint64_t*>(boxes + (kMode == kWeights ? kEpiWarps * kStageBox : 0));
   constexpr int kFull = 0, kEmpty = kMaxStages, kTfull = 2 * kMaxStages, kTempty = kTfull + kAcc,
                 kDone = kTempty + kAcc, kLast = kDone + 1, kBars = kLast + kMaxStages;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + kBars);
@@ -370,8 +385,6 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         for (int k = 0; k < depth; k += kBK) {
           ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kFull + s), ph, abort_flag, p.err, kErrMmaFull));
           if (!ok) break;
-          if constexpr (kMode == kWeights)
-            if (depth - k < kBK) fence_acquire_cluster();      // the zeros of both CTAs' warps 2
           tc_fence_after();
           const uint64_t da = a0 + (uint64_t)s * (p.stage_bytes >> 4), db = b0 + (uint64_t)s * (p.stage_bytes >> 4);
           if (elect_one()) {
@@ -411,15 +424,14 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const int s = (int)((it - 1) % (uint32_t)p.stages);
         if (!__all_sync(0xFFFFFFFFu, wait_phase(bar_at(kLast + s), (lph >> s) & 1u, abort_flag, p.err, kErrProducer))) break;
         lph ^= 1u << s;
-        const int z = -left & 15, nchunk = 2 + (x.n >> 7);       // rows up to the next 16; 64 columns each
+        const int z = (-left & 15) * 8;              // 16-byte pieces of the rows up to the next 16
         uint8_t* at = smem + (size_t)s * p.stage_bytes + left * 128;
-        for (int i = lane; i < z * 8 * nchunk; i += 32) {
-          const int c = i / (z * 8);
-          *reinterpret_cast<uint4*>(at + c * kChunk + (i - c * z * 8) * 16) = make_uint4(0, 0, 0, 0);
-        }
+        for (int c = 0; c < 2 + (x.n >> 7); ++c)     // 64 columns each
+          for (int i = lane; i < z; i += 32)
+            *reinterpret_cast<uint4*>(at + c * kChunk + i * 16) = make_uint4(0, 0, 0, 0);
         fence_proxy_async_smem();
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_release(cluster_addr(bar_at(kFull + s), 0));
+        if (lane == 0) mbar_arrive_cluster_data(cluster_addr(bar_at(kFull + s), 0));
       }
     }
   } else if (warp >= kEpiWarp0) {
@@ -428,9 +440,16 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const int h = (warp - kEpiWarp0) >> 2;
     const uint32_t tempty = cluster_addr(bar_at(kTempty), 0);
     const uint32_t tmem = tmem_base + ((uint32_t)(q * 32) << 16);
+    constexpr int kCols = kOut == 1 ? 64 : 32;   // (weights) columns of a box, one box a warp
+    uint8_t* box = boxes + (warp - kEpiWarp0) * kStageBox;
+    uint4 add[8];
     uint32_t acc = 0, aph = 0;
-    int box = 0;
     bool ok = true;
+    if constexpr (kOut == 2)
+      if (u0 < U) {
+        const Tile x = tile_of<kMode>(p, groups, u0);
+        load_addend(p, x, x.m0 + (int)rank * kHalf + q * 32, x.n0 + h * (x.n >> 1), lane, add);
+      }
     for (int u = u0; u < U && ok; u += ustep) {
       const Tile x = tile_of<kMode>(p, groups, u);
       const bool zero = kMode == kWeights && x.rows == 0;
@@ -449,13 +468,24 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           store_rows(p, v, x.row0 + c, x.rows - c, m + lane, lane);
         }
       } else {
-        constexpr int kCols = kOut == 1 ? 64 : 32;               // columns of a box
         const int c1 = (h + 1) * (x.n >> 1);
         for (int c = h * (x.n >> 1); c < c1; c += kCols) {
           const int col = x.n0 + c;
-          const bool in = m < p.mdim && col < p.ncols;
-          uint8_t* dst = boxes + ((warp - kEpiWarp0) * 2 + box) * kStageBox;
-          box ^= 1;
+          if (lane == 0) bulk_wait_read();                       // the box's last store has read it
+          __syncwarp();
+          if constexpr (kOut == 2) {
+            // the addend, 128 bytes of a row by eight lanes, then the next box's on its way
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+              *reinterpret_cast<uint4*>(box + (i * 4 + (lane >> 3)) * 128 +
+                                        (((lane ^ (i * 4 + (lane >> 3))) & 7) << 4)) = add[i];
+            __syncwarp();
+            if (c + kCols < c1) load_addend(p, x, m, col + kCols, lane, add);
+            else if (u + ustep < U) {
+              const Tile y = tile_of<kMode>(p, groups, u + ustep);
+              load_addend(p, y, y.m0 + (int)rank * kHalf + q * 32, y.n0 + h * (y.n >> 1), lane, add);
+            }
+          }
           uint32_t w[32];
           if constexpr (kOut == 1) {
             uint32_t v[64];
@@ -473,31 +503,24 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             }
 #pragma unroll
             for (int j = 0; j < 32; ++j) w[j] = zero ? 0u : w[j];
-            if constexpr (kOut == 2) {
-              if (m + lane < p.mdim) {
-                const float* a = p.add + ((long long)x.group * p.mdim + m + lane) * p.ncols + col;
-#pragma unroll
-                for (int j = 0; j < 32; j += 4)
-                  if (col + j < p.ncols) {                       // (ncols % 8 == 0)
-                    const float4 f = *reinterpret_cast<const float4*>(a + j);
-                    w[j] = __float_as_uint(__uint_as_float(w[j]) + f.x);
-                    w[j + 1] = __float_as_uint(__uint_as_float(w[j + 1]) + f.y);
-                    w[j + 2] = __float_as_uint(__uint_as_float(w[j + 2]) + f.z);
-                    w[j + 3] = __float_as_uint(__uint_as_float(w[j + 3]) + f.w);
-                  }
-              }
-            }
           }
-          if (lane == 0) bulk_wait_read_but_one();               // the box's last store has read it
-          __syncwarp();
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<uint4*>(dst + lane * 128 + ((j ^ (lane & 7)) << 4)) =
-                make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+          for (int j = 0; j < 8; ++j) {
+            uint4* at = reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4));
+            uint4 v = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
+            if constexpr (kOut == 2) {
+              const uint4 a = *at;
+              v.x = __float_as_uint(__uint_as_float(v.x) + __uint_as_float(a.x));
+              v.y = __float_as_uint(__uint_as_float(v.y) + __uint_as_float(a.y));
+              v.z = __float_as_uint(__uint_as_float(v.z) + __uint_as_float(a.z));
+              v.w = __float_as_uint(__uint_as_float(v.w) + __uint_as_float(a.w));
+            }
+            *at = v;
+          }
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (in) tma_store_3d(&tmO, smem_u32(dst), col, m, x.group);
+            if (m < p.mdim && col < p.ncols) tma_store_3d(&tmO, smem_u32(box), col, m, x.group);
             bulk_commit();
           }
         }
@@ -550,7 +573,7 @@ constexpr size_t kMaxSmem = 227 * 1024;
 
 // shared memory of a launch but for its stages
 constexpr size_t other_smem(int mode, int E) {
-  return 1024 + (mode == kWeights ? (size_t)kEpiWarps * 2 * kStageBox : 0) +
+  return 1024 + (mode == kWeights ? (size_t)kEpiWarps * kStageBox : 0) +
          (3 * kMaxStages + 2 * kAcc + 1) * 8 + 8 + (kThreads / 32) * 4 +
          (mode == kWeights ? 0 : (size_t)(3 * E + 1) * 4) + 16;
 }

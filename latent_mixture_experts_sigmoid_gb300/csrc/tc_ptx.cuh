@@ -187,14 +187,10 @@ __device__ __forceinline__ void tma_load_pair_3d(const CUtensorMap* map, uint32_
       : "memory");
 }
 
-// The same barrier with the release that writes into this CTA's shared memory need before the
-// other CTA's MMA reads them, and the wait that acquires them.
-__device__ __forceinline__ void mbar_arrive_cluster_release(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar)
-               : "memory");
-}
-__device__ __forceinline__ void fence_acquire_cluster() {
-  asm volatile("fence.acq_rel.cluster;" ::: "memory");
+// The same where this CTA's threads have written shared memory that the other CTA's MMAs read,
+// behind the writers' fence_proxy_async_smem() and a barrier among them.
+__device__ __forceinline__ void mbar_arrive_cluster_data(uint32_t cluster_bar) {
+  asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
 }
 
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
@@ -204,11 +200,6 @@ __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t sr
       "r"(src), "r"(c0), "r"(c1), "r"(c2)
       : "memory");
 }
-// every bulk store of this thread but the last has finished reading its shared memory
-__device__ __forceinline__ void bulk_wait_read_but_one() {
-  asm volatile("cp.async.bulk.wait_group.read 1;" ::: "memory");
-}
-
 __device__ __forceinline__ void tc_fence_before() {
   asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory");
 }
