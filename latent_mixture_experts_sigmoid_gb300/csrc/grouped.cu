@@ -53,7 +53,12 @@ constexpr uint32_t kABytes = kHalf * kBK * 2;
 constexpr int kAcc = 2;                             // TMEM accumulators of 256 columns
 constexpr int kMaxStages = 12;
 constexpr int kMaxGroups = 1024;
-constexpr uint32_t kStageBox = 32 * 128;            // the epilogue's box of a gradient of weights
+// shared memory of the epilogue: a box of 32 tokens x 128 bf16 features for each column half, or for
+// each warp one of 32 rows x 128 bytes of a gradient of weights
+constexpr uint32_t kRowBox = 32 * 256, kWeightBox = 32 * 128;
+__host__ __device__ constexpr uint32_t out_bytes(int mode) {
+  return mode == kWeights ? kEpiWarps * kWeightBox : 2 * kRowBox;
+}
 
 struct Params {
   int E, mdim, depth, ncols;     // M side's extent; terms of a sum and (weights) N side's extent
@@ -157,9 +162,13 @@ __device__ __forceinline__ Tile tile_of(const Params& p, const Groups& t, int u)
       if (t.prefix[mid] <= i) lo = mid; else hi = mid - 1;
     }
     x.group = lo;
+    // an expert's rows in tiles of about the same size: a rest of a few rows would read all
+    // weights for them (none is empty: the rows are more than nt times one tile less)
     const int2 r = t.rows[lo];
-    x.row0 = r.x + (i - t.prefix[lo]) * p.nt;
-    x.rows = min(p.nt, r.y - x.row0);
+    const int tiles = t.prefix[lo + 1] - t.prefix[lo];
+    const int each = ((r.y - r.x + tiles - 1) / tiles + 31) & ~31;
+    x.row0 = r.x + (i - t.prefix[lo]) * each;
+    x.rows = min(each, r.y - x.row0);
     x.n0 = 0;
     x.n = (x.rows + 31) & ~31;
   }
@@ -199,19 +208,49 @@ __device__ void build_groups(const Params& p, const Groups& t, int* warp_sum) {
   }
 }
 
-// forward, rows: 32 token columns of TMEM lane = feature f into the rows of out.  Neighbouring
-// lanes swap halves, so that each stores two features of every second row.
-__device__ __forceinline__ void store_rows(const Params& p, const uint32_t (&v)[32], int row0, int valid,
-                                           int f, int lane) {
-  uint16_t* at = p.out + (long long)(row0 + (lane & 1)) * p.mdim + (f & ~1);
-  const bool in = f < p.mdim;                        // (mdim is even: both of a pair, or none)
+// The four epilogue warps of a column half meet.
+__device__ __forceinline__ void half_sync(int h) {
+  asm volatile("barrier.cta.sync %0, 128;" ::"r"(1 + h) : "memory");
+}
+// ... and agree whether all of them are to go on.
+__device__ __forceinline__ bool half_all(int h, bool ok) {
+  uint32_t r;
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.u32 p, %2, 0;\n\t"
+      "barrier.cta.red.and.pred q, %1, 128, p;\n\t"
+      "selp.u32 %0, 1, 0, q;\n\t}"
+      : "=r"(r)
+      : "r"(1 + h), "r"((uint32_t)ok)
+      : "memory");
+  return r != 0;
+}
+
+// forward, rows: 32 token columns of the CTA's 128 features into rows of out, by the four warps of a
+// half.  A lane has one feature of all tokens: neighbours swap halves, so that each holds two
+// features of every second token, and the box [32 tokens][128 features] in shared memory gives 256
+// bytes of a token's row to 16 lanes (the warps' own 64 bytes a row took 1.6 times as long).  Every
+// second row of the box has its 64-byte halves swapped, so that the pairs meet no bank twice.
+__device__ __forceinline__ void store_rows(const Params& p, uint8_t* box, const uint32_t (&v)[32],
+                                           int row0, int valid, int f0, int q, int h, int lane) {
+  half_sync(h);                                  // the box has been read
+  uint8_t* to = box + (lane & 1) * 256 + ((q ^ (lane & 1)) * 64 + (lane >> 1) * 4);
 #pragma unroll
   for (int j = 0; j < 32; j += 2) {
     const uint32_t own = pack_bf16x2(__uint_as_float(v[j]), __uint_as_float(v[j + 1]));
     const uint32_t other = __shfl_xor_sync(0xFFFFFFFFu, own, 1);
     // even lane: row j, features f, f + 1 = own low, other low; odd: row j + 1, other high, own high
     const uint32_t two = lane & 1 ? __byte_perm(other, own, 0x7632) : __byte_perm(own, other, 0x5410);
-    if (in && j + (lane & 1) < valid) *reinterpret_cast<uint32_t*>(at + (long long)j * p.mdim) = two;
+    *reinterpret_cast<uint32_t*>(to + j * 256) = two;
+  }
+  half_sync(h);
+  const int c = lane & 15, f = f0 + c * 8;       // (mdim % 8 == 0)
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 8 + q * 2 + (lane >> 4);
+    const uint4 w = *reinterpret_cast<const uint4*>(box + r * 256 + ((c ^ ((r & 1) << 2)) * 16));
+    if (r < valid && f < p.mdim)
+      *reinterpret_cast<uint4*>(p.out + (long long)(row0 + r) * p.mdim + f) = w;
   }
 }
 
@@ -240,8 +279,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));
-  uint8_t* boxes = smem + (size_t)p.stages * p.stage_bytes;           // (weights)
-  uint64_t* bars = reinterpret_cast<uint64_t*>(boxes + (kMode == kWeights ? kEpiWarps * kStageBox : 0));
+  uint8_t* boxes = smem + (size_t)p.stages * p.stage_bytes;
+  uint64_t* bars = reinterpret_cast<uint64_t*>(boxes + out_bytes(kMode));
   constexpr int kFull = 0, kEmpty = kMaxStages, kTfull = 2 * kMaxStages, kTempty = kTfull + kAcc,
                 kDone = kTempty + kAcc, kLast = kDone + 1, kBars = kLast + kMaxStages;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + kBars);
@@ -441,7 +480,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
     const uint32_t tempty = cluster_addr(bar_at(kTempty), 0);
     const uint32_t tmem = tmem_base + ((uint32_t)(q * 32) << 16);
     constexpr int kCols = kOut == 1 ? 64 : 32;   // (weights) columns of a box, one box a warp
-    uint8_t* box = boxes + (warp - kEpiWarp0) * kStageBox;
+    uint8_t* box = boxes + (kMode == kWeights ? (warp - kEpiWarp0) * kWeightBox : h * kRowBox);
     uint4 add[8];
     uint32_t acc = 0, aph = 0;
     bool ok = true;
@@ -457,16 +496,35 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
       if (!zero) {
         // (a wait's outcome is one for the warp, whose lanes meet again below)
         ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kTfull + (int)acc), aph, abort_flag, p.err, kErrEpilogue));
+        if constexpr (kMode != kWeights) ok = half_all(h, ok);     // (they meet again in store_rows)
         if (!ok) break;
         tc_fence_after();
       }
       if constexpr (kMode != kWeights) {
-        for (int c = h * 32; c < x.rows; c += 64) {
-          uint32_t v[32];
-          tmem_ld32(tmem + acc * kTile + c, v);
-          tmem_wait_ld32(v);
-          store_rows(p, v, x.row0 + c, x.rows - c, m + lane, lane);
+        // the next columns are on their way while these are written; behind the last the
+        // accumulator goes back
+        const uint32_t at = tmem + acc * kTile;
+        auto give_back = [&] {
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster(tempty + 8u * acc);
+        };
+        uint32_t va[32], vb[32];
+        int c = h * 32;
+        if (c < x.rows) tmem_ld32(at + c, va);
+        else give_back();
+        for (; c < x.rows; c += 128) {
+          tmem_wait_ld32(va);
+          if (c + 64 < x.rows) tmem_ld32(at + c + 64, vb);
+          else give_back();
+          store_rows(p, box, va, x.row0 + c, x.rows - c, x.m0 + (int)rank * kHalf, q, h, lane);
+          if (c + 64 >= x.rows) break;
+          tmem_wait_ld32(vb);
+          if (c + 128 < x.rows) tmem_ld32(at + c + 128, va);
+          else give_back();
+          store_rows(p, box, vb, x.row0 + c + 64, x.rows - c - 64, x.m0 + (int)rank * kHalf, q, h, lane);
         }
+        if (++acc == kAcc) { acc = 0; aph ^= 1u; }
       } else {
         const int c1 = (h + 1) * (x.n >> 1);
         for (int c = h * (x.n >> 1); c < c1; c += kCols) {
@@ -525,7 +583,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           }
         }
       }
-      if (!zero) {
+      if (kMode == kWeights && !zero) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive_cluster(tempty + 8u * acc);
@@ -573,7 +631,7 @@ constexpr size_t kMaxSmem = 227 * 1024;
 
 // shared memory of a launch but for its stages
 constexpr size_t other_smem(int mode, int E) {
-  return 1024 + (mode == kWeights ? (size_t)kEpiWarps * kStageBox : 0) +
+  return 1024 + out_bytes(mode) +
          (3 * kMaxStages + 2 * kAcc + 1) * 8 + 8 + (kThreads / 32) * 4 +
          (mode == kWeights ? 0 : (size_t)(3 * E + 1) * 4) + 16;
 }
