@@ -1440,7 +1440,8 @@ int lmoe_rms_norm_backward(const lmoe_bf16* grad_out, const lmoe_bf16* h, const 
                           grad_norm_w ? workspace : nullptr}))
     return LMOE_ERR_DEVICE;
   const NormBackward n{grad_out, h, norm_w, grad_residual, grad_h, grad_norm_w,
-                       static_cast<float*>(workspace), T, H, rms_eps};
+                       static_cast<float*>(workspace), T, H, rms_eps, device_error_word()};
+  if (!n.err) return LMOE_ERR_CUDA;
   LMOE_TRY(launch_norm_backward(n, (cudaStream_t)stream));
   return LMOE_OK;
 }

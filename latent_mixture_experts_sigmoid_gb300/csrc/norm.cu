@@ -12,6 +12,7 @@
 
 #include "fp8_quant.cuh"
 #include "norm.cuh"
+#include "tc_ptx.cuh"
 
 namespace lmoe {
 namespace {
@@ -67,6 +68,17 @@ __device__ __forceinline__ float range_scale(float sum, float H, float eps) {
   if (sum < H * 8.077935669463161e-28f && eps < 8.077935669463161e-28f)      // 2^-90
     return 1.2089258196146292e24f;                                            // 2^80
   return 1.0f;
+}
+
+constexpr int kMaxRing = 16;                     // rows of the gradient's ring
+constexpr int kErrNormRow = 4;                   // device error word: a row did not arrive
+
+// A bounded wait, about two seconds.
+__device__ __forceinline__ bool wait_row(uint32_t bar, uint32_t parity) {
+  if (mbar_try_wait(bar, parity)) return true;
+  for (int n = 0; n < (1 << 21); ++n)
+    if (mbar_try_wait_ns(bar, parity, 1000u)) return true;
+  return false;
 }
 
 // kVec: 16-byte vectors a thread, vector i at column 8 (i threads + thread).  kWarpRow: a warp a
@@ -155,39 +167,103 @@ norm_kernel(const NormForward p) {
   }
 }
 
-// The gradient.  CTAs walk the rows; a thread keeps its columns' part of grad_w in registers and
-// leaves it in the workspace, one row of it a CTA (kWarpRow: a warp), summed in order by the
-// second kernel.
+// The gradient.  Walkers (CTAs, or warps for short rows) take every so-manieth row; a thread keeps
+// its columns' part of grad_w in registers and leaves it in the workspace, a row of it a walker,
+// which the join sums in order.
+
+// a thread's sums of h^2 and of g h, h scaled by s
+template <int kVec>
+__device__ __forceinline__ float2 sums_of(const uint4 (&hv)[kVec], const uint4 (&dv)[kVec],
+                                          const uint4 (&wv)[kVec], float s) {
+  float2 sum = make_float2(0.0f, 0.0f);
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    float h[8], d[8], w[8];
+    widen(hv[i], h);
+    widen(dv[i], d);
+    widen(wv[i], w);
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const float v = h[e] * s;
+      sum.x = fmaf(v, v, sum.x);
+      sum.y = fmaf(d[e] * w[e], v, sum.y);
+    }
+  }
+  return sum;
+}
+
+// n = (h s) r (not h (s r): s r may leave the range where the squares did);
+// grad_h = grad_residual + s r (g - n k), k = mean(g n)
+struct RowFactors {
+  float s, r, k;
+};
 template <int kVec, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? 256 : 512)
-norm_backward_kernel(const NormBackward p) {
-  __shared__ float2 slots[4][32];
-  pdl_trigger();
-  const int nt = kWarpRow ? 32 : (int)blockDim.x;
-  const int t = kWarpRow ? (int)threadIdx.x & 31 : (int)threadIdx.x;
-  const int per = kWarpRow ? (int)blockDim.x >> 5 : 1;
-  const int walker = kWarpRow ? (int)blockIdx.x * per + (int)(threadIdx.x >> 5) : (int)blockIdx.x;
-  const int walkers = (int)gridDim.x * per;
-  const int nvec = p.H >> 3;
-  pdl_wait();
-  float acc[kVec][8];
-  uint4 wv[kVec];
+__device__ __forceinline__ RowFactors factors_of(const uint4 (&hv)[kVec], const uint4 (&dv)[kVec],
+                                                 const uint4 (&wv)[kVec], float H, float eps,
+                                                 float2* slots, float2* more_slots) {
+  float2 sum = row_sum<kWarpRow>(sums_of<kVec>(hv, dv, wv, 1.0f), slots);
+  const float s = range_scale(sum.x, H, eps);    // (one for the row)
+  if (s != 1.0f) {
+    sum = row_sum<kWarpRow>(sums_of<kVec>(hv, dv, wv, s), more_slots);
+    eps = eps * s * s;
+  }
+  const float r = 1.0f / sqrtf(sum.x / H + eps);
+  return {s, r, sum.y * r / H};
+}
+
+__device__ __forceinline__ uint4 grad_of(const uint4& hv, const uint4& dv, const uint4& wv, const uint4& rv,
+                                         const RowFactors& f, float (&acc)[8]) {
+  float h[8], d[8], w[8], q[8];
+  widen(hv, h);
+  widen(dv, d);
+  widen(wv, w);
+  widen(rv, q);
+  const float sr = f.s * f.r;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const float n = h[e] * f.s * f.r;
+    acc[e] = fmaf(d[e], n, acc[e]);
+    q[e] = fmaf(sr, fmaf(-n, f.k, d[e] * w[e]), q[e]);
+  }
+  return narrow(q);
+}
+
+template <int kVec>
+__device__ __forceinline__ void store_partial(const NormBackward& p, int walker, int t, int nt,
+                                              const float (&acc)[kVec][8]) {
+  if (!p.dw) return;
+  float* part = p.partial + (long long)walker * p.H;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int j = i * nt + t;
-    wv[i] = make_uint4(0, 0, 0, 0);
-    if (j < nvec) wv[i] = p.w ? *reinterpret_cast<const uint4*>(p.w + 8 * j) : kOnes;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) acc[i][e] = 0.0f;
+    if (j < p.H >> 3) {
+      *reinterpret_cast<float4*>(part + 8 * j) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      *reinterpret_cast<float4*>(part + 8 * j + 4) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    }
   }
-  const float H = (float)p.H;
-  int flip = 0;
-  for (long long row = walker; row < p.T; row += walkers, flip ^= 1) {
+}
+
+// Short rows: a warp a row.
+template <int kVec>
+__global__ void __launch_bounds__(256)
+norm_backward_warp_kernel(const NormBackward p) {
+  pdl_trigger();
+  const int t = (int)threadIdx.x & 31, per = (int)blockDim.x >> 5, nvec = p.H >> 3;
+  const int walker = (int)blockIdx.x * per + (int)(threadIdx.x >> 5), walkers = (int)gridDim.x * per;
+  pdl_wait();
+  float acc[kVec][8] = {};
+  uint4 wv[kVec];
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int j = i * 32 + t;
+    wv[i] = j >= nvec ? make_uint4(0, 0, 0, 0) : p.w ? *reinterpret_cast<const uint4*>(p.w + 8 * j) : kOnes;
+  }
+  for (long long row = walker; row < p.T; row += walkers) {
     const long long base = row * p.H;
     uint4 dv[kVec], hv[kVec], rv[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      const int j = i * nt + t;
+      const int j = i * 32 + t;
       dv[i] = hv[i] = rv[i] = make_uint4(0, 0, 0, 0);
       if (j < nvec) {
         hv[i] = ld_stream(p.h + base + 8 * j);
@@ -195,94 +271,127 @@ norm_backward_kernel(const NormBackward p) {
         if (p.dres) rv[i] = ld_stream(p.dres + base + 8 * j);
       }
     }
-    float2 sum = make_float2(0.0f, 0.0f);        // of h^2 and of g h
+    const RowFactors f = factors_of<kVec, true>(hv, dv, wv, (float)p.H, p.eps, nullptr, nullptr);
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      float h[8], d[8], w[8];
-      widen(hv[i], h);
-      widen(dv[i], d);
-      widen(wv[i], w);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        sum.x = fmaf(h[e], h[e], sum.x);
-        sum.y = fmaf(d[e] * w[e], h[e], sum.y);
-      }
+      const int j = i * 32 + t;
+      const uint4 o = grad_of(hv[i], dv[i], wv[i], rv[i], f, acc[i]);
+      if (j < nvec) *reinterpret_cast<uint4*>(p.dh + base + 8 * j) = o;
     }
-    sum = row_sum<kWarpRow>(sum, slots[flip]);
-    float eps = p.eps;
-    const float s = range_scale(sum.x, H, eps);
-    if (s != 1.0f) {
-      sum = make_float2(0.0f, 0.0f);
-#pragma unroll
-      for (int i = 0; i < kVec; ++i) {
-        float h[8], d[8], w[8];
-        widen(hv[i], h);
-        widen(dv[i], d);
-        widen(wv[i], w);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const float v = h[e] * s;
-          sum.x = fmaf(v, v, sum.x);
-          sum.y = fmaf(d[e] * w[e], v, sum.y);
-        }
-      }
-      sum = row_sum<kWarpRow>(sum, slots[2 + flip]);
-      eps = eps * s * s;
-    }
-    const float r = 1.0f / sqrtf(sum.x / H + eps);
-    const float k = sum.y * r / H, sr = s * r;
+  }
+  store_partial<kVec>(p, walker, t, 32, acc);
+}
+
+// Long rows: a CTA a row.  Its next rows (of h, grad_out and grad_residual) are on their way into a
+// ring in shared memory meanwhile, as bulk copies that one thread issues: their bytes in flight do
+// not depend on how many warps the registers leave room for.  The barrier of a row's sums says that
+// the slot of the row before has been read.
+template <int kVec>
+__global__ void __launch_bounds__(kVec == 4 ? 512 : 1024 / kVec)
+norm_backward_kernel(const NormBackward p, int stages) {
+  extern __shared__ __align__(128) uint8_t ring[];
+  __shared__ float2 slots[4][32];
+  __shared__ uint64_t bars[kMaxRing];
+  __shared__ int abort_flag;
+  pdl_trigger();
+  const int nt = (int)blockDim.x, t = (int)threadIdx.x, nvec = p.H >> 3;
+  const uint32_t row_bytes = (uint32_t)p.H * 2, slot_bytes = row_bytes * (p.dres ? 3 : 2);
+  if (t == 0) {
+    for (int i = 0; i < stages; ++i) mbar_init(smem_u32(&bars[i]), 1);
+    abort_flag = 0;
+    fence_proxy_async_smem();
+  }
+  pdl_wait();
+  __syncthreads();
+  long long next = blockIdx.x;                   // the next row to copy (thread 0)
+  auto copy = [&](int s) {
+    const uint32_t bar = smem_u32(&bars[s]), at = smem_u32(ring) + (uint32_t)s * slot_bytes;
+    mbar_arrive_expect_tx(bar, slot_bytes);
+    bulk_load(at, p.h + next * p.H, row_bytes, bar);
+    bulk_load(at + row_bytes, p.dy + next * p.H, row_bytes, bar);
+    if (p.dres) bulk_load(at + 2 * row_bytes, p.dres + next * p.H, row_bytes, bar);
+    next += gridDim.x;
+  };
+  if (t == 0)
+    for (int s = 0; s < stages && next < p.T; ++s) copy(s);
+  float acc[kVec][8] = {};
+  uint4 wv[kVec];
+  auto load_weights = [&] {
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
       const int j = i * nt + t;
-      float h[8], d[8], w[8], q[8];
-      widen(hv[i], h);
-      widen(dv[i], d);
-      widen(wv[i], w);
-      widen(rv[i], q);
+      wv[i] = j >= nvec ? make_uint4(0, 0, 0, 0) : p.w ? *reinterpret_cast<const uint4*>(p.w + 8 * j) : kOnes;
+    }
+  };
+  load_weights();
+  int s = 0, flip = 0;
+  uint32_t ph = 0;
+  for (long long row = blockIdx.x; row < p.T; row += gridDim.x, flip ^= 1) {
+    if (!wait_row(smem_u32(&bars[s]), ph)) {
+      atomicCAS(p.err, 0, kErrNormRow);
+      *(volatile int*)&abort_flag = 1;
+    }
+    const uint4* slot = reinterpret_cast<const uint4*>(ring + (size_t)s * slot_bytes);
+    uint4 dv[kVec], hv[kVec];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const float n = h[e] * s * r;
-        acc[i][e] = fmaf(d[e], n, acc[i][e]);
-        q[e] = fmaf(sr, fmaf(-n, k, d[e] * w[e]), q[e]);
+    for (int i = 0; i < kVec; ++i) {
+      const int j = i * nt + t;
+      dv[i] = hv[i] = make_uint4(0, 0, 0, 0);
+      if (j < nvec) {
+        hv[i] = slot[j];
+        dv[i] = slot[nvec + j];
       }
-      if (j < nvec) *reinterpret_cast<uint4*>(p.dh + base + 8 * j) = narrow(q);
     }
-  }
-  if (!p.dw) return;
-  float* part = p.partial + (long long)walker * p.H;
+    if constexpr (kVec == 4) load_weights();     // (kept, they spill)
+    const RowFactors f = factors_of<kVec, false>(hv, dv, wv, (float)p.H, p.eps, slots[flip], slots[2 + flip]);
+    if (*(volatile int*)&abort_flag) break;      // (set ahead of the barrier in factors_of: for all)
+    const int last = s ? s - 1 : stages - 1;
+    if (t == 0 && row != blockIdx.x && next < p.T) copy(last);
 #pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int j = i * nt + t;
-    if (j < nvec) {
-      *reinterpret_cast<float4*>(part + 8 * j) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-      *reinterpret_cast<float4*>(part + 8 * j + 4) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    for (int i = 0; i < kVec; ++i) {
+      const int j = i * nt + t;
+      if (j < nvec) {
+        const uint4 rv = p.dres ? slot[2 * nvec + j] : make_uint4(0, 0, 0, 0);
+        *reinterpret_cast<uint4*>(p.dh + row * p.H + 8 * j) = grad_of(hv[i], dv[i], wv[i], rv, f, acc[i]);
+      }
     }
+    if (++s == stages) { s = 0; ph ^= 1u; }
   }
+  if (abort_flag) {
+    // copies may still be under way: the CTA does not leave before they have landed, or a bound
+    for (int i = 0; i < stages; ++i) wait_row(smem_u32(&bars[i]), i < s ? ph ^ 1u : ph);
+    return;
+  }
+  store_partial<kVec>(p, (int)blockIdx.x, t, nt, acc);
 }
 
-// grad_w: 32 columns a CTA, each of its warps a run of the partial rows, then the warps' sums in order.
+// grad_w: 32 columns a CTA, eight lanes of them four each, each quarter of its warps a run of the
+// partial rows; then the quarters' sums in order.
 constexpr int kJoinWarps = 16;
 __global__ void __launch_bounds__(kJoinWarps * 32)
 norm_join_kernel(const float* __restrict__ partial, int parts, int H, float* __restrict__ dw) {
-  __shared__ float sums[kJoinWarps][32];
+  __shared__ float4 sums[kJoinWarps * 4][8];
   pdl_trigger();
   pdl_wait();
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int col = blockIdx.x * 32 + lane;
-  const int each = (parts + kJoinWarps - 1) / kJoinWarps;
-  const int p0 = warp * each, p1 = min(p0 + each, parts);
-  float v = 0.0f;
+  const int run = threadIdx.x >> 3, c = threadIdx.x & 7;
+  const int col = blockIdx.x * 32 + c * 4;
+  const int each = (parts + kJoinWarps * 4 - 1) / (kJoinWarps * 4);
+  const int p0 = run * each, p1 = min(p0 + each, parts);
+  float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (col < H) {
 #pragma unroll 8
-    for (int p = p0; p < p1; ++p) v += partial[(long long)p * H + col];
+    for (int p = p0; p < p1; ++p) {
+      const float4 a = *reinterpret_cast<const float4*>(partial + (long long)p * H + col);
+      v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+    }
   }
-  sums[warp][lane] = v;
+  sums[run][c] = v;
   __syncthreads();
-  if (warp == 0 && col < H) {
-    v = 0.0f;
-#pragma unroll
-    for (int i = 0; i < kJoinWarps; ++i) v += sums[i][lane];
-    dw[col] = v;
+  if (threadIdx.x < 32 && blockIdx.x * 32 + threadIdx.x < H) {
+    float a = 0.0f;
+#pragma unroll 16
+    for (int i = 0; i < kJoinWarps * 4; ++i) a += reinterpret_cast<const float*>(sums[i])[threadIdx.x];
+    dw[blockIdx.x * 32 + threadIdx.x] = a;
   }
 }
 
@@ -291,20 +400,61 @@ int round32(int n) { return (n + 31) / 32 * 32; }
 constexpr int kRowWarps = 8;                     // rows of a CTA with a warp a row
 constexpr int kWarpRowVec = 4;                   // vectors a lane up to which a warp takes a row
 
-// CTAs of the backward kernel (kWarpRow: kRowWarps walkers each)
-int backward_blocks(int T, int H) {
-  const bool warp_row = H <= 8 * 32 * kWarpRowVec;
-  const long long rows = warp_row ? ceil_div(T, kRowWarps) : T;
-  const long long most = 4ll * num_sms();
-  return (int)(rows < most ? rows : most);
+constexpr int kBackwardWarpVec = 2;              // ... of the gradient
+
+// How the gradient's kernel is launched.  Long rows: as many CTAs an SM as the registers (64 a thread
+// with one vector, 128 with more) leave room for, if their rings have three rows each; together
+// the rings take up to 216 KB.
+struct BackwardPlan {
+  bool warp_row;
+  int vec, threads, blocks, stages;
+  size_t smem;
+};
+BackwardPlan backward_plan(int T, int H, bool residual) {
+  BackwardPlan b{};
+  const int nvec = H / 8;
+  b.warp_row = nvec <= 32 * kBackwardWarpVec;
+  long long rows = T, per_sm = 4;
+  if (b.warp_row) {
+    b.vec = nvec <= 32 ? 1 : 2;
+    b.threads = 32 * kRowWarps;
+    rows = ceil_div(T, kRowWarps);
+  } else {
+    b.vec = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
+    b.threads = round32((nvec + b.vec - 1) / b.vec);
+    const size_t slot = (size_t)H * 2 * (residual ? 3 : 2), most = 216 * 1024;
+    per_sm = (b.vec == 1 ? 1024 : 512) / b.threads;
+    while (per_sm > 1 && most / per_sm < 3 * slot) --per_sm;
+    b.stages = (int)(most / per_sm / slot);
+    if (b.stages > kMaxRing) b.stages = kMaxRing;
+    b.smem = b.stages * slot;
+  }
+  const long long blocks = per_sm * num_sms();
+  b.blocks = (int)(rows < blocks ? rows : blocks);
+  return b;
+}
+
+template <int kVec>
+cudaError_t launch_backward(const NormBackward& n, const BackwardPlan& b, cudaStream_t s) {
+  if (b.warp_row)
+    return launch_k(norm_backward_warp_kernel<kVec == 4 ? 2 : kVec>, dim3(b.blocks), dim3(b.threads), 0, s, n);
+  const cudaError_t e = cudaFuncSetAttribute(norm_backward_kernel<kVec>,
+                                             cudaFuncAttributeMaxDynamicSharedMemorySize, 216 * 1024);
+  if (e != cudaSuccess) return e;
+  return launch_k(norm_backward_kernel<kVec>, dim3(b.blocks), dim3(b.threads), b.smem, s, n, b.stages);
 }
 
 }  // namespace
 
 size_t norm_backward_workspace_bytes(int T, int H) {
-  const int per = H <= 8 * 32 * kWarpRowVec ? kRowWarps : 1;
-  const size_t n = (size_t)backward_blocks(T, H) * per * H * sizeof(float);
-  return (n + 255) & ~size_t(255);
+  // (without grad_residual there may be more CTAs)
+  size_t walkers = 0;
+  for (bool residual : {false, true}) {
+    const BackwardPlan b = backward_plan(T, H, residual);
+    const size_t w = (size_t)b.blocks * (b.warp_row ? kRowWarps : 1);
+    walkers = w > walkers ? w : walkers;
+  }
+  return (walkers * H * sizeof(float) + 255) & ~size_t(255);
 }
 
 cudaError_t launch_norm(const NormForward& n, cudaStream_t s) {
@@ -323,25 +473,13 @@ cudaError_t launch_norm(const NormForward& n, cudaStream_t s) {
 }
 
 cudaError_t launch_norm_backward(const NormBackward& n, cudaStream_t s) {
-  const int nvec = n.H / 8, blocks = backward_blocks(n.T, n.H);
-  int parts = blocks;
-  cudaError_t e;
-  if (nvec <= 32 * kWarpRowVec) {
-    const dim3 block(32 * kRowWarps);
-    parts *= kRowWarps;
-    if (nvec <= 32) e = launch_k(norm_backward_kernel<1, true>, dim3(blocks), block, 0, s, n);
-    else if (nvec <= 64) e = launch_k(norm_backward_kernel<2, true>, dim3(blocks), block, 0, s, n);
-    else e = launch_k(norm_backward_kernel<4, true>, dim3(blocks), block, 0, s, n);
-  } else if (nvec <= 512) {
-    e = launch_k(norm_backward_kernel<1, false>, dim3(blocks), dim3(round32(nvec)), 0, s, n);
-  } else if (nvec <= 1024) {
-    e = launch_k(norm_backward_kernel<2, false>, dim3(blocks), dim3(round32((nvec + 1) / 2)), 0, s, n);
-  } else {
-    e = launch_k(norm_backward_kernel<4, false>, dim3(blocks), dim3(round32((nvec + 3) / 4)), 0, s, n);
-  }
+  const BackwardPlan b = backward_plan(n.T, n.H, n.dres != nullptr);
+  const cudaError_t e = b.vec == 1   ? launch_backward<1>(n, b, s)
+                        : b.vec == 2 ? launch_backward<2>(n, b, s)
+                                     : launch_backward<4>(n, b, s);
   if (e != cudaSuccess || !n.dw) return e;
   return launch_k(norm_join_kernel, dim3(ceil_div(n.H, 32)), dim3(kJoinWarps * 32), 0, s,
-                  (const float*)n.partial, parts, n.H, n.dw);
+                  (const float*)n.partial, b.blocks * (b.warp_row ? kRowWarps : 1), n.H, n.dw);
 }
 
 }  // namespace lmoe

@@ -32,6 +32,7 @@ struct NormBackward {
   float* partial;              // workspace, with dw
   int T, H;
   float eps;
+  int* err;                    // the device error word
 };
 
 size_t norm_backward_workspace_bytes(int T, int H);

@@ -68,6 +68,14 @@ __device__ __forceinline__ void st_global32(void* p, const uint32_t (&w)[8]) {
                : "memory");
 }
 
+// `bytes` (a multiple of 16) consecutive bytes, both addresses 16-byte aligned
+__device__ __forceinline__ void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
+  asm volatile(
+      "cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+      "l"(src), "r"(bytes), "r"(bar)
+      : "memory");
+}
+
 __device__ __forceinline__ void tma_load_2d(const CUtensorMap* map, uint32_t dst, uint32_t bar,
                                             int c0, int c1) {
   asm volatile(
