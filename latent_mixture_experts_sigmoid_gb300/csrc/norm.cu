@@ -38,26 +38,28 @@ __device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
 
 constexpr uint4 kOnes = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};   // bf16 1.0
 
-// Sums over a row of two values at a time: a warp's rows by shuffles alone, a block's through
-// one slot a warp (the caller alternates two slots, so that one barrier a sum is enough).
-template <bool kWarpRow>
-__device__ __forceinline__ float2 row_sum(float2 v, float2* slots) {
+// Sums over a row of kN values at a time: those of a row of kLanes lanes by shuffles alone, of a
+// CTA's row (kLanes = 0) through one slot a warp (the caller alternates two slots, so that one
+// barrier a sum is enough).
+template <int kLanes, int kN>
+__device__ __forceinline__ void row_sum(float (&v)[kN], float (*slots)[2]) {
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    v.x += __shfl_xor_sync(kAll, v.x, o);
-    v.y += __shfl_xor_sync(kAll, v.y, o);
-  }
-  if (kWarpRow) return v;
-  const int lane = threadIdx.x & 31, warps = (int)blockDim.x >> 5;
-  if (lane == 0) slots[threadIdx.x >> 5] = v;
-  __syncthreads();
-  v = lane < warps ? slots[lane] : make_float2(0.0f, 0.0f);
+  for (int o = (kLanes ? kLanes : 32) / 2; o; o >>= 1)
 #pragma unroll
-  for (int o = 16; o; o >>= 1) {
-    v.x += __shfl_xor_sync(kAll, v.x, o);
-    v.y += __shfl_xor_sync(kAll, v.y, o);
+    for (int n = 0; n < kN; ++n) v[n] += __shfl_xor_sync(kAll, v[n], o);
+  if constexpr (kLanes == 0) {
+    const int lane = threadIdx.x & 31, warps = (int)blockDim.x >> 5;
+    if (lane == 0)
+#pragma unroll
+      for (int n = 0; n < kN; ++n) slots[threadIdx.x >> 5][n] = v[n];
+    __syncthreads();
+#pragma unroll
+    for (int n = 0; n < kN; ++n) v[n] = lane < warps ? slots[lane][n] : 0.0f;
+#pragma unroll
+    for (int o = 16; o; o >>= 1)
+#pragma unroll
+      for (int n = 0; n < kN; ++n) v[n] += __shfl_xor_sync(kAll, v[n], o);
   }
-  return v;
 }
 
 // Where the squares of a row leave the range of fp32, the row is scaled by a power of two first:
@@ -81,21 +83,22 @@ __device__ __forceinline__ bool wait_row(uint32_t bar, uint32_t parity) {
   return false;
 }
 
-// kVec: 16-byte vectors a thread, vector i at column 8 (i threads + thread).  kWarpRow: a warp a
-// row, blockDim.x / 32 rows a CTA; else a CTA a row.
-template <int kVec, bool kWarpRow>
-__global__ void __launch_bounds__(kWarpRow ? 256 : kVec == 4 ? 512 : 1024)
+// kVec: 16-byte vectors a thread, vector i at column 8 (i threads + thread).  kLanes: lanes a row,
+// blockDim.x / kLanes rows a CTA; 0: a CTA a row.
+// [4096, 7168] with residual and both outputs: @FWD@
+template <int kVec, int kLanes>
+__global__ void __launch_bounds__(kLanes ? 256 : kVec == 4 ? 512 : 1024)
 norm_kernel(const NormForward p) {
-  __shared__ float2 slots[2][32];
+  __shared__ float slots[2][32][2];
   pdl_trigger();
-  const int nt = kWarpRow ? 32 : (int)blockDim.x;
-  const int t = kWarpRow ? (int)threadIdx.x & 31 : (int)threadIdx.x;
-  const long long row = kWarpRow ? (long long)blockIdx.x * (blockDim.x >> 5) + (threadIdx.x >> 5)
-                                 : (long long)blockIdx.x;
-  pdl_wait();
-  if (row >= p.T) return;                        // (a warp, or none of a CTA)
-  const int nvec = p.H >> 3;
+  const int nt = kLanes ? kLanes : (int)blockDim.x;
+  const int t = kLanes ? (int)threadIdx.x % nt : (int)threadIdx.x;
+  const long long row = kLanes ? (long long)blockIdx.x * (blockDim.x / nt) + threadIdx.x / nt
+                               : (long long)blockIdx.x;
+  const bool there = row < p.T;                  // (lanes of a row that is not there stay for the shuffles)
+  const int nvec = there ? p.H >> 3 : 0;
   const long long base = row * p.H;
+  pdl_wait();
   uint4 a[kVec], b[kVec], wv[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
@@ -108,63 +111,81 @@ norm_kernel(const NormForward p) {
     }
   }
   float h[kVec][8];
-  float2 sum = make_float2(0.0f, 0.0f);
+  float sum[1] = {0.0f};
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
-    float r[8];
     widen(a[i], h[i]);
-    widen(b[i], r);
+    if (p.residual) {                            // (not -0 + 0)
+      float r[8];
+      widen(b[i], r);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      if (p.residual) h[i][e] += r[e];           // (not -0 + 0)
-      sum.x = fmaf(h[i][e], h[i][e], sum.x);
+      for (int e = 0; e < 8; ++e) h[i][e] += r[e];
     }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[0] = fmaf(h[i][e], h[i][e], sum[0]);
     const int j = i * nt + t;
     if (p.h && j < nvec) *reinterpret_cast<uint4*>(p.h + base + 8 * j) = narrow(h[i]);
   }
-  sum = row_sum<kWarpRow>(sum, slots[0]);
+  row_sum<kLanes, 1>(sum, slots[0]);
   const float H = (float)p.H;
   float eps = p.eps;
-  const float s = range_scale(sum.x, H, eps);    // (one for the row)
-  if (s != 1.0f) {
-    sum = make_float2(0.0f, 0.0f);
+  const float s = range_scale(sum[0], H, eps);   // (one for the row)
+  const bool scaled = s != 1.0f;
+  if (kLanes == 32 || kLanes == 0 ? scaled : __any_sync(kAll, scaled)) {
+    float more[1] = {0.0f};
 #pragma unroll
     for (int i = 0; i < kVec; ++i)
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         h[i][e] *= s;
-        sum.x = fmaf(h[i][e], h[i][e], sum.x);
+        more[0] = fmaf(h[i][e], h[i][e], more[0]);
       }
-    sum = row_sum<kWarpRow>(sum, slots[1]);
+    row_sum<kLanes, 1>(more, slots[1]);
+    sum[0] = more[0];
     eps = eps * s * s;
   }
-  const float r = 1.0f / sqrtf(sum.x / H + eps);
+  const float r = 1.0f / sqrtf(sum[0] / H + eps);
+  uint32_t m[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int j = i * nt + t;
     float w[8];
     widen(wv[i], w);
-    uint32_t m = 0;
+    m[i] = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       h[i][e] = h[i][e] * r * w[e];
-      m = max(m, abs_bits(h[i][e]));
+      m[i] = max(m[i], abs_bits(h[i][e]));
     }
+    if (j >= nvec) m[i] = 0;
     if (p.out && j < nvec) *reinterpret_cast<uint4*>(p.out + base + 8 * j) = narrow(h[i]);
-    if (p.codes) {
-      if (j >= nvec) m = 0;
+  }
+  if (!p.codes) return;
+  // sixteen lanes (or the row's) hold the blocks that their vectors belong to; lane i of them takes
+  // the divisions of block i for all
+  constexpr int kGroup = kLanes && kLanes < 16 ? kLanes : 16;
+  uint32_t mine = m[0];
 #pragma unroll
-      for (int o = 1; o < 16; o <<= 1) m = max(m, __shfl_xor_sync(kAll, m, o));
-      const BlockScale bs = block_scale(m);
-      if (j < nvec) {
-        uint2 c;
-        c.x = pack_e4m3x4(h[i][0] * bs.inv, h[i][1] * bs.inv, h[i][2] * bs.inv, h[i][3] * bs.inv);
-        c.y = pack_e4m3x4(h[i][4] * bs.inv, h[i][5] * bs.inv, h[i][6] * bs.inv, h[i][7] * bs.inv);
-        *reinterpret_cast<uint2*>(p.codes + base + 8 * j) = c;
-        if ((j & 15) == 0) p.scales[row * ((p.H + 127) >> 7) + (j >> 4)] = bs.scale;
-      }
+  for (int i = 0; i < kVec; ++i) {
+#pragma unroll
+    for (int o = 1; o < kGroup; o <<= 1) m[i] = max(m[i], __shfl_xor_sync(kAll, m[i], o));
+    if (t % kGroup == i) mine = m[i];
+  }
+  const BlockScale bs = block_scale(mine);
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int j = i * nt + t;
+    const float inv = __shfl_sync(kAll, bs.inv, (threadIdx.x & 31 & ~(kGroup - 1)) + i);
+    if (j < nvec) {
+      uint2 c;
+      c.x = pack_e4m3x4(h[i][0] * inv, h[i][1] * inv, h[i][2] * inv, h[i][3] * inv);
+      c.y = pack_e4m3x4(h[i][4] * inv, h[i][5] * inv, h[i][6] * inv, h[i][7] * inv);
+      *reinterpret_cast<uint2*>(p.codes + base + 8 * j) = c;
     }
   }
+  // lane i: the scale of its group's block in vector i
+  const int i = t % kGroup, j = i * nt + (t - i);
+  if (i < kVec && j < nvec) p.scales[row * ((p.H + 127) >> 7) + (j >> 4)] = bs.scale;
 }
 
 // The gradient.  Walkers (CTAs, or warps for short rows) take every so-manieth row; a thread keeps
@@ -173,9 +194,9 @@ norm_kernel(const NormForward p) {
 
 // a thread's sums of h^2 and of g h, h scaled by s
 template <int kVec>
-__device__ __forceinline__ float2 sums_of(const uint4 (&hv)[kVec], const uint4 (&dv)[kVec],
-                                          const uint4 (&wv)[kVec], float s) {
-  float2 sum = make_float2(0.0f, 0.0f);
+__device__ __forceinline__ void sums_of(float (&sum)[2], const uint4 (&hv)[kVec], const uint4 (&dv)[kVec],
+                                        const uint4 (&wv)[kVec], float s) {
+  sum[0] = sum[1] = 0.0f;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     float h[8], d[8], w[8];
@@ -185,11 +206,10 @@ __device__ __forceinline__ float2 sums_of(const uint4 (&hv)[kVec], const uint4 (
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
       const float v = h[e] * s;
-      sum.x = fmaf(v, v, sum.x);
-      sum.y = fmaf(d[e] * w[e], v, sum.y);
+      sum[0] = fmaf(v, v, sum[0]);
+      sum[1] = fmaf(d[e] * w[e], v, sum[1]);
     }
   }
-  return sum;
 }
 
 // n = (h s) r (not h (s r): s r may leave the range where the squares did);
@@ -197,18 +217,22 @@ __device__ __forceinline__ float2 sums_of(const uint4 (&hv)[kVec], const uint4 (
 struct RowFactors {
   float s, r, k;
 };
-template <int kVec, bool kWarpRow>
+template <int kVec, int kLanes>
 __device__ __forceinline__ RowFactors factors_of(const uint4 (&hv)[kVec], const uint4 (&dv)[kVec],
                                                  const uint4 (&wv)[kVec], float H, float eps,
-                                                 float2* slots, float2* more_slots) {
-  float2 sum = row_sum<kWarpRow>(sums_of<kVec>(hv, dv, wv, 1.0f), slots);
-  const float s = range_scale(sum.x, H, eps);    // (one for the row)
-  if (s != 1.0f) {
-    sum = row_sum<kWarpRow>(sums_of<kVec>(hv, dv, wv, s), more_slots);
+                                                 float (*slots)[2], float (*more_slots)[2]) {
+  float sum[2];
+  sums_of<kVec>(sum, hv, dv, wv, 1.0f);
+  row_sum<kLanes, 2>(sum, slots);
+  const float s = range_scale(sum[0], H, eps);   // (one for the row)
+  const bool scaled = s != 1.0f;
+  if (kLanes == 32 || kLanes == 0 ? scaled : __any_sync(kAll, scaled)) {
+    sums_of<kVec>(sum, hv, dv, wv, s);
+    row_sum<kLanes, 2>(sum, more_slots);
     eps = eps * s * s;
   }
-  const float r = 1.0f / sqrtf(sum.x / H + eps);
-  return {s, r, sum.y * r / H};
+  const float r = 1.0f / sqrtf(sum[0] / H + eps);
+  return {s, r, sum[1] * r / H};
 }
 
 __device__ __forceinline__ uint4 grad_of(const uint4& hv, const uint4& dv, const uint4& wv, const uint4& rv,
@@ -243,43 +267,46 @@ __device__ __forceinline__ void store_partial(const NormBackward& p, int walker,
   }
 }
 
-// Short rows: a warp a row.
-template <int kVec>
+// Short rows: kLanes lanes a row.
+template <int kVec, int kLanes>
 __global__ void __launch_bounds__(256)
-norm_backward_warp_kernel(const NormBackward p) {
+norm_backward_short_kernel(const NormBackward p) {
   pdl_trigger();
-  const int t = (int)threadIdx.x & 31, per = (int)blockDim.x >> 5, nvec = p.H >> 3;
-  const int walker = (int)blockIdx.x * per + (int)(threadIdx.x >> 5), walkers = (int)gridDim.x * per;
+  const int t = (int)threadIdx.x % kLanes, per = (int)blockDim.x / kLanes, nvec = p.H >> 3;
+  const int walker = (int)blockIdx.x * per + (int)threadIdx.x / kLanes, walkers = (int)gridDim.x * per;
+  const int first = (int)blockIdx.x * per + (int)(threadIdx.x & ~31u) / kLanes;   // the warp's first walker
   pdl_wait();
   float acc[kVec][8] = {};
   uint4 wv[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
-    const int j = i * 32 + t;
+    const int j = i * kLanes + t;
     wv[i] = j >= nvec ? make_uint4(0, 0, 0, 0) : p.w ? *reinterpret_cast<const uint4*>(p.w + 8 * j) : kOnes;
   }
-  for (long long row = walker; row < p.T; row += walkers) {
-    const long long base = row * p.H;
+  for (long long r0 = first; r0 < p.T; r0 += walkers) {
+    const long long row = r0 + (walker - first), base = row * p.H;
+    const bool there = row < p.T;                // (the lanes of other rows of the warp go on)
     uint4 dv[kVec], hv[kVec], rv[kVec];
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      const int j = i * 32 + t;
+      const int j = i * kLanes + t;
       dv[i] = hv[i] = rv[i] = make_uint4(0, 0, 0, 0);
-      if (j < nvec) {
+      if (there && j < nvec) {
         hv[i] = ld_stream(p.h + base + 8 * j);
         dv[i] = ld_stream(p.dy + base + 8 * j);
         if (p.dres) rv[i] = ld_stream(p.dres + base + 8 * j);
       }
     }
-    const RowFactors f = factors_of<kVec, true>(hv, dv, wv, (float)p.H, p.eps, nullptr, nullptr);
+    const RowFactors f = factors_of<kVec, kLanes>(hv, dv, wv, (float)p.H, p.eps, nullptr, nullptr);
+    if (!there) continue;                        // (with eps = 0 its zeros would be NaN)
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
-      const int j = i * 32 + t;
+      const int j = i * kLanes + t;
       const uint4 o = grad_of(hv[i], dv[i], wv[i], rv[i], f, acc[i]);
       if (j < nvec) *reinterpret_cast<uint4*>(p.dh + base + 8 * j) = o;
     }
   }
-  store_partial<kVec>(p, walker, t, 32, acc);
+  store_partial<kVec>(p, walker, t, kLanes, acc);
 }
 
 // Long rows: a CTA a row.  Its next rows (of h, grad_out and grad_residual) are on their way into a
@@ -287,10 +314,10 @@ norm_backward_warp_kernel(const NormBackward p) {
 // not depend on how many warps the registers leave room for.  The barrier of a row's sums says that
 // the slot of the row before has been read.
 template <int kVec>
-__global__ void __launch_bounds__(kVec == 4 ? 512 : 1024 / kVec)
+__global__ void __launch_bounds__(512)
 norm_backward_kernel(const NormBackward p, int stages) {
   extern __shared__ __align__(128) uint8_t ring[];
-  __shared__ float2 slots[4][32];
+  __shared__ float slots[4][32][2];
   __shared__ uint64_t bars[kMaxRing];
   __shared__ int abort_flag;
   pdl_trigger();
@@ -343,7 +370,7 @@ norm_backward_kernel(const NormBackward p, int stages) {
       }
     }
     if constexpr (kVec == 4) load_weights();     // (kept, they spill)
-    const RowFactors f = factors_of<kVec, false>(hv, dv, wv, (float)p.H, p.eps, slots[flip], slots[2 + flip]);
+    const RowFactors f = factors_of<kVec, 0>(hv, dv, wv, (float)p.H, p.eps, slots[flip], slots[2 + flip]);
     if (*(volatile int*)&abort_flag) break;      // (set ahead of the barrier in factors_of: for all)
     const int last = s ? s - 1 : stages - 1;
     if (t == 0 && row != blockIdx.x && next < p.T) copy(last);
@@ -397,33 +424,43 @@ norm_join_kernel(const float* __restrict__ partial, int parts, int H, float* __r
 
 int round32(int n) { return (n + 31) / 32 * 32; }
 
-constexpr int kRowWarps = 8;                     // rows of a CTA with a warp a row
-constexpr int kWarpRowVec = 4;                   // vectors a lane up to which a warp takes a row
+constexpr int kShortThreads = 256;               // a CTA of several short rows
+// lanes that a short row takes, vectors a lane (of H <= 512; the forward's up to 1024)
+struct ShortRow {
+  int lanes, vec;
+};
+ShortRow short_row(int nvec) {
+  if (nvec <= 8) return {8, 1};
+  if (nvec <= 16) return {16, 1};
+  return {32, nvec <= 32 ? 1 : nvec <= 64 ? 2 : 4};
+}
+constexpr int kForwardShort = 128, kBackwardShort = 64;      // vectors
 
-constexpr int kBackwardWarpVec = 2;              // ... of the gradient
-
-// How the gradient's kernel is launched.  Long rows: as many CTAs an SM as the registers (64 a thread
-// with one vector, 128 with more) leave room for, if their rings have three rows each; together
-// the rings take up to 216 KB.
+// How the gradient's kernel is launched.  Long rows: as many CTAs of 512 threads together as the
+// registers (128 a thread) leave room for, if their rings have three rows each; together the rings
+// take up to 216 KB.
 struct BackwardPlan {
-  bool warp_row;
-  int vec, threads, blocks, stages;
+  int lanes, vec;              // lanes 0: long rows
+  int threads, blocks, walkers, stages;
   size_t smem;
 };
 BackwardPlan backward_plan(int T, int H, bool residual) {
   BackwardPlan b{};
   const int nvec = H / 8;
-  b.warp_row = nvec <= 32 * kBackwardWarpVec;
   long long rows = T, per_sm = 4;
-  if (b.warp_row) {
-    b.vec = nvec <= 32 ? 1 : 2;
-    b.threads = 32 * kRowWarps;
-    rows = ceil_div(T, kRowWarps);
+  int per = 1;
+  if (nvec <= kBackwardShort) {
+    const ShortRow r = short_row(nvec);
+    b.lanes = r.lanes;
+    b.vec = r.vec;
+    b.threads = kShortThreads;
+    per = kShortThreads / r.lanes;
+    rows = ceil_div(T, per);
   } else {
-    b.vec = nvec <= 256 ? 1 : nvec <= 1024 ? 2 : 4;
+    b.vec = nvec <= 1024 ? 2 : 4;
     b.threads = round32((nvec + b.vec - 1) / b.vec);
     const size_t slot = (size_t)H * 2 * (residual ? 3 : 2), most = 216 * 1024;
-    per_sm = (b.vec == 1 ? 1024 : 512) / b.threads;
+    per_sm = 512 / b.threads;
     while (per_sm > 1 && most / per_sm < 3 * slot) --per_sm;
     b.stages = (int)(most / per_sm / slot);
     if (b.stages > kMaxRing) b.stages = kMaxRing;
@@ -431,55 +468,60 @@ BackwardPlan backward_plan(int T, int H, bool residual) {
   }
   const long long blocks = per_sm * num_sms();
   b.blocks = (int)(rows < blocks ? rows : blocks);
+  b.walkers = b.blocks * per;
   return b;
 }
 
 template <int kVec>
-cudaError_t launch_backward(const NormBackward& n, const BackwardPlan& b, cudaStream_t s) {
-  if (b.warp_row)
-    return launch_k(norm_backward_warp_kernel<kVec == 4 ? 2 : kVec>, dim3(b.blocks), dim3(b.threads), 0, s, n);
+cudaError_t launch_long(const NormBackward& n, const BackwardPlan& b, cudaStream_t s) {
   const cudaError_t e = cudaFuncSetAttribute(norm_backward_kernel<kVec>,
                                              cudaFuncAttributeMaxDynamicSharedMemorySize, 216 * 1024);
   if (e != cudaSuccess) return e;
   return launch_k(norm_backward_kernel<kVec>, dim3(b.blocks), dim3(b.threads), b.smem, s, n, b.stages);
 }
 
+cudaError_t launch_backward(const NormBackward& n, const BackwardPlan& b, cudaStream_t s) {
+  const dim3 grid(b.blocks), block(b.threads);
+  if (b.lanes == 8) return launch_k(norm_backward_short_kernel<1, 8>, grid, block, 0, s, n);
+  if (b.lanes == 16) return launch_k(norm_backward_short_kernel<1, 16>, grid, block, 0, s, n);
+  if (b.lanes == 32)
+    return b.vec == 1 ? launch_k(norm_backward_short_kernel<1, 32>, grid, block, 0, s, n)
+                      : launch_k(norm_backward_short_kernel<2, 32>, grid, block, 0, s, n);
+  return b.vec == 2 ? launch_long<2>(n, b, s) : launch_long<4>(n, b, s);
+}
+
 }  // namespace
 
 size_t norm_backward_workspace_bytes(int T, int H) {
   // (without grad_residual there may be more CTAs)
-  size_t walkers = 0;
-  for (bool residual : {false, true}) {
-    const BackwardPlan b = backward_plan(T, H, residual);
-    const size_t w = (size_t)b.blocks * (b.warp_row ? kRowWarps : 1);
-    walkers = w > walkers ? w : walkers;
-  }
-  return (walkers * H * sizeof(float) + 255) & ~size_t(255);
+  const int a = backward_plan(T, H, false).walkers, b = backward_plan(T, H, true).walkers;
+  return ((size_t)(a > b ? a : b) * H * sizeof(float) + 255) & ~size_t(255);
 }
 
 cudaError_t launch_norm(const NormForward& n, cudaStream_t s) {
   const int nvec = n.H / 8;
-  if (nvec <= 32 * kWarpRowVec) {
-    const dim3 grid((unsigned)ceil_div(n.T, kRowWarps)), block(32 * kRowWarps);
-    if (nvec <= 32) return launch_k(norm_kernel<1, true>, grid, block, 0, s, n);
-    if (nvec <= 64) return launch_k(norm_kernel<2, true>, grid, block, 0, s, n);
-    return launch_k(norm_kernel<4, true>, grid, block, 0, s, n);
+  if (nvec <= kForwardShort) {
+    const ShortRow r = short_row(nvec);
+    const dim3 grid((unsigned)ceil_div(n.T, kShortThreads / r.lanes)), block(kShortThreads);
+    if (r.lanes == 8) return launch_k(norm_kernel<1, 8>, grid, block, 0, s, n);
+    if (r.lanes == 16) return launch_k(norm_kernel<1, 16>, grid, block, 0, s, n);
+    return r.vec == 1   ? launch_k(norm_kernel<1, 32>, grid, block, 0, s, n)
+           : r.vec == 2 ? launch_k(norm_kernel<2, 32>, grid, block, 0, s, n)
+                        : launch_k(norm_kernel<4, 32>, grid, block, 0, s, n);
   }
   const dim3 grid((unsigned)n.T);
   if (n.T <= 2 * num_sms())
-    return nvec <= 1024 ? launch_k(norm_kernel<1, false>, grid, dim3(round32(nvec)), 0, s, n)
-                        : launch_k(norm_kernel<2, false>, grid, dim3(round32((nvec + 1) / 2)), 0, s, n);
-  return launch_k(norm_kernel<4, false>, grid, dim3(round32((nvec + 3) / 4)), 0, s, n);
+    return nvec <= 1024 ? launch_k(norm_kernel<1, 0>, grid, dim3(round32(nvec)), 0, s, n)
+                        : launch_k(norm_kernel<2, 0>, grid, dim3(round32((nvec + 1) / 2)), 0, s, n);
+  return launch_k(norm_kernel<4, 0>, grid, dim3(round32((nvec + 3) / 4)), 0, s, n);
 }
 
 cudaError_t launch_norm_backward(const NormBackward& n, cudaStream_t s) {
   const BackwardPlan b = backward_plan(n.T, n.H, n.dres != nullptr);
-  const cudaError_t e = b.vec == 1   ? launch_backward<1>(n, b, s)
-                        : b.vec == 2 ? launch_backward<2>(n, b, s)
-                                     : launch_backward<4>(n, b, s);
+  const cudaError_t e = launch_backward(n, b, s);
   if (e != cudaSuccess || !n.dw) return e;
   return launch_k(norm_join_kernel, dim3(ceil_div(n.H, 32)), dim3(kJoinWarps * 32), 0, s,
-                  (const float*)n.partial, b.blocks * (b.warp_row ? kRowWarps : 1), n.H, n.dw);
+                  (const float*)n.partial, b.walkers, n.H, n.dw);
 }
 
 }  // namespace lmoe

@@ -96,81 +96,87 @@ int rows_for(int d) {
 
 // ---------------------------------------------------------------------------
 // Gradient.  With z = g / beta, s = sigmoid(g), v = u / linear_beta and the factors
-//   a = beta tanh(z) s,  b = linear_beta tanh(v)  (or u):   out = a b,
-//   grad_gate = dy b [ sech^2(z) s + beta tanh(z) s (1 - s) ],
-//   grad_up   = dy a sech^2(v)  (or dy a).
-// All of it comes from three exponentials of non-positive arguments and one reciprocal:
-//   q = e^{-2|z|}:  |tanh z| = (1 - q) / (1 + q),  sech^2 z = 4 q / (1 + q)^2
-//   p = e^{-|g|}:   s (1 - s) = p / (1 + p)^2,     s = 1 / (1 + p)  (g < 0: p / (1 + p))
-//   k = e^{-2|v|}:  as q
-// and 1 / ((1 + q)(1 + p)(1 + k)), whose divisor lies in [1, 8].  sech^2 = 1 - tanh^2 would
-// cancel where the activation saturates; these keep their relative accuracy.  1 - q cancels
-// for small z, where its cubic stands in.
+//   A = beta tanh(z),  b = linear_beta tanh(v)  (or u):   out = A s b,
+//   grad_gate = dy s b [ sech^2(z) + A (1 - s) ],
+//   grad_up   = dy s A sech^2(v)  (or dy s A).
+// Besides the two hardware tanh (as the forward's) all of it comes from three exponentials of
+// non-positive arguments and one reciprocal:
+//   q = e^{-2|z|}:  sech^2 z = 4 q / (1 + q)^2;   k = e^{-2|v|}: as q
+//   p = e^{-|g|}:   s and 1 - s are 1 / (1 + p) and p / (1 + p), the other way round for g < 0
+// and 1 / ((1 + q)(1 + p)(1 + k)), whose divisor lies in [1, 8].  sech^2 = 1 - tanh^2 and
+// 1 - s would cancel where the activation saturates; these keep their relative accuracy.
 // ---------------------------------------------------------------------------
+struct SituGradParams {
+  float beta, inv_beta, lbeta, inv_lbeta;
+  float ez, ev;                // -2 log2(e) / beta, / linear_beta: 2^(ez |g|) = q
+};
 
-// |tanh x| from m = |x|, q = e^{-2m} and r = 1 / (1 + q).  Below 2^-5 the first two terms of
-// the series (the third is 2 m^4 / 15 < 2^-22 of the first); from there on 1 - q has lost at
-// most five bits to cancellation.
-__device__ __forceinline__ float tanh_of(float m, float q, float r) {
-  return m < 0.03125f ? fmaf(m * m, m * -0.33333334f, m) : (1.0f - q) * r;
-}
-
+struct GradPair {
+  f32x2 gate, up;
+};
+// two elements: gate, up and grad_out as bf16 pairs
 template <bool kLinear>
-__device__ __forceinline__ float2 situ_grad(float g, float u, float dy, const SituParams& c) {
-  constexpr float kLog2e = 1.4426950408889634f;
-  const float z = fabsf(g) * c.inv_beta;
-  const float q = ex2_fast(z * (-2.0f * kLog2e)), p = ex2_fast(fabsf(g) * -kLog2e);
-  const float q1 = 1.0f + q, p1 = 1.0f + p;
-  float rq, rp, b = u, db = 1.0f;
+__device__ __forceinline__ GradPair situ_grad2(uint32_t g2, uint32_t u2, uint32_t dy2,
+                                               const SituGradParams& c) {
+  auto wide = [](uint32_t w) { return f2_make(w << 16, w & 0xFFFF0000u); };
+  const f32x2 one = f2_splat(1.0f);
+  const f32x2 g = wide(g2), ag = wide(g2 & 0x7FFF7FFFu), dy = wide(dy2);
+  const f32x2 q = LMOE_F2_APPLY(ex2_fast, f2_mul(ag, f2_splat(c.ez)));
+  const f32x2 p = LMOE_F2_APPLY(ex2_fast, f2_mul(ag, f2_splat(-1.4426950408889634f)));
+  const f32x2 q1 = f2_add(q, one), p1 = f2_add(p, one), qp = f2_mul(q1, p1);
+  f32x2 b = wide(u2), db = one, rqp;
   if constexpr (kLinear) {
-    const float v = fabsf(u) * c.inv_lbeta;
-    const float k = ex2_fast(v * (-2.0f * kLog2e)), k1 = 1.0f + k;
-    const float qp = q1 * p1;
-    const float r = rcp_fast(qp * k1);
-    const float rk = r * qp, rqp = r * k1;
-    rq = rqp * p1;
-    rp = rqp * q1;
-    b = copysignf(c.lbeta * tanh_of(v, k, rk), u);
-    db = 4.0f * k * rk * rk;
+    const f32x2 k = LMOE_F2_APPLY(ex2_fast, f2_mul(wide(u2 & 0x7FFF7FFFu), f2_splat(c.ev)));
+    const f32x2 k1 = f2_add(k, one);
+    const f32x2 r = LMOE_F2_APPLY(rcp_fast, f2_mul(qp, k1));
+    const f32x2 rk = f2_mul(r, qp), twice = f2_add(rk, rk);
+    rqp = f2_mul(r, k1);
+    db = f2_mul(f2_mul(twice, twice), k);
+    b = f2_mul(LMOE_F2_APPLY(tanh_fast, f2_mul(b, f2_splat(c.inv_lbeta))), f2_splat(c.lbeta));
   } else {
-    const float r = rcp_fast(q1 * p1);
-    rq = r * p1;
-    rp = r * q1;
+    rqp = LMOE_F2_APPLY(rcp_fast, qp);
   }
-  const float t = tanh_of(z, q, rq);                       // |tanh z|
-  const float s = g < 0.0f ? p * rp : rp;                  // sigmoid
-  const float sb = c.beta * t;
-  // beta tanh(z) s (1 - s), of g's sign, and sech^2(z) s
-  const float da = fmaf(4.0f * q * rq * rq, s, copysignf(sb * p * rp * rp, g));
-  return make_float2(dy * b * da, dy * copysignf(sb * s, g) * db);
+  const f32x2 rq = f2_mul(rqp, p1), rp = f2_mul(rqp, q1), pr = f2_mul(p, rp);
+  const f32x2 twice = f2_add(rq, rq);
+  const f32x2 sech2 = f2_mul(f2_mul(twice, twice), q);
+  const bool lo = f2_lo(g) < 0.0f, hi = f2_hi(g) < 0.0f;
+  const f32x2 s = f2_make(__float_as_uint(lo ? f2_lo(pr) : f2_lo(rp)), __float_as_uint(hi ? f2_hi(pr) : f2_hi(rp)));
+  const f32x2 t = f2_make(__float_as_uint(lo ? f2_lo(rp) : f2_lo(pr)), __float_as_uint(hi ? f2_hi(rp) : f2_hi(pr)));
+  const f32x2 A = f2_mul(LMOE_F2_APPLY(tanh_fast, f2_mul(g, f2_splat(c.inv_beta))), f2_splat(c.beta));
+  const f32x2 ds = f2_mul(dy, s);
+  GradPair o;
+  o.gate = f2_mul(f2_mul(ds, b), f2_fma(A, t, sech2));
+  o.up = f2_mul(ds, A);
+  if constexpr (kLinear) o.up = f2_mul(o.up, db);
+  return o;
 }
 
-// Eight elements a step: 48 bytes read, 32 written.  Bound by memory.
+// Eight elements a thread: 48 bytes read, 32 written; a CTA blockDim.y rows (blockIdx.x) of
+// 8 blockDim.x columns (blockIdx.y).
+// [65536, 2 x 512]: @SITU@
 template <bool kLinear>
 __global__ void __launch_bounds__(kThreads)
-situ_backward_kernel(const uint16_t* __restrict__ in, const uint16_t* __restrict__ dy,
-                     uint16_t* __restrict__ dx, long long total, int vpr, SituParams p) {
+situ_backward_kernel(const uint16_t* __restrict__ in, const uint16_t* __restrict__ dy, uint16_t* dx,
+                     long long N, int d, SituGradParams p) {
   pdl_trigger();
+  const long long row = (long long)blockIdx.x * blockDim.y + threadIdx.y;
+  const int c = (int)(blockIdx.y * blockDim.x + threadIdx.x) * 8;
   pdl_wait();
-  const long long j = (long long)blockIdx.x * kThreads + threadIdx.x;
-  if (j >= total) return;
-  const long long row = j / vpr;
-  const int c = (int)(j - row * vpr);
-  const long long at = (row * 2 * vpr + c) * 8;
+  if (row >= N || c >= d) return;
+  const long long at = row * 2 * d + c;
   const uint4 g = ld_stream(reinterpret_cast<const uint4*>(in + at));
-  const uint4 u = ld_stream(reinterpret_cast<const uint4*>(in + at + 8ll * vpr));
-  const uint4 d = ld_stream(reinterpret_cast<const uint4*>(dy + j * 8));
-  const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w}, dw[4] = {d.x, d.y, d.z, d.w};
+  const uint4 u = ld_stream(reinterpret_cast<const uint4*>(in + at + d));
+  const uint4 y = ld_stream(reinterpret_cast<const uint4*>(dy + row * d + c));
+  const uint32_t gw[4] = {g.x, g.y, g.z, g.w}, uw[4] = {u.x, u.y, u.z, u.w}, yw[4] = {y.x, y.y, y.z, y.w};
   uint32_t og[4], ou[4];
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const float2 lo = situ_grad<kLinear>(bf16_lo(gw[i]), bf16_lo(uw[i]), bf16_lo(dw[i]), p);
-    const float2 hi = situ_grad<kLinear>(bf16_hi(gw[i]), bf16_hi(uw[i]), bf16_hi(dw[i]), p);
-    og[i] = pack_bf16x2(lo.x, hi.x);
-    ou[i] = pack_bf16x2(lo.y, hi.y);
+    const GradPair o = situ_grad2<kLinear>(gw[i], uw[i], yw[i], p);
+    og[i] = pack_bf16x2(f2_lo(o.gate), f2_hi(o.gate));
+    ou[i] = pack_bf16x2(f2_lo(o.up), f2_hi(o.up));
   }
   *reinterpret_cast<uint4*>(dx + at) = make_uint4(og[0], og[1], og[2], og[3]);
-  *reinterpret_cast<uint4*>(dx + at + 8ll * vpr) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
+  *reinterpret_cast<uint4*>(dx + at + d) = make_uint4(ou[0], ou[1], ou[2], ou[3]);
 }
 
 }  // namespace
@@ -198,12 +204,13 @@ cudaError_t launch_masked_situ(const uint16_t* in, uint16_t* out, const int32_t*
 cudaError_t launch_situ_backward(const uint16_t* in, const uint16_t* dy, uint16_t* dx, long long N,
                                  int d, float beta, float lbeta, cudaStream_t s) {
   if (N <= 0) return cudaSuccess;
-  const SituParams p = make_situ_params(beta, lbeta);
-  const long long total = N * (d / 8);
-  const dim3 grid((unsigned)((total + kThreads - 1) / kThreads)), block(kThreads);
-  return p.has_lbeta
-             ? launch_k(situ_backward_kernel<true>, grid, block, 0, s, in, dy, dx, total, d / 8, p)
-             : launch_k(situ_backward_kernel<false>, grid, block, 0, s, in, dy, dx, total, d / 8, p);
+  const SituParams f = make_situ_params(beta, lbeta);
+  const float twice = -2.0f * 1.4426950408889634f;
+  const SituGradParams p{f.beta, f.inv_beta, f.lbeta, f.inv_lbeta, twice * f.inv_beta, twice * f.inv_lbeta};
+  const int vpr = d / 8, cols = ceil_div(vpr, kThreads), tx = ceil_div(vpr, cols);
+  const dim3 block(tx, kThreads / tx), grid((unsigned)((N + block.y - 1) / block.y), cols);
+  return f.has_lbeta ? launch_k(situ_backward_kernel<true>, grid, block, 0, s, in, dy, dx, N, d, p)
+                     : launch_k(situ_backward_kernel<false>, grid, block, 0, s, in, dy, dx, N, d, p);
 }
 
 }  // namespace lmoe
