@@ -26,6 +26,14 @@ __device__ __forceinline__ uint4 ld_stream(const uint16_t* p) {
   return v;
 }
 
+// a load that is not moved ahead of what is written before it
+__device__ __forceinline__ uint4 ld_here(const uint16_t* p) {
+  uint4 v;
+  asm volatile("ld.global.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+
 __device__ __forceinline__ void widen(const uint4& v, float (&f)[8]) {
   f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
   f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
@@ -87,7 +95,7 @@ __device__ __forceinline__ bool wait_row(uint32_t bar, uint32_t parity) {
 // blockDim.x / kLanes rows a CTA; 0: a CTA a row.
 // [4096, 7168] with residual and both outputs: @FWD@
 template <int kVec, int kLanes>
-__global__ void __launch_bounds__(kLanes ? 256 : kVec == 4 ? 512 : 1024)
+__global__ void __launch_bounds__(kLanes ? 256 : kVec == 4 ? 512 : 1024, kLanes == 0 && kVec == 4 ? 2 : 1)
 norm_kernel(const NormForward p) {
   __shared__ float slots[2][32][2];
   pdl_trigger();
@@ -103,11 +111,10 @@ norm_kernel(const NormForward p) {
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int j = i * nt + t;
-    a[i] = b[i] = wv[i] = make_uint4(0, 0, 0, 0);
+    a[i] = b[i] = make_uint4(0, 0, 0, 0);
     if (j < nvec) {
       a[i] = ld_stream(p.x + base + 8 * j);
       if (p.residual) b[i] = ld_stream(p.residual + base + 8 * j);
-      wv[i] = p.w ? *reinterpret_cast<const uint4*>(p.w + 8 * j) : kOnes;
     }
   }
   float h[kVec][8];
@@ -125,6 +132,12 @@ norm_kernel(const NormForward p) {
     for (int e = 0; e < 8; ++e) sum[0] = fmaf(h[i][e], h[i][e], sum[0]);
     const int j = i * nt + t;
     if (p.h && j < nvec) *reinterpret_cast<uint4*>(p.h + base + 8 * j) = narrow(h[i]);
+  }
+  // (asked for here: the registers of x and the residual are free again)
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int j = i * nt + t;
+    wv[i] = j >= nvec ? make_uint4(0, 0, 0, 0) : p.w ? ld_here(p.w + 8 * j) : kOnes;
   }
   row_sum<kLanes, 1>(sum, slots[0]);
   const float H = (float)p.H;
@@ -188,9 +201,9 @@ norm_kernel(const NormForward p) {
   if (i < kVec && j < nvec) p.scales[row * ((p.H + 127) >> 7) + (j >> 4)] = bs.scale;
 }
 
-// The gradient.  Walkers (CTAs, or warps for short rows) take every so-manieth row; a thread keeps
-// its columns' part of grad_w in registers and leaves it in the workspace, a row of it a walker,
-// which the join sums in order.
+// The gradient.  CTAs (of short rows: groups of lanes) take every so-manieth row; a thread keeps its
+// columns' part of grad_w in registers, each CTA leaves a row of it in the workspace, and the join
+// sums those in order.
 
 // a thread's sums of h^2 and of g h, h scaled by s
 template <int kVec>
@@ -252,21 +265,6 @@ __device__ __forceinline__ uint4 grad_of(const uint4& hv, const uint4& dv, const
   return narrow(q);
 }
 
-template <int kVec>
-__device__ __forceinline__ void store_partial(const NormBackward& p, int walker, int t, int nt,
-                                              const float (&acc)[kVec][8]) {
-  if (!p.dw) return;
-  float* part = p.partial + (long long)walker * p.H;
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int j = i * nt + t;
-    if (j < p.H >> 3) {
-      *reinterpret_cast<float4*>(part + 8 * j) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-      *reinterpret_cast<float4*>(part + 8 * j + 4) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
-    }
-  }
-}
-
 // Short rows: kLanes lanes a row.
 template <int kVec, int kLanes>
 __global__ void __launch_bounds__(256)
@@ -306,7 +304,23 @@ norm_backward_short_kernel(const NormBackward p) {
       if (j < nvec) *reinterpret_cast<uint4*>(p.dh + base + 8 * j) = o;
     }
   }
-  store_partial<kVec>(p, walker, t, kLanes, acc);
+  // the CTA's rows of sums as one, in order
+  if (!p.dw) return;
+  constexpr int kCols = kVec * kLanes * 8;
+  __shared__ float sums[256 / kLanes][kCols];
+#pragma unroll
+  for (int i = 0; i < kVec; ++i)
+#pragma unroll
+    for (int e = 0; e < 8; e += 4)
+      *reinterpret_cast<float4*>(&sums[threadIdx.x / kLanes][(i * kLanes + t) * 8 + e]) =
+          make_float4(acc[i][e], acc[i][e + 1], acc[i][e + 2], acc[i][e + 3]);
+  __syncthreads();
+  for (int c = threadIdx.x; c < p.H; c += 256) {
+    float v = 0.0f;
+#pragma unroll
+    for (int w = 0; w < 256 / kLanes; ++w) v += sums[w][c];
+    p.partial[(long long)blockIdx.x * p.H + c] = v;
+  }
 }
 
 // Long rows: a CTA a row.  Its next rows (of h, grad_out and grad_residual) are on their way into a
@@ -389,7 +403,16 @@ norm_backward_kernel(const NormBackward p, int stages) {
     for (int i = 0; i < stages; ++i) wait_row(smem_u32(&bars[i]), i < s ? ph ^ 1u : ph);
     return;
   }
-  store_partial<kVec>(p, (int)blockIdx.x, t, nt, acc);
+  if (!p.dw) return;
+  float* part = p.partial + (long long)blockIdx.x * p.H;
+#pragma unroll
+  for (int i = 0; i < kVec; ++i) {
+    const int j = i * nt + t;
+    if (j < nvec) {
+      *reinterpret_cast<float4*>(part + 8 * j) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
+      *reinterpret_cast<float4*>(part + 8 * j + 4) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
+    }
+  }
 }
 
 // grad_w: 32 columns a CTA, eight lanes of them four each, each quarter of its warps a run of the
@@ -441,21 +464,19 @@ constexpr int kForwardShort = 128, kBackwardShort = 64;      // vectors
 // take up to 216 KB.
 struct BackwardPlan {
   int lanes, vec;              // lanes 0: long rows
-  int threads, blocks, walkers, stages;
+  int threads, blocks, stages;
   size_t smem;
 };
 BackwardPlan backward_plan(int T, int H, bool residual) {
   BackwardPlan b{};
   const int nvec = H / 8;
   long long rows = T, per_sm = 4;
-  int per = 1;
   if (nvec <= kBackwardShort) {
     const ShortRow r = short_row(nvec);
     b.lanes = r.lanes;
     b.vec = r.vec;
     b.threads = kShortThreads;
-    per = kShortThreads / r.lanes;
-    rows = ceil_div(T, per);
+    rows = ceil_div(T, kShortThreads / r.lanes);
   } else {
     b.vec = nvec <= 1024 ? 2 : 4;
     b.threads = round32((nvec + b.vec - 1) / b.vec);
@@ -468,7 +489,6 @@ BackwardPlan backward_plan(int T, int H, bool residual) {
   }
   const long long blocks = per_sm * num_sms();
   b.blocks = (int)(rows < blocks ? rows : blocks);
-  b.walkers = b.blocks * per;
   return b;
 }
 
@@ -494,7 +514,7 @@ cudaError_t launch_backward(const NormBackward& n, const BackwardPlan& b, cudaSt
 
 size_t norm_backward_workspace_bytes(int T, int H) {
   // (without grad_residual there may be more CTAs)
-  const int a = backward_plan(T, H, false).walkers, b = backward_plan(T, H, true).walkers;
+  const int a = backward_plan(T, H, false).blocks, b = backward_plan(T, H, true).blocks;
   return ((size_t)(a > b ? a : b) * H * sizeof(float) + 255) & ~size_t(255);
 }
 
@@ -521,7 +541,7 @@ cudaError_t launch_norm_backward(const NormBackward& n, cudaStream_t s) {
   const cudaError_t e = launch_backward(n, b, s);
   if (e != cudaSuccess || !n.dw) return e;
   return launch_k(norm_join_kernel, dim3(ceil_div(n.H, 32)), dim3(kJoinWarps * 32), 0, s,
-                  (const float*)n.partial, b.walkers, n.H, n.dw);
+                  (const float*)n.partial, b.blocks, n.H, n.dw);
 }
 
 }  // namespace lmoe
