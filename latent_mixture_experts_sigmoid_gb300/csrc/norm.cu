@@ -44,6 +44,23 @@ __device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
                     pack_bf16x2(f[6], f[7]));
 }
 
+// four packed pairs of fp32
+__device__ __forceinline__ void widen2(const uint4& v, f32x2 (&f)[4]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = f2_make(w[i] << 16, w[i] & 0xFFFF0000u);
+}
+__device__ __forceinline__ uint4 narrow2(const f32x2 (&f)[4]) {
+  return make_uint4(pack_bf16x2(f2_lo(f[0]), f2_hi(f[0])), pack_bf16x2(f2_lo(f[1]), f2_hi(f[1])),
+                    pack_bf16x2(f2_lo(f[2]), f2_hi(f[2])), pack_bf16x2(f2_lo(f[3]), f2_hi(f[3])));
+}
+// the larger magnitude, NaN if one is
+__device__ __forceinline__ float max_abs(float a, float b) {
+  float m;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(m) : "f"(fabsf(a)), "f"(fabsf(b)));
+  return m;
+}
+
 constexpr uint4 kOnes = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};   // bf16 1.0
 
 // Sums over a row of kN values at a time: those of a row of kLanes lanes by shuffles alone, of a
@@ -94,7 +111,9 @@ __device__ __forceinline__ bool wait_row(uint32_t bar, uint32_t parity) {
 // kVec: 16-byte vectors a thread, vector i at column 8 (i threads + thread).  kLanes: lanes a row,
 // blockDim.x / kLanes rows a CTA; 0: a CTA a row.
 // [4096, 7168] with residual and both outputs: @FWD@
-template <int kVec, int kLanes>
+// (kRes: with a residual.  Packed fp32 throughout: at 29 instructions an element, one by one, the
+// kernel was bound by their issue.)
+template <int kVec, int kLanes, bool kRes>
 __global__ void __launch_bounds__(kLanes ? 256 : kVec == 4 ? 512 : 1024, kLanes == 0 && kVec == 4 ? 2 : 1)
 norm_kernel(const NormForward p) {
   __shared__ float slots[2][32][2];
@@ -103,98 +122,96 @@ norm_kernel(const NormForward p) {
   const int t = kLanes ? (int)threadIdx.x % nt : (int)threadIdx.x;
   const long long row = kLanes ? (long long)blockIdx.x * (blockDim.x / nt) + threadIdx.x / nt
                                : (long long)blockIdx.x;
-  const bool there = row < p.T;                  // (lanes of a row that is not there stay for the shuffles)
-  const int nvec = there ? p.H >> 3 : 0;
-  const long long base = row * p.H;
+  // (lanes of a row that is not there stay for the shuffles)
+  const int nvec = row < p.T ? p.H >> 3 : 0;
+  const long long base = row * p.H + 8 * t;
   pdl_wait();
   uint4 a[kVec], b[kVec], wv[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
-    const int j = i * nt + t;
     a[i] = b[i] = make_uint4(0, 0, 0, 0);
-    if (j < nvec) {
-      a[i] = ld_stream(p.x + base + 8 * j);
-      if (p.residual) b[i] = ld_stream(p.residual + base + 8 * j);
+    if (i * nt + t < nvec) {
+      a[i] = ld_stream(p.x + base + 8 * i * nt);
+      if (kRes) b[i] = ld_stream(p.residual + base + 8 * i * nt);
     }
   }
-  float h[kVec][8];
-  float sum[1] = {0.0f};
+  auto load_weights = [&] {
+#pragma unroll
+    for (int i = 0; i < kVec; ++i)
+      wv[i] = i * nt + t >= nvec ? make_uint4(0, 0, 0, 0) : p.w ? ld_here(p.w + 8 * (i * nt + t)) : kOnes;
+  };
+  if (kLanes) load_weights();
+  f32x2 h[kVec][4], squares = 0ull;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
-    widen(a[i], h[i]);
-    if (p.residual) {                            // (not -0 + 0)
-      float r[8];
-      widen(b[i], r);
+    widen2(a[i], h[i]);
+    f32x2 r[4];
+    widen2(b[i], r);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) h[i][e] += r[e];
+    for (int e = 0; e < 4; ++e) {
+      if (kRes) h[i][e] = f2_add(h[i][e], r[e]);
+      squares = f2_fma(h[i][e], h[i][e], squares);
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) sum[0] = fmaf(h[i][e], h[i][e], sum[0]);
-    const int j = i * nt + t;
-    if (p.h && j < nvec) *reinterpret_cast<uint4*>(p.h + base + 8 * j) = narrow(h[i]);
+    if (p.h && i * nt + t < nvec) *reinterpret_cast<uint4*>(p.h + base + 8 * i * nt) = narrow2(h[i]);
   }
   // (asked for here: the registers of x and the residual are free again)
-#pragma unroll
-  for (int i = 0; i < kVec; ++i) {
-    const int j = i * nt + t;
-    wv[i] = j >= nvec ? make_uint4(0, 0, 0, 0) : p.w ? ld_here(p.w + 8 * j) : kOnes;
-  }
+  if (!kLanes) load_weights();
+  float sum[1] = {f2_lo(squares) + f2_hi(squares)};
   row_sum<kLanes, 1>(sum, slots[0]);
   const float H = (float)p.H;
   float eps = p.eps;
   const float s = range_scale(sum[0], H, eps);   // (one for the row)
   const bool scaled = s != 1.0f;
   if (kLanes == 32 || kLanes == 0 ? scaled : __any_sync(kAll, scaled)) {
-    float more[1] = {0.0f};
+    squares = 0ull;
 #pragma unroll
     for (int i = 0; i < kVec; ++i)
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        h[i][e] *= s;
-        more[0] = fmaf(h[i][e], h[i][e], more[0]);
+      for (int e = 0; e < 4; ++e) {
+        h[i][e] = f2_mul(h[i][e], f2_splat(s));
+        squares = f2_fma(h[i][e], h[i][e], squares);
       }
-    row_sum<kLanes, 1>(more, slots[1]);
-    sum[0] = more[0];
+    sum[0] = f2_lo(squares) + f2_hi(squares);
+    row_sum<kLanes, 1>(sum, slots[1]);
     eps = eps * s * s;
   }
-  const float r = 1.0f / sqrtf(sum[0] / H + eps);
-  uint32_t m[kVec];
+  const f32x2 r = f2_splat(1.0f / sqrtf(sum[0] / H + eps));
+  float m[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
-    const int j = i * nt + t;
-    float w[8];
-    widen(wv[i], w);
-    m[i] = 0;
+    f32x2 w[4];
+    widen2(wv[i], w);
+    m[i] = 0.0f;
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      h[i][e] = h[i][e] * r * w[e];
-      m[i] = max(m[i], abs_bits(h[i][e]));
+    for (int e = 0; e < 4; ++e) {
+      h[i][e] = f2_mul(f2_mul(h[i][e], r), w[e]);
+      m[i] = max_abs(m[i], max_abs(f2_lo(h[i][e]), f2_hi(h[i][e])));
     }
-    if (j >= nvec) m[i] = 0;
-    if (p.out && j < nvec) *reinterpret_cast<uint4*>(p.out + base + 8 * j) = narrow(h[i]);
+    if (i * nt + t >= nvec) m[i] = 0.0f;
+    if (p.out && i * nt + t < nvec) *reinterpret_cast<uint4*>(p.out + base + 8 * i * nt) = narrow2(h[i]);
   }
   if (!p.codes) return;
   // sixteen lanes (or the row's) hold the blocks that their vectors belong to; lane i of them takes
   // the divisions of block i for all
   constexpr int kGroup = kLanes && kLanes < 16 ? kLanes : 16;
-  uint32_t mine = m[0];
+  float mine = 0.0f;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
 #pragma unroll
-    for (int o = 1; o < kGroup; o <<= 1) m[i] = max(m[i], __shfl_xor_sync(kAll, m[i], o));
-    if (t % kGroup == i) mine = m[i];
+    for (int o = 1; o < kGroup; o <<= 1) m[i] = max_abs(m[i], __shfl_xor_sync(kAll, m[i], o));
+    if (i == 0 || t % kGroup == i) mine = m[i];
   }
-  const BlockScale bs = block_scale(mine);
+  const BlockScale bs = block_scale(__float_as_uint(mine));
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
-    const int j = i * nt + t;
-    const float inv = __shfl_sync(kAll, bs.inv, (threadIdx.x & 31 & ~(kGroup - 1)) + i);
-    if (j < nvec) {
-      uint2 c;
-      c.x = pack_e4m3x4(h[i][0] * inv, h[i][1] * inv, h[i][2] * inv, h[i][3] * inv);
-      c.y = pack_e4m3x4(h[i][4] * inv, h[i][5] * inv, h[i][6] * inv, h[i][7] * inv);
-      *reinterpret_cast<uint2*>(p.codes + base + 8 * j) = c;
-    }
+    const f32x2 inv = f2_splat(__shfl_sync(kAll, bs.inv, (threadIdx.x & 31 & ~(kGroup - 1)) + i));
+    f32x2 c[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) c[e] = f2_mul(h[i][e], inv);
+    if (i * nt + t < nvec)
+      *reinterpret_cast<uint2*>(p.codes + base + 8 * i * nt) =
+          make_uint2(pack_e4m3x4(f2_lo(c[0]), f2_hi(c[0]), f2_lo(c[1]), f2_hi(c[1])),
+                     pack_e4m3x4(f2_lo(c[2]), f2_hi(c[2]), f2_lo(c[3]), f2_hi(c[3])));
   }
   // lane i: the scale of its group's block in vector i
   const int i = t % kGroup, j = i * nt + (t - i);
@@ -518,22 +535,28 @@ size_t norm_backward_workspace_bytes(int T, int H) {
   return ((size_t)(a > b ? a : b) * H * sizeof(float) + 255) & ~size_t(255);
 }
 
+template <int kVec, int kLanes>
+static cudaError_t launch_norm_as(const NormForward& n, dim3 grid, int threads, cudaStream_t s) {
+  return n.residual ? launch_k(norm_kernel<kVec, kLanes, true>, grid, dim3(threads), 0, s, n)
+                    : launch_k(norm_kernel<kVec, kLanes, false>, grid, dim3(threads), 0, s, n);
+}
+
 cudaError_t launch_norm(const NormForward& n, cudaStream_t s) {
   const int nvec = n.H / 8;
   if (nvec <= kForwardShort) {
     const ShortRow r = short_row(nvec);
-    const dim3 grid((unsigned)ceil_div(n.T, kShortThreads / r.lanes)), block(kShortThreads);
-    if (r.lanes == 8) return launch_k(norm_kernel<1, 8>, grid, block, 0, s, n);
-    if (r.lanes == 16) return launch_k(norm_kernel<1, 16>, grid, block, 0, s, n);
-    return r.vec == 1   ? launch_k(norm_kernel<1, 32>, grid, block, 0, s, n)
-           : r.vec == 2 ? launch_k(norm_kernel<2, 32>, grid, block, 0, s, n)
-                        : launch_k(norm_kernel<4, 32>, grid, block, 0, s, n);
+    const dim3 grid((unsigned)ceil_div(n.T, kShortThreads / r.lanes));
+    if (r.lanes == 8) return launch_norm_as<1, 8>(n, grid, kShortThreads, s);
+    if (r.lanes == 16) return launch_norm_as<1, 16>(n, grid, kShortThreads, s);
+    return r.vec == 1   ? launch_norm_as<1, 32>(n, grid, kShortThreads, s)
+           : r.vec == 2 ? launch_norm_as<2, 32>(n, grid, kShortThreads, s)
+                        : launch_norm_as<4, 32>(n, grid, kShortThreads, s);
   }
   const dim3 grid((unsigned)n.T);
   if (n.T <= 2 * num_sms())
-    return nvec <= 1024 ? launch_k(norm_kernel<1, 0>, grid, dim3(round32(nvec)), 0, s, n)
-                        : launch_k(norm_kernel<2, 0>, grid, dim3(round32((nvec + 1) / 2)), 0, s, n);
-  return launch_k(norm_kernel<4, 0>, grid, dim3(round32((nvec + 3) / 4)), 0, s, n);
+    return nvec <= 1024 ? launch_norm_as<1, 0>(n, grid, round32(nvec), s)
+                        : launch_norm_as<2, 0>(n, grid, round32((nvec + 1) / 2), s);
+  return launch_norm_as<4, 0>(n, grid, round32((nvec + 3) / 4), s);
 }
 
 cudaError_t launch_norm_backward(const NormBackward& n, cudaStream_t s) {
