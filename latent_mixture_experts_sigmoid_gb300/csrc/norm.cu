@@ -34,23 +34,13 @@ __device__ __forceinline__ uint4 ld_here(const uint16_t* p) {
   return v;
 }
 
-__device__ __forceinline__ void widen(const uint4& v, float (&f)[8]) {
-  f[0] = bf16_lo(v.x); f[1] = bf16_hi(v.x); f[2] = bf16_lo(v.y); f[3] = bf16_hi(v.y);
-  f[4] = bf16_lo(v.z); f[5] = bf16_hi(v.z); f[6] = bf16_lo(v.w); f[7] = bf16_hi(v.w);
-}
-
-__device__ __forceinline__ uint4 narrow(const float (&f)[8]) {
-  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]),
-                    pack_bf16x2(f[6], f[7]));
-}
-
-// four packed pairs of fp32
-__device__ __forceinline__ void widen2(const uint4& v, f32x2 (&f)[4]) {
+// eight bf16 as four packed pairs of fp32, and back
+__device__ __forceinline__ void widen(const uint4& v, f32x2 (&f)[4]) {
   const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
   for (int i = 0; i < 4; ++i) f[i] = f2_make(w[i] << 16, w[i] & 0xFFFF0000u);
 }
-__device__ __forceinline__ uint4 narrow2(const f32x2 (&f)[4]) {
+__device__ __forceinline__ uint4 narrow(const f32x2 (&f)[4]) {
   return make_uint4(pack_bf16x2(f2_lo(f[0]), f2_hi(f[0])), pack_bf16x2(f2_lo(f[1]), f2_hi(f[1])),
                     pack_bf16x2(f2_lo(f[2]), f2_hi(f[2])), pack_bf16x2(f2_lo(f[3]), f2_hi(f[3])));
 }
@@ -144,15 +134,15 @@ norm_kernel(const NormForward p) {
   f32x2 h[kVec][4], squares = 0ull;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
-    widen2(a[i], h[i]);
+    widen(a[i], h[i]);
     f32x2 r[4];
-    widen2(b[i], r);
+    widen(b[i], r);
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       if (kRes) h[i][e] = f2_add(h[i][e], r[e]);
       squares = f2_fma(h[i][e], h[i][e], squares);
     }
-    if (p.h && i * nt + t < nvec) *reinterpret_cast<uint4*>(p.h + base + 8 * i * nt) = narrow2(h[i]);
+    if (p.h && i * nt + t < nvec) *reinterpret_cast<uint4*>(p.h + base + 8 * i * nt) = narrow(h[i]);
   }
   // (asked for here: the registers of x and the residual are free again)
   if (!kLanes) load_weights();
@@ -180,7 +170,7 @@ norm_kernel(const NormForward p) {
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     f32x2 w[4];
-    widen2(wv[i], w);
+    widen(wv[i], w);
     m[i] = 0.0f;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
@@ -188,7 +178,7 @@ norm_kernel(const NormForward p) {
       m[i] = max_abs(m[i], max_abs(f2_lo(h[i][e]), f2_hi(h[i][e])));
     }
     if (i * nt + t >= nvec) m[i] = 0.0f;
-    if (p.out && i * nt + t < nvec) *reinterpret_cast<uint4*>(p.out + base + 8 * i * nt) = narrow2(h[i]);
+    if (p.out && i * nt + t < nvec) *reinterpret_cast<uint4*>(p.out + base + 8 * i * nt) = narrow(h[i]);
   }
   if (!p.codes) return;
   // sixteen lanes (or the row's) hold the blocks that their vectors belong to; lane i of them takes
@@ -226,20 +216,22 @@ norm_kernel(const NormForward p) {
 template <int kVec>
 __device__ __forceinline__ void sums_of(float (&sum)[2], const uint4 (&hv)[kVec], const uint4 (&dv)[kVec],
                                         const uint4 (&wv)[kVec], float s) {
-  sum[0] = sum[1] = 0.0f;
+  f32x2 hh = 0ull, gh = 0ull;
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
-    float h[8], d[8], w[8];
+    f32x2 h[4], d[4], w[4];
     widen(hv[i], h);
     widen(dv[i], d);
     widen(wv[i], w);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float v = h[e] * s;
-      sum[0] = fmaf(v, v, sum[0]);
-      sum[1] = fmaf(d[e] * w[e], v, sum[1]);
+    for (int e = 0; e < 4; ++e) {
+      if (s != 1.0f) h[e] = f2_mul(h[e], f2_splat(s));
+      hh = f2_fma(h[e], h[e], hh);
+      gh = f2_fma(f2_mul(d[e], w[e]), h[e], gh);
     }
   }
+  sum[0] = f2_lo(hh) + f2_hi(hh);
+  sum[1] = f2_lo(gh) + f2_hi(gh);
 }
 
 // n = (h s) r (not h (s r): s r may leave the range where the squares did);
@@ -266,18 +258,18 @@ __device__ __forceinline__ RowFactors factors_of(const uint4 (&hv)[kVec], const 
 }
 
 __device__ __forceinline__ uint4 grad_of(const uint4& hv, const uint4& dv, const uint4& wv, const uint4& rv,
-                                         const RowFactors& f, float (&acc)[8]) {
-  float h[8], d[8], w[8], q[8];
+                                         const RowFactors& f, f32x2 (&acc)[4]) {
+  f32x2 h[4], d[4], w[4], q[4];
   widen(hv, h);
   widen(dv, d);
   widen(wv, w);
   widen(rv, q);
-  const float sr = f.s * f.r;
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const float n = h[e] * f.s * f.r;
-    acc[e] = fmaf(d[e], n, acc[e]);
-    q[e] = fmaf(sr, fmaf(-n, f.k, d[e] * w[e]), q[e]);
+  for (int e = 0; e < 4; ++e) {
+    if (f.s != 1.0f) h[e] = f2_mul(h[e], f2_splat(f.s));
+    const f32x2 n = f2_mul(h[e], f2_splat(f.r));
+    acc[e] = f2_fma(d[e], n, acc[e]);
+    q[e] = f2_fma(f2_splat(f.s * f.r), f2_fma(n, f2_splat(-f.k), f2_mul(d[e], w[e])), q[e]);
   }
   return narrow(q);
 }
@@ -291,7 +283,7 @@ norm_backward_short_kernel(const NormBackward p) {
   const int walker = (int)blockIdx.x * per + (int)threadIdx.x / kLanes, walkers = (int)gridDim.x * per;
   const int first = (int)blockIdx.x * per + (int)(threadIdx.x & ~31u) / kLanes;   // the warp's first walker
   pdl_wait();
-  float acc[kVec][8] = {};
+  f32x2 acc[kVec][4] = {};
   uint4 wv[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
@@ -324,13 +316,12 @@ norm_backward_short_kernel(const NormBackward p) {
   // the CTA's rows of sums as one, in order
   if (!p.dw) return;
   constexpr int kCols = kVec * kLanes * 8;
-  __shared__ float sums[256 / kLanes][kCols];
+  __shared__ __align__(16) float sums[256 / kLanes][kCols];
 #pragma unroll
   for (int i = 0; i < kVec; ++i)
 #pragma unroll
-    for (int e = 0; e < 8; e += 4)
-      *reinterpret_cast<float4*>(&sums[threadIdx.x / kLanes][(i * kLanes + t) * 8 + e]) =
-          make_float4(acc[i][e], acc[i][e + 1], acc[i][e + 2], acc[i][e + 3]);
+    for (int e = 0; e < 4; ++e)
+      *reinterpret_cast<f32x2*>(&sums[threadIdx.x / kLanes][(i * kLanes + t) * 8 + 2 * e]) = acc[i][e];
   __syncthreads();
   for (int c = threadIdx.x; c < p.H; c += 256) {
     float v = 0.0f;
@@ -372,7 +363,7 @@ norm_backward_kernel(const NormBackward p, int stages) {
   };
   if (t == 0)
     for (int s = 0; s < stages && next < p.T; ++s) copy(s);
-  float acc[kVec][8] = {};
+  f32x2 acc[kVec][4] = {};
   uint4 wv[kVec];
   auto load_weights = [&] {
 #pragma unroll
@@ -425,10 +416,9 @@ norm_backward_kernel(const NormBackward p, int stages) {
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
     const int j = i * nt + t;
-    if (j < nvec) {
-      *reinterpret_cast<float4*>(part + 8 * j) = make_float4(acc[i][0], acc[i][1], acc[i][2], acc[i][3]);
-      *reinterpret_cast<float4*>(part + 8 * j + 4) = make_float4(acc[i][4], acc[i][5], acc[i][6], acc[i][7]);
-    }
+    if (j < nvec)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) *reinterpret_cast<f32x2*>(part + 8 * j + 2 * e) = acc[i][e];
   }
 }
 
