@@ -148,7 +148,7 @@ norm_kernel(const NormForward p) {
   if (!kLanes) load_weights();
   float sum[1] = {f2_lo(squares) + f2_hi(squares)};
   row_sum<kLanes, 1>(sum, slots[0]);
-  const float H = (float)p.H;
+  const float H = (float)p.H, inv_H = 1.0f / H;
   float eps = p.eps;
   const float s = range_scale(sum[0], H, eps);   // (one for the row)
   const bool scaled = s != 1.0f;
@@ -165,7 +165,7 @@ norm_kernel(const NormForward p) {
     row_sum<kLanes, 1>(sum, slots[1]);
     eps = eps * s * s;
   }
-  const f32x2 r = f2_splat(1.0f / sqrtf(sum[0] / H + eps));
+  const f32x2 r = f2_splat(rsqrtf(fmaf(sum[0], inv_H, eps)));
   float m[kVec];
 #pragma unroll
   for (int i = 0; i < kVec; ++i) {
@@ -241,8 +241,8 @@ struct RowFactors {
 };
 template <int kVec, int kLanes>
 __device__ __forceinline__ RowFactors factors_of(const uint4 (&hv)[kVec], const uint4 (&dv)[kVec],
-                                                 const uint4 (&wv)[kVec], float H, float eps,
-                                                 float (*slots)[2], float (*more_slots)[2]) {
+                                                 const uint4 (&wv)[kVec], float H, float inv_H,
+                                                 float eps, float (*slots)[2], float (*more_slots)[2]) {
   float sum[2];
   sums_of<kVec>(sum, hv, dv, wv, 1.0f);
   row_sum<kLanes, 2>(sum, slots);
@@ -253,8 +253,8 @@ __device__ __forceinline__ RowFactors factors_of(const uint4 (&hv)[kVec], const 
     row_sum<kLanes, 2>(sum, more_slots);
     eps = eps * s * s;
   }
-  const float r = 1.0f / sqrtf(sum[0] / H + eps);
-  return {s, r, sum[1] * r / H};
+  const float r = rsqrtf(fmaf(sum[0], inv_H, eps));
+  return {s, r, sum[1] * inv_H * r};
 }
 
 __device__ __forceinline__ uint4 grad_of(const uint4& hv, const uint4& dv, const uint4& wv, const uint4& rv,
@@ -283,6 +283,7 @@ norm_backward_short_kernel(const NormBackward p) {
   const int walker = (int)blockIdx.x * per + (int)threadIdx.x / kLanes, walkers = (int)gridDim.x * per;
   const int first = (int)blockIdx.x * per + (int)(threadIdx.x & ~31u) / kLanes;   // the warp's first walker
   pdl_wait();
+  const float inv_H = 1.0f / (float)p.H;
   f32x2 acc[kVec][4] = {};
   uint4 wv[kVec];
 #pragma unroll
@@ -304,7 +305,7 @@ norm_backward_short_kernel(const NormBackward p) {
         if (p.dres) rv[i] = ld_stream(p.dres + base + 8 * j);
       }
     }
-    const RowFactors f = factors_of<kVec, kLanes>(hv, dv, wv, (float)p.H, p.eps, nullptr, nullptr);
+    const RowFactors f = factors_of<kVec, kLanes>(hv, dv, wv, (float)p.H, inv_H, p.eps, nullptr, nullptr);
     if (!there) continue;                        // (with eps = 0 its zeros would be NaN)
 #pragma unroll
     for (int i = 0; i < kVec; ++i) {
@@ -363,6 +364,7 @@ norm_backward_kernel(const NormBackward p, int stages) {
   };
   if (t == 0)
     for (int s = 0; s < stages && next < p.T; ++s) copy(s);
+  const float inv_H = 1.0f / (float)p.H;
   f32x2 acc[kVec][4] = {};
   uint4 wv[kVec];
   auto load_weights = [&] {
@@ -392,7 +394,7 @@ norm_backward_kernel(const NormBackward p, int stages) {
       }
     }
     if constexpr (kVec == 4) load_weights();     // (kept, they spill)
-    const RowFactors f = factors_of<kVec, 0>(hv, dv, wv, (float)p.H, p.eps, slots[flip], slots[2 + flip]);
+    const RowFactors f = factors_of<kVec, 0>(hv, dv, wv, (float)p.H, inv_H, p.eps, slots[flip], slots[2 + flip]);
     if (*(volatile int*)&abort_flag) break;      // (set ahead of the barrier in factors_of: for all)
     const int last = s ? s - 1 : stages - 1;
     if (t == 0 && row != blockIdx.x && next < p.T) copy(last);
