@@ -110,11 +110,10 @@ def test_backward_x(name, N, K):
     check_rows(lm.lmoe_grouped_linear_backward_x, O.grouped_linear_backward_x, dy, w, off, COUNTS[name], N, K)
 
 
-@pytest.mark.parametrize("form", ["fp32", "add", "in place", "bf16"])
-@pytest.mark.parametrize("name,N,K", CASES)
+# (the addend at a few sizes)
+@pytest.mark.parametrize("name,N,K,form", [(*c, f) for c in CASES for f in ("fp32", "bf16")] +
+                         [(*c, f) for c in FEW for f in ("add", "in place")])
 def test_backward_w(name, N, K, form):
-    if form in ("add", "in place") and (name, N, K) not in FEW:
-        pytest.skip("the addend at a few sizes")
     off, x, dy, w, R = make(name, N, K)
     E, counts = w.shape[0], COUNTS[name]
     dt = torch.bfloat16 if form == "bf16" else torch.float32
