@@ -51,6 +51,11 @@ constexpr int kBK = 64;                             // a K block: 128 bytes
 constexpr uint32_t kChunk = kBK * 128;              // 64 M or N columns of a block, K rows of 128 bytes
 constexpr uint32_t kABytes = kHalf * kBK * 2;
 constexpr int kAcc = 2;                             // TMEM accumulators of 256 columns
+// weights: rows that the tensor cores add up before registers take over.  Their additions truncate:
+// a sum of n rows comes out low by about n 2^-30 of itself (65536 rows: 8e-5, of numbers of one sign
+// 4e-4).  256 rows are 2e-7 off, the registers' additions round, and a read of TMEM every 2048
+// cycles of MMAs hides behind them.
+constexpr int kFlush = 256;
 constexpr int kMaxStages = 12;
 constexpr int kMaxGroups = 1024;
 // shared memory of the epilogue: a box of 32 tokens x 128 bf16 features for each column half, or for
@@ -331,184 +336,185 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   const int u0 = (int)(blockIdx.x >> 1), ustep = (int)(gridDim.x >> 1);
   const int nkb_rows = (p.depth + kBK - 1) / kBK;
 
-  if (warp == 0) {
-    // ---------------- TMA producer ----------------
-    // (the warp runs as one and a lane issues, as in the MMA warp)
-    int s = 0;
-    uint32_t ph = 0, it = 0;
-    bool ok = true;
-    for (int u = u0; u < U && ok; u += ustep) {
-      const Tile x = tile_of<kMode>(p, groups, u);
-      const int m = x.m0 + (int)rank * kHalf, half = x.n >> 1;
-      const int nkb = kMode == kWeights ? (x.rows + kBK - 1) / kBK : nkb_rows;
-      // token rows: one box of all, or as many partial ones as this CTA's half takes
-      const bool whole = x.n == p.nt;
-      const int nbox = whole ? 1 : (half + p.part - 1) / p.part;
-      const int brows = whole ? p.nt >> 1 : p.part;
-      const int tok = x.row0 + (int)rank * half;
-      const int nchunk = x.n >> 7;                   // (weights: 64 columns each)
-      const int n0 = x.n0 + (int)rank * half;
-      for (int kb = 0; kb < nkb; ++kb, ++it) {
-        ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kEmpty + s), ph ^ 1u, abort_flag, p.err, kErrProducer));
-        if (!ok) break;
-        const uint32_t at = smem_u32(smem) + (uint32_t)s * p.stage_bytes, bt = at + kABytes;
-        const int k = kb * kBK;
-        const int left = x.rows - k;                 // (weights)
-        if (elect_one()) {
-          if (kMode == kWeights && left < kBK) {
-            const int n16 = (left + 15) >> 4;
-            const uint32_t bar = bar_at(kLast + s);
-            mbar_arrive_expect_tx(bar, (uint32_t)((2 + nchunk) * n16) * 2048u);
-            for (int c = 0; c < 2; ++c)
-              for (int i = 0; i < n16; ++i)
-                tma_load_2d(&tmAp, at + c * kChunk + i * 2048u, bar, m + c * 64, x.row0 + k + i * 16);
-            for (int c = 0; c < nchunk; ++c)
-              for (int i = 0; i < n16; ++i)
-                tma_load_2d(&tmBp, bt + c * kChunk + i * 2048u, bar, n0 + c * 64, x.row0 + k + i * 16);
-          } else {
-            const uint32_t bar = cluster_addr(bar_at(kFull + s), 0);
-            if (rank == 0) {
-              const uint32_t bytes = kMode == kWeights ? (uint32_t)(2 + nchunk) * kChunk
-                                                       : kABytes + (uint32_t)(nbox * brows) * 128u;
-              if constexpr (kMode == kWeights) mbar_arrive(bar_at(kFull + s));
-              mbar_arrive_expect_tx(bar_at(kFull + s), 2 * bytes);
-            }
-            if constexpr (kMode == kForward) {
-              tma_load_pair_3d(&tmA, at, bar, k, m, x.group);
-            } else if constexpr (kMode == kRows) {
-              tma_load_pair_3d(&tmA, at, bar, m, k, x.group);
-              tma_load_pair_3d(&tmA, at + kChunk, bar, m + 64, k, x.group);
-            } else {
-              tma_load_pair(&tmA, at, bar, m, x.row0 + k);
-              tma_load_pair(&tmA, at + kChunk, bar, m + 64, x.row0 + k);
-            }
-            if constexpr (kMode == kWeights) {
-              tma_load_pair(&tmB, bt, bar, n0, x.row0 + k);
-              if (nchunk > 1) tma_load_pair(&tmB, bt + kChunk, bar, n0 + 64, x.row0 + k);
-            } else if (whole) {
-              tma_load_pair(&tmB, bt, bar, k, tok);
-            } else {
-              for (int i = 0; i < nbox; ++i)
-                tma_load_pair(&tmBp, bt + (uint32_t)(i * brows) * 128u, bar, k, tok + i * brows);
-            }
-          }
-        }
-        __syncwarp();
-        if (++s == p.stages) { s = 0; ph ^= 1u; }
-      }
-    }
-    // the leader: every copy of the pair has landed before the CTAs exit
-    if (rank == 0)
-      for (uint32_t j = it > (uint32_t)p.stages ? it - p.stages : 0u; j < it; ++j) {
-        volatile int never = 0;
-        if (!wait_phase(bar_at(kFull + (int)(j % p.stages)), (j / p.stages) & 1u, &never, p.err, kErrDrain))
-          break;
-      }
-  } else if (warp == 1) {
-    if (rank == 0) {
-      // ---------------- MMA issuer of the pair ----------------
-      // The warp runs the loop as one and a lane of it issues: an MMA's operands go through
-      // registers of the warp, which a branch of one lane fills at about 130 cycles an MMA.
-      const uint64_t a0 = sdesc<kAK>(smem_u32(smem)), b0 = sdesc<kBK_>(smem_u32(smem) + kABytes);
+  // weights: the launch's 168 registers a thread, split anew: 168 * 384 = 40 * 128 + 232 * 256
+  if (warp < kEpiWarp0) {
+    if constexpr (kMode == kWeights) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+    if (warp == 0) {
+      // ---------------- TMA producer ----------------
+      // (the warp runs as one and a lane issues, as in the MMA warp)
       int s = 0;
-      uint32_t ph = 0, acc = 0, aph = 0;
+      uint32_t ph = 0, it = 0;
       bool ok = true;
       for (int u = u0; u < U && ok; u += ustep) {
         const Tile x = tile_of<kMode>(p, groups, u);
-        const int depth = kMode == kWeights ? x.rows : p.depth;
-        if (depth == 0) continue;                    // (an expert without rows: the epilogue writes zeros)
-        ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kTempty + (int)acc), aph ^ 1u, abort_flag, p.err, kErrMmaTmem));
-        if (!ok) break;
-        tc_fence_after();
-        const uint32_t id = idesc<kMode>(x.n), d = tmem_base + acc * kTile;
-        for (int k = 0; k < depth; k += kBK) {
-          ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kFull + s), ph, abort_flag, p.err, kErrMmaFull));
+        const int m = x.m0 + (int)rank * kHalf, half = x.n >> 1;
+        const int nkb = kMode == kWeights ? (x.rows + kBK - 1) / kBK : nkb_rows;
+        // token rows: one box of all, or as many partial ones as this CTA's half takes
+        const bool whole = x.n == p.nt;
+        const int nbox = whole ? 1 : (half + p.part - 1) / p.part;
+        const int brows = whole ? p.nt >> 1 : p.part;
+        const int tok = x.row0 + (int)rank * half;
+        const int nchunk = x.n >> 7;                   // (weights: 64 columns each)
+        const int n0 = x.n0 + (int)rank * half;
+        for (int kb = 0; kb < nkb; ++kb, ++it) {
+          ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kEmpty + s), ph ^ 1u, abort_flag, p.err, kErrProducer));
           if (!ok) break;
-          tc_fence_after();
-          const uint64_t da = a0 + (uint64_t)s * (p.stage_bytes >> 4), db = b0 + (uint64_t)s * (p.stage_bytes >> 4);
+          const uint32_t at = smem_u32(smem) + (uint32_t)s * p.stage_bytes, bt = at + kABytes;
+          const int k = kb * kBK;
+          const int left = x.rows - k;                 // (weights)
           if (elect_one()) {
-#pragma unroll
-            for (int j = 0; j < kBK / 16; ++j)
-              // (weights: not past the zeros; the others' blocks are whole or filled up with zeros)
-              if (kMode != kWeights || k + 16 * j < depth)
-                mma_pair(d, da + j * kStep<kAK>, db + j * kStep<kBK_>, id, j ? 1u : (uint32_t)(k != 0));
-            commit_both(bar_at(kEmpty + s));
+            if (kMode == kWeights && left < kBK) {
+              const int n16 = (left + 15) >> 4;
+              const uint32_t bar = bar_at(kLast + s);
+              mbar_arrive_expect_tx(bar, (uint32_t)((2 + nchunk) * n16) * 2048u);
+              for (int c = 0; c < 2; ++c)
+                for (int i = 0; i < n16; ++i)
+                  tma_load_2d(&tmAp, at + c * kChunk + i * 2048u, bar, m + c * 64, x.row0 + k + i * 16);
+              for (int c = 0; c < nchunk; ++c)
+                for (int i = 0; i < n16; ++i)
+                  tma_load_2d(&tmBp, bt + c * kChunk + i * 2048u, bar, n0 + c * 64, x.row0 + k + i * 16);
+            } else {
+              const uint32_t bar = cluster_addr(bar_at(kFull + s), 0);
+              if (rank == 0) {
+                const uint32_t bytes = kMode == kWeights ? (uint32_t)(2 + nchunk) * kChunk
+                                                         : kABytes + (uint32_t)(nbox * brows) * 128u;
+                if constexpr (kMode == kWeights) mbar_arrive(bar_at(kFull + s));
+                mbar_arrive_expect_tx(bar_at(kFull + s), 2 * bytes);
+              }
+              if constexpr (kMode == kForward) {
+                tma_load_pair_3d(&tmA, at, bar, k, m, x.group);
+              } else if constexpr (kMode == kRows) {
+                tma_load_pair_3d(&tmA, at, bar, m, k, x.group);
+                tma_load_pair_3d(&tmA, at + kChunk, bar, m + 64, k, x.group);
+              } else {
+                tma_load_pair(&tmA, at, bar, m, x.row0 + k);
+                tma_load_pair(&tmA, at + kChunk, bar, m + 64, x.row0 + k);
+              }
+              if constexpr (kMode == kWeights) {
+                tma_load_pair(&tmB, bt, bar, n0, x.row0 + k);
+                if (nchunk > 1) tma_load_pair(&tmB, bt + kChunk, bar, n0 + 64, x.row0 + k);
+              } else if (whole) {
+                tma_load_pair(&tmB, bt, bar, k, tok);
+              } else {
+                for (int i = 0; i < nbox; ++i)
+                  tma_load_pair(&tmBp, bt + (uint32_t)(i * brows) * 128u, bar, k, tok + i * brows);
+              }
+            }
           }
           __syncwarp();
           if (++s == p.stages) { s = 0; ph ^= 1u; }
         }
-        if (!ok) break;
-        if (elect_one()) commit_both(bar_at(kTfull + (int)acc));
-        __syncwarp();
-        if (++acc == kAcc) { acc = 0; aph ^= 1u; }
       }
-      // every MMA the lane issued has completed before TMEM is freed
-      if (elect_one())
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
-                         bar_at(kDone))
-                     : "memory");
-      __syncwarp();
-      volatile int never = 0;
-      wait_phase(bar_at(kDone), 0u, &never, p.err, kErrDone);
-    }
-  } else if (warp == 2) {
-    if constexpr (kMode == kWeights) {
-      // ---------------- zeros behind an expert's last row ----------------
-      uint32_t it = 0, lph = 0;                      // lph: a stage's phase of kLast, a bit each
-      for (int u = u0; u < U; u += ustep) {
-        const Tile x = tile_of<kMode>(p, groups, u);
-        it += (uint32_t)(x.rows + kBK - 1) / kBK;
-        const int left = x.rows & (kBK - 1);
-        if (left == 0) continue;
-        const int s = (int)((it - 1) % (uint32_t)p.stages);
-        if (!__all_sync(0xFFFFFFFFu, wait_phase(bar_at(kLast + s), (lph >> s) & 1u, abort_flag, p.err, kErrProducer))) break;
-        lph ^= 1u << s;
-        const int z = (-left & 15) * 8;              // 16-byte pieces of the rows up to the next 16
-        uint8_t* at = smem + (size_t)s * p.stage_bytes + left * 128;
-        for (int c = 0; c < 2 + (x.n >> 7); ++c)     // 64 columns each
-          for (int i = lane; i < z; i += 32)
-            *reinterpret_cast<uint4*>(at + c * kChunk + i * 16) = make_uint4(0, 0, 0, 0);
-        fence_proxy_async_smem();
+      // the leader: every copy of the pair has landed before the CTAs exit
+      if (rank == 0)
+        for (uint32_t j = it > (uint32_t)p.stages ? it - p.stages : 0u; j < it; ++j) {
+          volatile int never = 0;
+          if (!wait_phase(bar_at(kFull + (int)(j % p.stages)), (j / p.stages) & 1u, &never, p.err, kErrDrain))
+            break;
+        }
+    } else if (warp == 1) {
+      if (rank == 0) {
+        // ---------------- MMA issuer of the pair ----------------
+        // The warp runs the loop as one and a lane of it issues: an MMA's operands go through
+        // registers of the warp, which a branch of one lane fills at about 130 cycles an MMA.
+        const uint64_t a0 = sdesc<kAK>(smem_u32(smem)), b0 = sdesc<kBK_>(smem_u32(smem) + kABytes);
+        int s = 0;
+        uint32_t ph = 0, acc = 0, aph = 0;
+        bool ok = true;
+        for (int u = u0; u < U && ok; u += ustep) {
+          const Tile x = tile_of<kMode>(p, groups, u);
+          const int depth = kMode == kWeights ? x.rows : p.depth;
+          if (depth == 0) continue;                    // (an expert without rows: the epilogue writes zeros)
+          const uint32_t id = idesc<kMode>(x.n);
+          for (int k = 0; k < depth; k += kBK) {
+            const bool fresh = kMode == kWeights ? k % kFlush == 0 : k == 0;     // a new accumulator
+            if (fresh) {
+              ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kTempty + (int)acc), aph ^ 1u, abort_flag, p.err, kErrMmaTmem));
+              if (!ok) break;
+            }
+            ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kFull + s), ph, abort_flag, p.err, kErrMmaFull));
+            if (!ok) break;
+            tc_fence_after();
+            const uint64_t da = a0 + (uint64_t)s * (p.stage_bytes >> 4), db = b0 + (uint64_t)s * (p.stage_bytes >> 4);
+            const uint32_t d = tmem_base + acc * kTile;
+            const bool last = k + kBK >= depth || (kMode == kWeights && (k + kBK) % kFlush == 0);
+            if (elect_one()) {
+#pragma unroll
+              for (int j = 0; j < kBK / 16; ++j)
+                // (weights: not past the zeros; the others' blocks are whole or filled up with zeros)
+                if (kMode != kWeights || k + 16 * j < depth)
+                  mma_pair(d, da + j * kStep<kAK>, db + j * kStep<kBK_>, id, j ? 1u : (uint32_t)!fresh);
+              commit_both(bar_at(kEmpty + s));
+              if (last) commit_both(bar_at(kTfull + (int)acc));
+            }
+            __syncwarp();
+            if (++s == p.stages) { s = 0; ph ^= 1u; }
+            if (last && ++acc == kAcc) { acc = 0; aph ^= 1u; }
+          }
+          if (!ok) break;
+        }
+        // every MMA the lane issued has completed before TMEM is freed
+        if (elect_one())
+          asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(
+                           bar_at(kDone))
+                       : "memory");
         __syncwarp();
-        if (lane == 0) mbar_arrive_cluster_data(cluster_addr(bar_at(kFull + s), 0));
+        volatile int never = 0;
+        wait_phase(bar_at(kDone), 0u, &never, p.err, kErrDone);
+      }
+    } else if (warp == 2) {
+      if constexpr (kMode == kWeights) {
+        // ---------------- zeros behind an expert's last row ----------------
+        uint32_t it = 0, lph = 0;                      // lph: a stage's phase of kLast, a bit each
+        for (int u = u0; u < U; u += ustep) {
+          const Tile x = tile_of<kMode>(p, groups, u);
+          it += (uint32_t)(x.rows + kBK - 1) / kBK;
+          const int left = x.rows & (kBK - 1);
+          if (left == 0) continue;
+          const int s = (int)((it - 1) % (uint32_t)p.stages);
+          if (!__all_sync(0xFFFFFFFFu, wait_phase(bar_at(kLast + s), (lph >> s) & 1u, abort_flag, p.err, kErrProducer))) break;
+          lph ^= 1u << s;
+          const int z = (-left & 15) * 8;              // 16-byte pieces of the rows up to the next 16
+          uint8_t* at = smem + (size_t)s * p.stage_bytes + left * 128;
+          for (int c = 0; c < 2 + (x.n >> 7); ++c)     // 64 columns each
+            for (int i = lane; i < z; i += 32)
+              *reinterpret_cast<uint4*>(at + c * kChunk + i * 16) = make_uint4(0, 0, 0, 0);
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive_cluster_data(cluster_addr(bar_at(kFull + s), 0));
+        }
       }
     }
-  } else if (warp >= kEpiWarp0) {
+  } else {
+    if constexpr (kMode == kWeights) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     // ---------------- epilogue ----------------
     const int q = warp & 3;                      // TMEM lane quarter this warp may access
     const int h = (warp - kEpiWarp0) >> 2;
     const uint32_t tempty = cluster_addr(bar_at(kTempty), 0);
     const uint32_t tmem = tmem_base + ((uint32_t)(q * 32) << 16);
-    constexpr int kCols = kOut == 1 ? 64 : 32;   // (weights) columns of a box, one box a warp
-    uint8_t* box = boxes + (kMode == kWeights ? (warp - kEpiWarp0) * kWeightBox : h * kRowBox);
-    uint4 add[8];
     uint32_t acc = 0, aph = 0;
     bool ok = true;
-    if constexpr (kOut == 2)
-      if (u0 < U) {
-        const Tile x = tile_of<kMode>(p, groups, u0);
-        load_addend(p, x, x.m0 + (int)rank * kHalf + q * 32, x.n0 + h * (x.n >> 1), lane, add);
-      }
-    for (int u = u0; u < U && ok; u += ustep) {
-      const Tile x = tile_of<kMode>(p, groups, u);
-      const bool zero = kMode == kWeights && x.rows == 0;
-      const int m = x.m0 + (int)rank * kHalf + q * 32;           // first M row of the warp
-      if (!zero) {
-        // (a wait's outcome is one for the warp, whose lanes meet again below)
-        ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kTfull + (int)acc), aph, abort_flag, p.err, kErrEpilogue));
-        if constexpr (kMode != kWeights) ok = half_all(h, ok);     // (they meet again in store_rows)
-        if (!ok) break;
-        tc_fence_after();
-      }
-      if constexpr (kMode != kWeights) {
+    // (a wait's outcome is one for the warp, whose lanes meet again below)
+    auto wait_full = [&] {
+      ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kTfull + (int)acc), aph, abort_flag, p.err, kErrEpilogue));
+      if constexpr (kMode != kWeights) ok = half_all(h, ok);     // (they meet again in store_rows)
+      tc_fence_after();
+      return ok;
+    };
+    auto give_back = [&] {
+      tc_fence_before();
+      __syncwarp();
+      if (lane == 0) mbar_arrive_cluster(tempty + 8u * acc);
+    };
+    if constexpr (kMode != kWeights) {
+      uint8_t* box = boxes + h * kRowBox;
+      for (int u = u0; u < U && ok; u += ustep) {
+        const Tile x = tile_of<kMode>(p, groups, u);
+        const int f0 = x.m0 + (int)rank * kHalf;
+        if (!wait_full()) break;
         // the next columns are on their way while these are written; behind the last the
         // accumulator goes back
         const uint32_t at = tmem + acc * kTile;
-        auto give_back = [&] {
-          tc_fence_before();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster(tempty + 8u * acc);
-        };
         uint32_t va[32], vb[32];
         int c = h * 32;
         if (c < x.rows) tmem_ld32(at + c, va);
@@ -517,18 +523,57 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           tmem_wait_ld32(va);
           if (c + 64 < x.rows) tmem_ld32(at + c + 64, vb);
           else give_back();
-          store_rows(p, box, va, x.row0 + c, x.rows - c, x.m0 + (int)rank * kHalf, q, h, lane);
+          store_rows(p, box, va, x.row0 + c, x.rows - c, f0, q, h, lane);
           if (c + 64 >= x.rows) break;
           tmem_wait_ld32(vb);
           if (c + 128 < x.rows) tmem_ld32(at + c + 128, va);
           else give_back();
-          store_rows(p, box, vb, x.row0 + c + 64, x.rows - c - 64, x.m0 + (int)rank * kHalf, q, h, lane);
+          store_rows(p, box, vb, x.row0 + c + 64, x.rows - c - 64, f0, q, h, lane);
         }
         if (++acc == kAcc) { acc = 0; aph ^= 1u; }
-      } else {
-        const int c1 = (h + 1) * (x.n >> 1);
-        for (int c = h * (x.n >> 1); c < c1; c += kCols) {
-          const int col = x.n0 + c;
+      }
+    } else {
+      constexpr int kCols = kOut == 1 ? 64 : 32;                 // columns of a box, one box a warp
+      uint8_t* box = boxes + (warp - kEpiWarp0) * kWeightBox;
+      uint4 add[8];
+      if constexpr (kOut == 2)
+        if (u0 < U) {
+          const Tile x = tile_of<kMode>(p, groups, u0);
+          load_addend(p, x, x.m0 + (int)rank * kHalf + q * 32, x.n0 + h * (x.n >> 1), lane, add);
+        }
+      for (int u = u0; u < U && ok; u += ustep) {
+        const Tile x = tile_of<kMode>(p, groups, u);
+        const int m = x.m0 + (int)rank * kHalf + q * 32;         // first M row of the warp
+        const int width = x.n >> 1, c0 = x.n0 + h * width;       // its columns
+        f32x2 y[kHalf / 2];
+#pragma unroll
+        for (int j = 0; j < kHalf / 2; ++j) y[j] = 0ull;
+        for (int r = 0; r < x.rows; r += kFlush) {
+          if (!wait_full()) break;
+          constexpr int kLoad = kOut == 2 ? 32 : 64;             // (the addend takes registers, too)
+#pragma unroll
+          for (int i = 0; i < kHalf; i += kLoad) {
+            if (i >= width) break;
+            uint32_t v[kLoad];
+            if constexpr (kLoad == 64) {
+              tmem_ld64(tmem + acc * kTile + h * width + i, v);
+              tmem_wait_ld64(v);
+            } else {
+              tmem_ld32(tmem + acc * kTile + h * width + i, v);
+              tmem_wait_ld32(v);
+            }
+            if (i + kLoad == width) give_back();
+#pragma unroll
+            for (int j = 0; j < kLoad / 2; ++j)
+              y[i / 2 + j] = f2_add(y[i / 2 + j], f2_make(v[2 * j], v[2 * j + 1]));
+          }
+          if (++acc == kAcc) { acc = 0; aph ^= 1u; }
+        }
+        if (!ok) break;
+#pragma unroll
+        for (int b = 0; b < kHalf / kCols; ++b) {
+          if (b * kCols >= width) break;
+          const int col = c0 + b * kCols;
           if (lane == 0) bulk_wait_read();                       // the box's last store has read it
           __syncwarp();
           if constexpr (kOut == 2) {
@@ -538,42 +583,28 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
               *reinterpret_cast<uint4*>(box + (i * 4 + (lane >> 3)) * 128 +
                                         (((lane ^ (i * 4 + (lane >> 3))) & 7) << 4)) = add[i];
             __syncwarp();
-            if (c + kCols < c1) load_addend(p, x, m, col + kCols, lane, add);
+            if ((b + 1) * kCols < width) load_addend(p, x, m, col + kCols, lane, add);
             else if (u + ustep < U) {
-              const Tile y = tile_of<kMode>(p, groups, u + ustep);
-              load_addend(p, y, y.m0 + (int)rank * kHalf + q * 32, y.n0 + h * (y.n >> 1), lane, add);
+              const Tile t = tile_of<kMode>(p, groups, u + ustep);
+              load_addend(p, t, t.m0 + (int)rank * kHalf + q * 32, t.n0 + h * (t.n >> 1), lane, add);
             }
-          }
-          uint32_t w[32];
-          if constexpr (kOut == 1) {
-            uint32_t v[64];
-            if (!zero) {
-              tmem_ld64(tmem + acc * kTile + c, v);
-              tmem_wait_ld64(v);
-            }
-#pragma unroll
-            for (int j = 0; j < 32; ++j)
-              w[j] = zero ? 0u : pack_bf16x2(__uint_as_float(v[2 * j]), __uint_as_float(v[2 * j + 1]));
-          } else {
-            if (!zero) {
-              tmem_ld32(tmem + acc * kTile + c, w);
-              tmem_wait_ld32(w);
-            }
-#pragma unroll
-            for (int j = 0; j < 32; ++j) w[j] = zero ? 0u : w[j];
           }
 #pragma unroll
           for (int j = 0; j < 8; ++j) {
             uint4* at = reinterpret_cast<uint4*>(box + lane * 128 + ((j ^ (lane & 7)) << 4));
-            uint4 v = make_uint4(w[4 * j], w[4 * j + 1], w[4 * j + 2], w[4 * j + 3]);
-            if constexpr (kOut == 2) {
-              const uint4 a = *at;
-              v.x = __float_as_uint(__uint_as_float(v.x) + __uint_as_float(a.x));
-              v.y = __float_as_uint(__uint_as_float(v.y) + __uint_as_float(a.y));
-              v.z = __float_as_uint(__uint_as_float(v.z) + __uint_as_float(a.z));
-              v.w = __float_as_uint(__uint_as_float(v.w) + __uint_as_float(a.w));
+            if constexpr (kOut == 1) {
+              const f32x2* v = y + b * 32 + 4 * j;
+              *at = make_uint4(pack_bf16x2(f2_lo(v[0]), f2_hi(v[0])), pack_bf16x2(f2_lo(v[1]), f2_hi(v[1])),
+                               pack_bf16x2(f2_lo(v[2]), f2_hi(v[2])), pack_bf16x2(f2_lo(v[3]), f2_hi(v[3])));
+            } else {
+              f32x2 v0 = y[b * 16 + 2 * j], v1 = y[b * 16 + 2 * j + 1];
+              if constexpr (kOut == 2) {
+                const uint4 a = *at;
+                v0 = f2_add(v0, f2_make(a.x, a.y));
+                v1 = f2_add(v1, f2_make(a.z, a.w));
+              }
+              *at = make_uint4((uint32_t)v0, (uint32_t)(v0 >> 32), (uint32_t)v1, (uint32_t)(v1 >> 32));
             }
-            *at = v;
           }
           fence_proxy_async_smem();
           __syncwarp();
@@ -582,12 +613,6 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             bulk_commit();
           }
         }
-      }
-      if (kMode == kWeights && !zero) {
-        tc_fence_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive_cluster(tempty + 8u * acc);
-        if (++acc == kAcc) { acc = 0; aph ^= 1u; }
       }
     }
     if (kMode == kWeights && lane == 0) bulk_wait_all();
