@@ -53,9 +53,9 @@ constexpr uint32_t kABytes = kHalf * kBK * 2;
 constexpr int kAcc = 2;                             // TMEM accumulators of 256 columns
 // weights: rows that the tensor cores add up before registers take over.  Their additions truncate:
 // a sum of n rows comes out low by about n 2^-30 of itself (65536 rows: 8e-5, of numbers of one sign
-// 4e-4).  256 rows are 2e-7 off, the registers' additions round, and a read of TMEM every 2048
-// cycles of MMAs hides behind them.
-constexpr int kFlush = 256;
+// 4e-4).  512 rows are 5e-7 off, the registers' additions round, and a read of TMEM every 4096
+// cycles of MMAs hides behind them (256 rows: the same but with an addend, 473 us for 438).
+constexpr int kFlush = 512;
 constexpr int kMaxStages = 12;
 constexpr int kMaxGroups = 1024;
 // shared memory of the epilogue: a box of 32 tokens x 128 bf16 features for each column half, or for

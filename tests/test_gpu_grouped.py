@@ -43,9 +43,9 @@ def slack(n):
 
 
 def slack_w(n):
-    """Of the weights' gradients: the tensor cores add up 256 rows at a time (16 steps), registers
+    """Of the weights' gradients: the tensor cores add up 512 rows at a time (32 steps), registers
     those sums, each addition rounded to 2^-24."""
-    return (np.minimum(n, 256) / 16 + 2) * 2.0 ** -23 + n / 256 * 2.0 ** -24
+    return (np.minimum(n, 512) / 16 + 2) * 2.0 ** -23 + n / 512 * 2.0 ** -24
 
 
 def offsets(counts, first=0):
@@ -156,7 +156,7 @@ def test_backward_w(name, N, K, form):
 @pytest.mark.parametrize("sign", [False, True])
 def test_long_sums_keep_fp32(sign):
     # where the tensor cores' truncating sums alone would be 4e-5 (of one sign 2e-4) off
-    counts, N, K = [30000, 257, 0, 513], 64, 72
+    counts, N, K = [30000, 513, 0, 1025], 64, 72
     off, R = offsets(counts), sum(counts)
     x, dy = rand((R, K), 0), rand((R, N), 1)
     if sign:
