@@ -532,8 +532,10 @@ int lmoe_rms_norm(const lmoe_bf16* x, const lmoe_bf16* residual, const lmoe_bf16
 /* (not computed; no workspace is needed then).  grad_h may be grad_out, h or  */
 /* grad_residual.  Sums are fp32 in a fixed order: repeated calls give the     */
 /* same bits.  Limits of lmoe_rms_norm; H % 8 == 0.  T == 0: grad_norm_w       */
-/* becomes 0 where it is memory of the current device.  The workspace          */
-/* (256-byte aligned) does not fall as T grows.                               */
+/* becomes 0 where it is memory of the current device.  The sum of             */
+/* grad_out * norm_w * h over a row is taken in fp32 and must be in its range.  */
+/* The workspace (256-byte aligned, not shared with a call that may overlap)   */
+/* does not fall as T grows.                                                  */
 size_t lmoe_rms_norm_backward_workspace_bytes(int T, int H);
 int lmoe_rms_norm_backward(const lmoe_bf16* grad_out, const lmoe_bf16* h, const lmoe_bf16* norm_w,
                            const lmoe_bf16* grad_residual, float rms_eps, lmoe_bf16* grad_h,
@@ -563,7 +565,10 @@ int situ_and_mul_backward(const lmoe_bf16* in, const lmoe_bf16* grad_out, lmoe_b
 /* fp32 or NULL, with grad_w only (LMOE_ERR_NULL otherwise), may be grad_w     */
 /* itself (a gradient summed over micro-batches).  Every element of grad_w is  */
 /* written, add or 0 for experts without rows (also with rows == 0).           */
-/* Products are summed on the tensor cores in fp32 and rounded once; repeated  */
+/* Products are summed on the tensor cores in fp32 and rounded once.  Those     */
+/* sums truncate: out and grad_x come out low by up to n/16 * 2^-24 of the sum  */
+/* of n magnitudes (n = K, N), at 65536 a tenth of a bf16 rounding; grad_w's    */
+/* are taken 512 rows at a time and joined by rounded additions.  Repeated      */
 /* calls give the same bits.  A NaN or infinity in a row reaches that row of   */
 /* out and grad_x, and the gradients of its expert's weights, alone.           */
 /* Requires 1 <= E <= 1024, N % 8 == 0, K % 8 == 0, 8 <= N, K <= 65536,         */
@@ -624,8 +629,8 @@ int lmoe_linear(const lmoe_bf16* x, const lmoe_bf16* w, const lmoe_bf16* add, lm
 const char* lmoe_status_string(int status);
 
 /* Reads (and with clear != 0 resets) the device error word of the current    */
-/* device: 0 = nothing went wrong; 1-6 = a bounded wait of the tensor-core    */
-/* GEMM gave up; 7 = latent_moe_forward_routed met an expert id outside      */
+/* device: 0 = nothing went wrong; 1-6 = a bounded wait of a kernel gave up   */
+/* (of the tensor-core products, of a ring of copies); 7 = latent_moe_forward_routed met an expert id outside      */
 /* [0, E).  The first code written stays until cleared.  Synchronises the    */
 /* device.                                                                    */
 /* Returns the word, or LMOE_ERR_CUDA if it cannot be read.                   */

@@ -808,10 +808,22 @@ def situ_and_mul_backward(inp, grad_out, grad_in, beta: float, linear_beta: floa
 # --- bf16 products grouped by expert -----------------------------------------------
 
 
+def _grouped_shape(rows, weights, width: int, shape):
+    """(rows, E, N, K) of a [rows, N or K] matrix and [E, N, K] weights; width: the index of
+    the rows' width in [E, N, K]."""
+    if shape is not None:
+        return tuple(int(v) for v in shape)
+    R, wide = rows.shape
+    E, N, K = weights.shape
+    if wide != weights.shape[width]:
+        raise ValueError(f"rows of {wide} elements, weights {tuple(weights.shape)}")
+    return R, E, N, K
+
+
 def lmoe_grouped_linear(x, w, expert_offsets, out, stream=None, shape: tuple | None = None):
     """out [rows, N] = x [rows, K] @ w[e]^T for the rows of each expert e (expert_offsets[e] ..
     expert_offsets[e+1]); w [E, N, K].  shape (rows, E, N, K) for raw addresses."""
-    R, E, N, K = (int(v) for v in (shape if shape is not None else (x.shape[0], *w.shape)))
+    R, E, N, K = _grouped_shape(x, w, 2, shape)
     st = load_library().lmoe_grouped_linear(
         _dev(x, "x", _BF16, R * K), _dev(w, "w", _BF16, E * N * K),
         _dev(expert_offsets, "expert_offsets", torch.int32, E + 1), _dev(out, "out", _BF16, R * N),
@@ -822,7 +834,7 @@ def lmoe_grouped_linear(x, w, expert_offsets, out, stream=None, shape: tuple | N
 def lmoe_grouped_linear_backward_x(grad_out, w, expert_offsets, grad_x, stream=None,
                                    shape: tuple | None = None):
     """grad_x [rows, K] = grad_out [rows, N] @ w[e] for the rows of each expert e."""
-    R, E, N, K = (int(v) for v in (shape if shape is not None else (grad_out.shape[0], *w.shape)))
+    R, E, N, K = _grouped_shape(grad_out, w, 1, shape)
     st = load_library().lmoe_grouped_linear_backward_x(
         _dev(grad_out, "grad_out", _BF16, R * N), _dev(w, "w", _BF16, E * N * K),
         _dev(expert_offsets, "expert_offsets", torch.int32, E + 1),
@@ -835,7 +847,9 @@ def lmoe_grouped_linear_backward_w(grad_out, x, expert_offsets, grad_w, add=None
     """grad_w[e] [N, K] = grad_out^T @ x over the rows of expert e (+ add[e]), fp32 or bf16 by
     grad_w's dtype; add fp32, with an fp32 grad_w only (it may be grad_w).  Raw addresses: shape
     (rows, E, N, K), grad_w is fp32 then."""
-    R, E, N, K = (int(v) for v in (shape if shape is not None else (x.shape[0], *grad_w.shape)))
+    R, E, N, K = _grouped_shape(x, grad_w, 2, shape)
+    if shape is None and tuple(grad_out.shape) != (R, N):
+        raise ValueError(f"grad_out {tuple(grad_out.shape)}, expected {(R, N)}")
     half = getattr(grad_w, "dtype", torch.float32) in _BF16
     out = _dev(grad_w, "grad_w", _BF16 if half else torch.float32, E * N * K)
     st = load_library().lmoe_grouped_linear_backward_w(

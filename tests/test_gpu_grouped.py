@@ -260,6 +260,60 @@ def test_far_rows_and_experts():
     assert torch.equal(dw[-2:], dws) and not dw[:-2].any()
 
 
+def test_most_experts_in_large_tiles():
+    # the largest table beside the largest stages
+    E, N, K = 1024, 40, 64
+    counts = [(37 * i) % 83 for i in range(E)]
+    off, R = offsets(counts), sum(counts)
+    assert R > 32 * E
+    x, w = rand((R, K), 0), rand((E, N, K), 1)
+    out = torch.empty((R, N), dtype=torch.bfloat16, device="cuda")
+    lm.lmoe_grouped_linear(x, w, off, out)
+    ref = O.grouped_linear(f64(x), f64(w), f64(off), np.zeros((R, N)))
+    mag = O.grouped_linear(np.abs(f64(x)), np.abs(f64(w)), f64(off), np.zeros((R, N)))
+    assert np.all(np.abs(f64(out) - ref) <= BF16 * (1 + 2 ** -7) * np.abs(ref) + slack(K) * mag)
+
+
+FIRST_IN_CAPTURE = """
+import torch, latent_mixture_experts_sigmoid_gb300 as lm
+d, b, f = "cuda", torch.bfloat16, torch.float32
+x, w = torch.randn((40, 1040), device=d).to(b), torch.randn((2, 64, 1040), device=d).to(b)
+off = torch.tensor([0, 30, 40], dtype=torch.int32, device=d)
+y, dx, dw = torch.zeros((40, 64), dtype=b, device=d), torch.zeros_like(x), torch.zeros((2, 64, 1040), device=d)
+n, dh, ds = torch.zeros_like(x), torch.zeros_like(x), torch.zeros((40, 64), dtype=b, device=d)
+g, dg = torch.zeros(1040, device=d), torch.randn((40, 32), device=d).to(b)
+lm.load_library()
+ws = torch.empty(lm.lmoe_rms_norm_backward_workspace_bytes(40, 1040), dtype=torch.uint8, device=d)
+def run():
+    lm.lmoe_rms_norm(x, None, 1e-6, out=n)
+    lm.lmoe_grouped_linear(n, w, off, y)
+    lm.situ_and_mul_backward(y, dg, ds, 4.0, 8.0)
+    lm.lmoe_grouped_linear_backward_x(ds, w, off, dx)
+    lm.lmoe_grouped_linear_backward_w(ds, n, off, dw)
+    lm.lmoe_rms_norm_backward(dx, x, None, 1e-6, dh, grad_norm_w=g, workspace=ws)
+torch.cuda.synchronize()
+graph = torch.cuda.CUDAGraph()
+with torch.cuda.graph(graph):
+    run()
+graph.replay()
+torch.cuda.synchronize()
+got = [t.clone() for t in (y, dx, dw, dh, g)]
+run()
+torch.cuda.synchronize()
+assert all(torch.equal(a, b) and a.any() for a, b in zip(got, (y, dx, dw, dh, g)))
+assert lm.lmoe_device_error() == 0
+"""
+
+
+def test_first_call_of_a_process_inside_a_capture():
+    import os
+    import subprocess
+    import sys
+    root = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+    r = subprocess.run([sys.executable, "-c", FIRST_IN_CAPTURE], cwd=root, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]
+
+
 def test_no_rows():
     w, off = rand((3, 64, 64), 0), torch.zeros(4, dtype=torch.int32, device="cuda")
     e = torch.empty((0, 64), dtype=torch.bfloat16, device="cuda")

@@ -110,6 +110,11 @@ def test_binding_refuses_host_tensors():
     b, f = torch.zeros((4, 128), dtype=torch.bfloat16), torch.zeros((4, 1))
     off = torch.zeros(3, dtype=torch.int32)
     w = torch.zeros((2, 128, 128), dtype=torch.bfloat16)
+    for call in (lambda: lm.lmoe_grouped_linear(b[:, :64], w, off, b),            # widths that do not fit
+                 lambda: lm.lmoe_grouped_linear_backward_x(b[:, :64], w, off, b),
+                 lambda: lm.lmoe_grouped_linear_backward_w(b[:2], b, off, w)):
+        with pytest.raises(ValueError, match="rows of 64|grad_out"):
+            call()
     for call in (lambda: lm.lmoe_rms_norm(b, None, 1e-6, out=b),
                  lambda: lm.lmoe_rms_norm_backward(b, b, None, 1e-6, b),
                  lambda: lm.situ_and_mul_backward(b, b, b, 4.0, 8.0),
