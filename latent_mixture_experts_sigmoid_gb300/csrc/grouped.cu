@@ -707,9 +707,28 @@ cudaError_t launch(const Maps& m, Params& p, long long units, cudaStream_t s) {
                           m.bp, m.o, p);
 }
 
+// Whether few rows stream through registers (grouped_stream.cu), by what both forms take in
+// microseconds if every row has an expert of its own (the offsets are on the device).  That form:
+// its CTAs, then the weights at 4.4 TB/s.  Here: the launch and a unit's K blocks one after another,
+// or the weights at 6.2 TB/s.  Measured, stream / here, rows of different experts:
+//   forward 1024 x 2048:  1 row 5.2 / 12.2, 8 rows 9.4 / 12.5, 16 rows 18.6 / 16.3
+//   forward 2048 x 512:   1 row 3.3 / 7.2,  8 rows 6.7 / 7.6,  16 rows 13.0 / 10.3
+//   rows    1024 x 2048:  1 row 5.6 / 9.2,  4 rows 5.9 / 9.4,  8 rows 11.8 / 9.7
+//   rows    2048 x 512:   1 row 5.8 / 12.1, 16 rows 10.3 / 12.5, 32 rows 19.5 / 16.2
+//   forward 256 x 128:    1 row 2.1 / 5.0,  128 rows of 16 experts 4.1 / 5.1, 256 rows 5.8 / 5.2
+bool streams(const GroupedLinear& g, bool backward) {
+  const long long ctas = grouped_stream_ctas(g, backward);
+  if (ctas > 4096) return false;
+  const double bytes = 2.0 * (double)(g.R < g.E ? g.R : g.E) * g.N * g.K;
+  const double few = 2.2 + 0.0009 * (double)ctas + bytes / 4.4e6;
+  const double latency = 5.3 + 0.0035 * (backward ? g.N : g.K), stream = bytes / 6.2e6;
+  return few < (latency > stream ? latency : stream);
+}
+
 }  // namespace
 
 cudaError_t launch_grouped_linear(const GroupedLinear& g, bool backward, cudaStream_t s) {
+  if (streams(g, backward)) return launch_grouped_stream(g, backward, s);
   Params p{};
   p.E = g.E;
   p.mdim = backward ? g.K : g.N;

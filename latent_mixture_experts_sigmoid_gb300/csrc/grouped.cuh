@@ -32,6 +32,9 @@ struct GroupedWeightGrad {
   int E, N, K;
 };
 
+// ... for few rows in all (grouped_stream.cu); launch_grouped_linear calls it
+long long grouped_stream_ctas(const GroupedLinear& g, bool backward);
+cudaError_t launch_grouped_stream(const GroupedLinear& g, bool backward, cudaStream_t s);
 cudaError_t launch_grouped_linear(const GroupedLinear& g, bool backward, cudaStream_t s);
 cudaError_t launch_grouped_weight_grad(const GroupedWeightGrad& g, cudaStream_t s);
 

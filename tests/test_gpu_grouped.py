@@ -217,6 +217,12 @@ def test_specials_stay_with_their_rows(value):
     assert torch.equal(y[others], want[0][others]) and torch.equal(dx[others], want[1][others])
 
 
+def near(got, fn, rows, w, off, terms):
+    rows, w, shape = f64(rows), f64(w), tuple(got.shape)
+    ref, mag = fn(rows, w, off, np.zeros(shape)), fn(np.abs(rows), np.abs(w), off, np.zeros(shape))
+    assert np.all(np.abs(f64(got) - ref) <= BF16 * (1 + 2 ** -7) * np.abs(ref) + slack(terms) * mag)
+
+
 def test_far_rows_and_experts():
     # element offsets past 2^31: the last rows of a long batch, the last of many experts
     K, N = 2048, 72
@@ -225,39 +231,39 @@ def test_far_rows_and_experts():
     tail = rand((200, K), 0)
     x[-200:] = tail
     off = torch.tensor([R - 190, R - 150, R - 3], dtype=torch.int32, device="cuda")
+    rel, rows = [0, 40, 187], slice(R - 190, R - 3)
     w = rand((2, N, K), 1, 0.05)
     out = torch.empty((R, N), dtype=torch.bfloat16, device="cuda")
     lm.lmoe_grouped_linear(x, w, off, out)
-    rel = torch.tensor([0, 40, 187], dtype=torch.int32, device="cuda")
-    small = torch.empty((187, N), dtype=torch.bfloat16, device="cuda")
-    lm.lmoe_grouped_linear(tail[10:197].contiguous(), w, rel, small)
-    assert torch.equal(out[R - 190:R - 3], small)
+    near(out[rows], O.grouped_linear, tail[10:197], w, rel, K)
     dy = torch.empty((R, N), dtype=torch.bfloat16, device="cuda")
     dy[-200:] = rand((200, N), 2)
-    dx, dw, dws = torch.empty_like(x), torch.empty((2, N, K), device="cuda"), torch.empty((2, N, K), device="cuda")
+    dx, dw = torch.empty_like(x), torch.empty((2, N, K), device="cuda")
     lm.lmoe_grouped_linear_backward_x(dy, w, off, dx)
+    near(dx[rows], O.grouped_linear_backward_x, dy[rows], w, rel, N)
     lm.lmoe_grouped_linear_backward_w(dy, x, off, dw)
-    sx = torch.empty((187, K), dtype=torch.bfloat16, device="cuda")
-    part = dy[R - 190:R - 3].contiguous()
-    lm.lmoe_grouped_linear_backward_x(part, w, rel, sx)
-    lm.lmoe_grouped_linear_backward_w(part, tail[10:197].contiguous(), rel, dws)
-    assert torch.equal(dx[R - 190:R - 3], sx) and torch.equal(dw, dws)
+    ref = O.grouped_linear_backward_w(f64(dy[rows]), f64(tail[10:197]), rel)
+    mag = O.grouped_linear_backward_w(np.abs(f64(dy[rows])), np.abs(f64(tail[10:197])), rel)
+    assert np.all(np.abs(f64(dw) - ref) <= 2.0 ** -24 * np.abs(ref) + slack_w(150) * mag)
     del x, dx, dy, out
     E, N, K = 1024, 1032, 2088                          # 2.2e9 weights
     w = torch.zeros((E, N, K), dtype=torch.bfloat16, device="cuda")
     w[-2:] = rand((2, N, K), 3, 0.05)
-    off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
-    off[-2], off[-1] = 30, 70
-    x, out, sm = rand((70, K), 4), torch.empty((70, N), dtype=torch.bfloat16, device="cuda"), None
-    lm.lmoe_grouped_linear(x, w, off, out)
-    sm = torch.empty_like(out)
-    lm.lmoe_grouped_linear(x, w[-2:].contiguous(), torch.tensor([0, 30, 70], dtype=torch.int32, device="cuda"), sm)
-    assert torch.equal(out, sm)
+    for counts in ([30, 40], [1, 1]):                   # a few rows more and fewer than tiles are worth
+        R = sum(counts)
+        off = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+        off[-2], off[-1] = counts[0], R
+        rel = [0, counts[0], R]
+        x, dy = rand((R, K), 4), rand((R, N), 5)
+        out, dx = torch.empty((R, N), dtype=torch.bfloat16, device="cuda"), torch.empty((R, K), dtype=torch.bfloat16, device="cuda")
+        lm.lmoe_grouped_linear(x, w, off, out)
+        near(out, O.grouped_linear, x, w[-2:], rel, K)
+        lm.lmoe_grouped_linear_backward_x(dy, w, off, dx)
+        near(dx, O.grouped_linear_backward_x, dy, w[-2:], rel, N)
     dw = torch.full((E, N, K), 7.0, dtype=torch.bfloat16, device="cuda")
-    lm.lmoe_grouped_linear_backward_w(out, x, off, dw)
-    dws = torch.empty((2, N, K), dtype=torch.bfloat16, device="cuda")
-    lm.lmoe_grouped_linear_backward_w(out, x, torch.tensor([0, 30, 70], dtype=torch.int32, device="cuda"), dws)
-    assert torch.equal(dw[-2:], dws) and not dw[:-2].any()
+    lm.lmoe_grouped_linear_backward_w(dy, x, off, dw)
+    ref = O.grouped_linear_backward_w(f64(dy), f64(x), rel)
+    assert np.all(np.abs(f64(dw[-2:]) - ref) <= BF16 * (1 + 2 ** -7) * np.abs(ref) + 1e-30) and not dw[:-2].any()
 
 
 def test_most_experts_in_large_tiles():
