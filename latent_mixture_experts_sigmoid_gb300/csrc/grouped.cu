@@ -56,7 +56,8 @@ constexpr int kAcc = 2;                             // TMEM accumulators of 256 
 // 4e-4).  512 rows are 5e-7 off, the registers' additions round, and a read of TMEM every 4096
 // cycles of MMAs hides behind them (256 rows: the same but with an addend, 473 us for 438).
 constexpr int kFlush = 512;
-constexpr int kMaxStages = 12;
+constexpr int kMaxStages = 8;
+constexpr int kPartBox = 32;                        // token rows of a partial box
 constexpr int kMaxGroups = 1024;
 // shared memory of the epilogue: a box of 32 tokens x 128 bf16 features for each column half, or for
 // each warp one of 32 rows x 128 bytes of a gradient of weights
@@ -68,7 +69,7 @@ __host__ __device__ constexpr uint32_t out_bytes(int mode) {
 struct Params {
   int E, mdim, depth, ncols;     // M side's extent; terms of a sum and (weights) N side's extent
   int mtiles, ntiles;            // tiles of a group, ntiles: weights only
-  int nt, part;                  // most token rows of a tile; rows of a partial box
+  int nt;                        // most token rows of a tile
   int stages;
   uint32_t stage_bytes;
   long long R;
@@ -351,8 +352,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         const int nkb = kMode == kWeights ? (x.rows + kBK - 1) / kBK : nkb_rows;
         // token rows: one box of all, or as many partial ones as this CTA's half takes
         const bool whole = x.n == p.nt;
-        const int nbox = whole ? 1 : (half + p.part - 1) / p.part;
-        const int brows = whole ? p.nt >> 1 : p.part;
+        const int nbox = whole ? 1 : (half + kPartBox - 1) / kPartBox;
+        const int brows = whole ? p.nt >> 1 : kPartBox;
         const int tok = x.row0 + (int)rank * half;
         const int nchunk = x.n >> 7;                   // (weights: 64 columns each)
         const int n0 = x.n0 + (int)rank * half;
@@ -734,8 +735,11 @@ cudaError_t launch_grouped_linear(const GroupedLinear& g, bool backward, cudaStr
   p.mdim = backward ? g.K : g.N;
   p.depth = backward ? g.N : g.K;
   p.mtiles = ceil_div(p.mdim, kTile);
-  p.nt = g.R <= 8ll * g.E ? 32 : g.R <= 32ll * g.E ? 128 : 256;
-  p.part = p.nt >= 64 ? 32 : 16;
+  // Most token rows of a tile: with few rows an expert, smaller token boxes leave room for eight stages
+  // of weights, not six (896 experts of 1024 x 2048, 128 / 256 rows: 16384 rows 560 / 575 us, 65536 rows
+  // 604 / 619; 128 experts of 2048 x 512: 8192 rows 52 / 54, 32768 rows 102 / 78.  32 and 64 were behind
+  // one of the two everywhere.)
+  p.nt = g.R <= 96ll * g.E ? 128 : 256;
   p.stage_bytes = kABytes + (uint32_t)p.nt * 64;
   p.R = g.R;
   p.offsets = g.offsets;
@@ -743,7 +747,7 @@ cudaError_t launch_grouped_linear(const GroupedLinear& g, bool backward, cudaStr
   Maps m;
   if (!make_map(&m.a, g.w, false, g.E, g.N, g.K, backward ? kBK : kHalf) ||
       !make_map(&m.b, g.rows_in, false, 0, g.R, p.depth, p.nt / 2) ||
-      !make_map(&m.bp, g.rows_in, false, 0, g.R, p.depth, p.part))
+      !make_map(&m.bp, g.rows_in, false, 0, g.R, p.depth, kPartBox))
     return cudaErrorInvalidValue;
   m.ap = m.a;
   m.o = m.a;

@@ -12,7 +12,7 @@
 //             column j of each thread's four makes MMA j (pairs of rows packed by byte permutes)
 // The warps' partial sums meet in shared memory and are added in order.
 // One row, 1024 x 2048: forward 5.2 us, rows 5.6; 2048 x 512: 3.3 and 5.8; 256 x 128: 2.1 and 2.3 (tiles of
-// 256: 12.2, 9.2, 7.2, 12.1, 5.0, 5.3).  Rows of 64 columns a CTA, 32 warps' sums less: 7.8 for 5.6 us.
+// 256: 12.2, 9.2, 7.2, 12.1, 5.0, 5.3); rows with 64 columns and eight parts of N a CTA: 7.8 us.
 #include "grouped.cuh"
 
 namespace lmoe {
