@@ -210,16 +210,29 @@ def _ptr(t) -> int | None:
 _BF16 = (torch.bfloat16, torch.int16)   # bf16 values, or their raw 16-bit patterns
 
 
-def _dev(t, name: str, dtypes, numel: int) -> int | None:
+_get_device = getattr(torch._C, "_cuda_getDevice", None)           # (looked up once: 30 ns a call)
+_get_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _current_device() -> int:
+    """The current CUDA device, -2 (no tensor's) where there is none."""
+    try:
+        return _get_device()
+    except (TypeError, RuntimeError):
+        return -2
+
+
+def _dev(t, name: str, dtypes, numel: int, device: int | None = None) -> int | None:
     """Device address of a tensor argument, after checking that the kernels can
     access it as the C ABI describes: a contiguous tensor on the current CUDA
     device, of one of `dtypes`, holding at least `numel` elements.  None and raw
-    integer addresses pass through unchecked (the caller vouches for them)."""
+    integer addresses pass through unchecked (the caller vouches for them).
+    device: _current_device(), where a call with many tensors has asked once."""
     if t is None or type(t) is int:
         return t
     try:
         # one pass of cheap queries; whatever fails it is told apart below
-        if (t.get_device() == torch._C._cuda_getDevice() and t.is_contiguous()
+        if (t.get_device() == (_current_device() if device is None else device) and t.is_contiguous()
                 and (t.dtype is dtypes or t.dtype in dtypes) and t.numel() >= numel):
             return t.data_ptr()
     except (AttributeError, TypeError, RuntimeError):
@@ -251,7 +264,7 @@ def _stream(stream) -> int | None:
     if stream is None:
         if torch.cuda.is_initialized():
             # the current stream's handle without building a torch.cuda.Stream (0.3 us, not 3.6)
-            return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+            return _get_raw_stream(_get_device())
         if torch.cuda.is_available():
             return torch.cuda.current_stream().cuda_stream
         return None
@@ -760,11 +773,12 @@ def lmoe_rms_norm(x, norm_w, rms_eps: float, out=None, codes=None, scales=None, 
         H = x.shape[-1]
         T = x.numel() // H
     T, H = int(T), int(H)
+    here = _current_device()
     st = load_library().lmoe_rms_norm(
-        _dev(x, "x", _BF16, T * H), _dev(residual, "residual", _BF16, T * H),
-        _dev(norm_w, "norm_w", _BF16, H), float(rms_eps),
-        _dev(residual_out, "residual_out", _BF16, T * H), _dev(out, "out", _BF16, T * H),
-        _dev(codes, "codes", _E4M3, T * H), _dev(scales, "scales", torch.float32, T * _blocks(H)),
+        _dev(x, "x", _BF16, T * H, here), _dev(residual, "residual", _BF16, T * H, here),
+        _dev(norm_w, "norm_w", _BF16, H, here), float(rms_eps),
+        _dev(residual_out, "residual_out", _BF16, T * H, here), _dev(out, "out", _BF16, T * H, here),
+        _dev(codes, "codes", _E4M3, T * H, here), _dev(scales, "scales", torch.float32, T * _blocks(H), here),
         T, H, _stream(stream))
     _check(st, "lmoe_rms_norm")
 
@@ -783,11 +797,12 @@ def lmoe_rms_norm_backward(grad_out, h, norm_w, rms_eps: float, grad_h, grad_nor
         T = h.numel() // H
     T, H = int(T), int(H)
     wsp, wsn = _workspace(workspace, None)
+    here = _current_device()
     st = load_library().lmoe_rms_norm_backward(
-        _dev(grad_out, "grad_out", _BF16, T * H), _dev(h, "h", _BF16, T * H),
-        _dev(norm_w, "norm_w", _BF16, H), _dev(grad_residual, "grad_residual", _BF16, T * H),
-        float(rms_eps), _dev(grad_h, "grad_h", _BF16, T * H),
-        _dev(grad_norm_w, "grad_norm_w", torch.float32, H), T, H, wsp, wsn, _stream(stream))
+        _dev(grad_out, "grad_out", _BF16, T * H, here), _dev(h, "h", _BF16, T * H, here),
+        _dev(norm_w, "norm_w", _BF16, H, here), _dev(grad_residual, "grad_residual", _BF16, T * H, here),
+        float(rms_eps), _dev(grad_h, "grad_h", _BF16, T * H, here),
+        _dev(grad_norm_w, "grad_norm_w", torch.float32, H, here), T, H, wsp, wsn, _stream(stream))
     _check(st, "lmoe_rms_norm_backward")
 
 
@@ -798,9 +813,10 @@ def situ_and_mul_backward(inp, grad_out, grad_in, beta: float, linear_beta: floa
         d = inp.shape[-1] // 2
         N = inp.numel() // (2 * d)
     N, d = int(N), int(d)
+    here = _current_device()
     st = load_library().situ_and_mul_backward(
-        _dev(inp, "input", _BF16, N * 2 * d), _dev(grad_out, "grad_out", _BF16, N * d),
-        _dev(grad_in, "grad_in", _BF16, N * 2 * d), N, d, float(beta), float(linear_beta),
+        _dev(inp, "input", _BF16, N * 2 * d, here), _dev(grad_out, "grad_out", _BF16, N * d, here),
+        _dev(grad_in, "grad_in", _BF16, N * 2 * d, here), N, d, float(beta), float(linear_beta),
         _stream(stream))
     _check(st, "situ_and_mul_backward")
 
@@ -824,9 +840,10 @@ def lmoe_grouped_linear(x, w, expert_offsets, out, stream=None, shape: tuple | N
     """out [rows, N] = x [rows, K] @ w[e]^T for the rows of each expert e (expert_offsets[e] ..
     expert_offsets[e+1]); w [E, N, K].  shape (rows, E, N, K) for raw addresses."""
     R, E, N, K = _grouped_shape(x, w, 2, shape)
+    here = _current_device()
     st = load_library().lmoe_grouped_linear(
-        _dev(x, "x", _BF16, R * K), _dev(w, "w", _BF16, E * N * K),
-        _dev(expert_offsets, "expert_offsets", torch.int32, E + 1), _dev(out, "out", _BF16, R * N),
+        _dev(x, "x", _BF16, R * K, here), _dev(w, "w", _BF16, E * N * K, here),
+        _dev(expert_offsets, "expert_offsets", torch.int32, E + 1, here), _dev(out, "out", _BF16, R * N, here),
         R, E, N, K, _stream(stream))
     _check(st, "lmoe_grouped_linear")
 
@@ -835,10 +852,11 @@ def lmoe_grouped_linear_backward_x(grad_out, w, expert_offsets, grad_x, stream=N
                                    shape: tuple | None = None):
     """grad_x [rows, K] = grad_out [rows, N] @ w[e] for the rows of each expert e."""
     R, E, N, K = _grouped_shape(grad_out, w, 1, shape)
+    here = _current_device()
     st = load_library().lmoe_grouped_linear_backward_x(
-        _dev(grad_out, "grad_out", _BF16, R * N), _dev(w, "w", _BF16, E * N * K),
-        _dev(expert_offsets, "expert_offsets", torch.int32, E + 1),
-        _dev(grad_x, "grad_x", _BF16, R * K), R, E, N, K, _stream(stream))
+        _dev(grad_out, "grad_out", _BF16, R * N, here), _dev(w, "w", _BF16, E * N * K, here),
+        _dev(expert_offsets, "expert_offsets", torch.int32, E + 1, here),
+        _dev(grad_x, "grad_x", _BF16, R * K, here), R, E, N, K, _stream(stream))
     _check(st, "lmoe_grouped_linear_backward_x")
 
 
@@ -851,10 +869,11 @@ def lmoe_grouped_linear_backward_w(grad_out, x, expert_offsets, grad_w, add=None
     if shape is None and tuple(grad_out.shape) != (R, N):
         raise ValueError(f"grad_out {tuple(grad_out.shape)}, expected {(R, N)}")
     half = getattr(grad_w, "dtype", torch.float32) in _BF16
-    out = _dev(grad_w, "grad_w", _BF16 if half else torch.float32, E * N * K)
+    here = _current_device()
+    out = _dev(grad_w, "grad_w", _BF16 if half else torch.float32, E * N * K, here)
     st = load_library().lmoe_grouped_linear_backward_w(
-        _dev(grad_out, "grad_out", _BF16, R * N), _dev(x, "x", _BF16, R * K),
-        _dev(expert_offsets, "expert_offsets", torch.int32, E + 1),
-        _dev(add, "add", torch.float32, E * N * K), None if half else out, out if half else None,
+        _dev(grad_out, "grad_out", _BF16, R * N, here), _dev(x, "x", _BF16, R * K, here),
+        _dev(expert_offsets, "expert_offsets", torch.int32, E + 1, here),
+        _dev(add, "add", torch.float32, E * N * K, here), None if half else out, out if half else None,
         R, E, N, K, _stream(stream))
     _check(st, "lmoe_grouped_linear_backward_w")

@@ -10,6 +10,8 @@
 // and its outputs, and is written once.  h is not rounded before it is normalised.
 #include <float.h>
 
+#include <atomic>
+
 #include "fp8_quant.cuh"
 #include "norm.cuh"
 #include "tc_ptx.cuh"
@@ -507,9 +509,15 @@ BackwardPlan backward_plan(int T, int H, bool residual) {
 
 template <int kVec>
 cudaError_t launch_long(const NormBackward& n, const BackwardPlan& b, cudaStream_t s) {
-  const cudaError_t e = cudaFuncSetAttribute(norm_backward_kernel<kVec>,
-                                             cudaFuncAttributeMaxDynamicSharedMemorySize, 216 * 1024);
-  if (e != cudaSuccess) return e;
+  static std::atomic<bool> set[64];              // (once a device)
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return cudaErrorInvalidDevice;
+  if (!set[dev].load(std::memory_order_acquire)) {
+    const cudaError_t e = cudaFuncSetAttribute(norm_backward_kernel<kVec>,
+                                               cudaFuncAttributeMaxDynamicSharedMemorySize, 216 * 1024);
+    if (e != cudaSuccess) return e;
+    set[dev].store(true, std::memory_order_release);
+  }
   return launch_k(norm_backward_kernel<kVec>, dim3(b.blocks), dim3(b.threads), b.smem, s, n, b.stages);
 }
 
