@@ -543,8 +543,8 @@ int lmoe_rms_norm_backward(const lmoe_bf16* grad_out, const lmoe_bf16* h, const 
                            size_t workspace_bytes, void* stream);
 
 /* The gradient of situ_and_mul: grad_in [N, 2d] of in [N, 2d] and grad_out   */
-/* [N, d], all bf16 (grad_in may be in).  Requires d % 8 == 0, N * d <= 2^40;  */
-/* beta <= 0 -> LMOE_ERR_BETA.                                                */
+/* [N, d], all bf16 (grad_in may be in).  Requires d % 8 == 0, d <= 2^26,      */
+/* N * d <= 2^40; beta <= 0 -> LMOE_ERR_BETA.                                 */
 int situ_and_mul_backward(const lmoe_bf16* in, const lmoe_bf16* grad_out, lmoe_bf16* grad_in,
                           int64_t N, int d, float beta, float linear_beta, void* stream);
 

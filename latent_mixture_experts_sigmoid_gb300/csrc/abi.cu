@@ -1449,7 +1449,8 @@ int lmoe_rms_norm_backward(const lmoe_bf16* grad_out, const lmoe_bf16* h, const 
 int situ_and_mul_backward(const lmoe_bf16* in, const lmoe_bf16* grad_out, lmoe_bf16* grad_in,
                           int64_t N, int d, float beta, float linear_beta, void* stream) {
   if (!finite_pos(beta)) return LMOE_ERR_BETA;
-  if (N < 0 || d <= 0 || d % 8 || !isfinite(linear_beta) || N > (1ll << 40) / d) return LMOE_ERR_DIM;
+  if (N < 0 || d <= 0 || d % 8 || d > 1 << 26 || !isfinite(linear_beta) || N > (1ll << 40) / d)
+    return LMOE_ERR_DIM;
   if (N == 0) return LMOE_OK;
   if (!in || !grad_out || !grad_in) return LMOE_ERR_NULL;
   if (!aligned16(in) || !aligned16(grad_out) || !aligned16(grad_in)) return LMOE_ERR_ALIGN;

@@ -443,7 +443,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           for (int k = 0; k < depth; k += kBK) {
             const bool fresh = kMode == kWeights ? k % kFlush == 0 : k == 0;     // a new accumulator
             if (fresh) {
-              ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kTempty + (int)acc), aph ^ 1u, abort_flag, p.err, kErrMmaTmem));
+              ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kTempty + (int)acc), aph ^ 1u, abort_flag,
+                                                      p.err, kErrMmaTmem));
               if (!ok) break;
             }
             ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kFull + s), ph, abort_flag, p.err, kErrMmaFull));
@@ -486,7 +487,9 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           const int left = x.rows & (kBK - 1);
           if (left == 0) continue;
           const int s = (int)((it - 1) % (uint32_t)p.stages);
-          if (!__all_sync(0xFFFFFFFFu, wait_phase(bar_at(kLast + s), (lph >> s) & 1u, abort_flag, p.err, kErrProducer))) break;
+          if (!__all_sync(0xFFFFFFFFu, wait_phase(bar_at(kLast + s), (lph >> s) & 1u, abort_flag, p.err,
+                                                  kErrProducer)))
+            break;
           lph ^= 1u << s;
           const int z = (-left & 15) * 8;              // 16-byte pieces of the rows up to the next 16
           uint8_t* at = smem + (size_t)s * p.stage_bytes + left * 128;
@@ -686,6 +689,11 @@ int pairs_resident() {
   if (cache[dev]) return cache[dev];
   auto* kern = grouped_kernel<kMode, kOut>;
   if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kMaxSmem) != cudaSuccess)
+    return 0;
+  // (the register split of the weights' kernels waits for ever in a launch with fewer)
+  cudaFuncAttributes fa;
+  if (cudaFuncGetAttributes(&fa, kern) != cudaSuccess ||
+      (kMode == kWeights && fa.numRegs * kThreads < 40 * kEpiWarp0 * 32 + 232 * kEpiWarps * 32))
     return 0;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(2 * num_sms());

@@ -67,6 +67,9 @@ COUNTS = {
 DIMS = [(8, 8), (64, 64), (256, 128), (136, 200), (120, 264), (1024, 512), (384, 1032)]
 FEW = [("borders", 256, 128), ("borders", 136, 200), ("more borders", 1032, 72), ("many small", 520, 136), ("large", 264, 520)]
 CASES = [(c, n, k) for c in COUNTS for n, k in DIMS if COUNTS[c] != [1500] or n * k < 1 << 18]
+# rows enough that tiles take the narrowest matrices, too; the widest ones, with few and with more rows
+COUNTS |= {"long": [5000, 0, 37], "few": [1, 2], "some": [300, 0, 31]}
+CASES += [("long", 8, 8), ("long", 24, 40), ("few", 16, 65536), ("some", 16, 65536), ("few", 65536, 16), ("some", 65536, 16)]
 
 
 def make(name, N, K, seed=0):

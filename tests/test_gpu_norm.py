@@ -67,7 +67,7 @@ def check_codes(codes, scales, y, bound):
 
 
 SHAPES = [(1, 8), (3, 16), (5, 48), (9, 256), (17, 264), (33, 512), (8, 1024), (7, 1032), (2, 2048), (305, 2064), (1, 7168),
-          (13, 7168), (400, 7168), (3, 8192), (2, 8200), (310, 8208), (1, 16384), (306, 16384), (2500, 128), (700, 144)]
+          (13, 7168), (400, 7168), (3, 8192), (2, 8200), (310, 8208), (1, 16384), (306, 16384), (2500, 128), (700, 144), (70000, 16)]
 
 
 @pytest.mark.parametrize("T,H", SHAPES)
@@ -170,7 +170,7 @@ def test_specials_stay_in_their_row(H):
 
 
 BACK = [(1, 8), (2, 16), (9, 256), (40, 264), (100, 520), (1300, 1024), (3, 1032), (33, 2048), (700, 2056), (300, 4096), (1, 4104),
-        (650, 7168), (5, 8192), (40, 8200), (1300, 16384), (5000, 64), (6000, 1024)]
+        (650, 7168), (5, 8192), (40, 8200), (1300, 16384), (5000, 64), (6000, 1024), (70000, 16)]
 
 
 @pytest.mark.parametrize("residual", [False, True])

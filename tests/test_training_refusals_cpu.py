@@ -58,6 +58,7 @@ def test_rms_norm_backward(lib):
 def test_situ_backward(lib):
     f = lib.situ_and_mul_backward
     assert f(p, p, p, 4, 8, 0.0, 8.0, None) == -4 and f(p, p, p, 4, 8, float("nan"), 8.0, None) == -4
+    assert f(p, p, p, 4, (1 << 26) + 8, 4.0, 8.0, None) == -2
     assert f(p, p, p, 4, 12, 4.0, 8.0, None) == -2 and f(p, p, p, -4, 8, 4.0, 8.0, None) == -2
     assert f(p, p, p, 4, 8, 4.0, float("inf"), None) == -2 and f(p, p, p, (1 << 40) // 8 + 1, 8, 4.0, 8.0, None) == -2
     for i in range(3):
