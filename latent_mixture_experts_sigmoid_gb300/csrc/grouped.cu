@@ -733,11 +733,11 @@ cudaError_t launch(const Maps& m, Params& p, long long units, cudaStream_t s) {
 // microseconds if every row has an expert of its own (the offsets are on the device).  That form:
 // its CTAs, then the weights at 4.4 TB/s.  Here: the launch and a unit's K blocks one after another,
 // or the weights at 6.2 TB/s.  Measured, stream / here, rows of different experts:
-//   forward 1024 x 2048:  1 row 5.2 / 12.2, 8 rows 9.4 / 12.5, 16 rows 18.6 / 16.3
-//   forward 2048 x 512:   1 row 3.3 / 7.2,  8 rows 6.7 / 7.6,  16 rows 13.0 / 10.3
-//   rows    1024 x 2048:  1 row 5.6 / 9.2,  4 rows 5.9 / 9.4,  8 rows 11.8 / 9.7
-//   rows    2048 x 512:   1 row 5.8 / 12.1, 16 rows 10.3 / 12.5, 32 rows 19.5 / 16.2
-//   forward 256 x 128:    1 row 2.1 / 5.0,  128 rows of 16 experts 4.1 / 5.1, 256 rows 5.8 / 5.2
+//   forward 1024 x 2048:  1 row 4.8 / 12.2, 8 rows 8.6 / 12.5, 16 rows 16.2 / 16.0
+//   forward 2048 x 512:   1 row 2.8 / 7.2,  8 rows 5.8 / 7.6,  16 rows 11.7 / 10.3
+//   rows    1024 x 2048:  1 row 5.3 / 9.2,  4 rows 5.6 / 9.4,  8 rows 10.8 / 9.7
+//   rows    2048 x 512:   1 row 5.6 / 12.1, 16 rows 10.1 / 12.5, 32 rows 19.2 / 16.2
+//   forward 256 x 128:    1 row 2.0 / 5.0,  128 rows of 16 experts 4.1 / 5.1, 256 rows 5.8 / 5.2
 bool streams(const GroupedLinear& g, bool backward) {
   const long long ctas = grouped_stream_ctas(g, backward);
   if (ctas > 4096) return false;

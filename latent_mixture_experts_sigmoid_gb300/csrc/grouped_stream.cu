@@ -11,8 +11,9 @@
 //   rows      B = W^T: a thread has 4 consecutive columns of the four weight rows 4t .. 4t + 3 of 16;
 //             column j of each thread's four makes MMA j (pairs of rows packed by byte permutes)
 // The warps' partial sums meet in shared memory and are added in order.
-// One row, 1024 x 2048: forward 5.2 us, rows 5.6; 2048 x 512: 3.3 and 5.8; 256 x 128: 2.1 and 2.3 (tiles of
-// 256: 12.2, 9.2, 7.2, 12.1, 5.0, 5.3); rows with 64 columns and eight parts of N a CTA: 7.8 us.
+// One row, 1024 x 2048: forward 4.8 us, rows 5.3; 2048 x 512: 2.8 and 5.6; 256 x 128: 2.0 and 2.3 (tiles of
+// 256: 12.2, 9.2, 7.2, 12.1, 5.0, 5.3); rows with 64 columns and eight parts of N a CTA: 7.8 us.  Rows of
+// many experts: 5.2 TB/s forward, 4 TB/s for the rows' gradient, whose pieces of a weight row are 64 bytes.
 #include "grouped.cuh"
 
 namespace lmoe {
@@ -33,9 +34,10 @@ __device__ __forceinline__ void mma_bf16(float (&c)[4], uint32_t a0, uint32_t a1
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
 
+// (a row's next 64-byte pieces come to L2 with the first: 64 rows of 64 experts, 1024 x 2048, 58 -> 51 us)
 __device__ __forceinline__ uint4 ld_weights(const uint16_t* p) {
   uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+  asm volatile("ld.global.L1::no_allocate.L2::256B.v4.u32 {%0,%1,%2,%3}, [%4];"
                : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p));
   return v;
 }
@@ -46,23 +48,27 @@ __device__ __forceinline__ uint2 ld_weights2(const uint16_t* p) {
   return v;
 }
 
-// The expert that owns row r and its rows; -1 if none does.  By all threads: one look at each pair
-// of offsets.
-__device__ __forceinline__ int owner(const GroupedLinear& p, int r, int2* rows, int* found) {
-  if (threadIdx.x == 0) *found = -1;
+// The expert that owns row r and its rows; -1 if none does.  By all threads, each with its run of the
+// offsets, asked for at once.  (At most 2^12 rows get here: a row number takes 16 bits.)
+template <int kThreads>
+__device__ __forceinline__ int owner(const GroupedLinear& p, int r, int2* rows, unsigned long long* found) {
+  constexpr int kPer = 1024 / kThreads;
+  if (threadIdx.x == 0) *found = 0;
+  const int R = (int)p.R, e0 = threadIdx.x * kPer;
+  int at[kPer + 1];
+#pragma unroll
+  for (int i = 0; i <= kPer; ++i) at[i] = __ldg(p.offsets + min(e0 + i, p.E));
   __syncthreads();
-  const int R = (int)p.R;
-  for (int e = threadIdx.x; e < p.E; e += (int)blockDim.x) {
-    const int a = min(max(__ldg(p.offsets + e), 0), R), b = min(max(__ldg(p.offsets + e + 1), a), R);
-    if (a <= r && r < b) atomicMax(found, e);   // (one, where the offsets ascend)
+#pragma unroll
+  for (int i = 0; i < kPer; ++i) {
+    const int a = min(max(at[i], 0), R), b = min(max(at[i + 1], a), R);
+    if (e0 + i < p.E && a <= r && r < b)         // (of one expert, where the offsets ascend)
+      atomicMax(found, (unsigned long long)(e0 + i + 1) << 32 | (unsigned)(a << 16 | b));
   }
   __syncthreads();
-  const int e = *found;
-  if (e >= 0) {
-    rows->x = min(max(__ldg(p.offsets + e), 0), R);
-    rows->y = min(max(__ldg(p.offsets + e + 1), rows->x), R);
-  }
-  return e;
+  const unsigned long long f = *found;
+  *rows = make_int2((int)(f >> 16 & 0xFFFF), (int)(f & 0xFFFF));
+  return (int)(f >> 32) - 1;
 }
 
 // grid: x strips of features or columns, y token rows; the CTAs of the rows that begin a tile of kTok
@@ -70,11 +76,11 @@ __device__ __forceinline__ int owner(const GroupedLinear& p, int r, int2* rows, 
 __global__ void __launch_bounds__(kForwardThreads)
 stream_forward_kernel(const GroupedLinear p) {
   __shared__ float part[kFeatSplit][kTok][kFeat];
-  __shared__ int found;
+  __shared__ unsigned long long found;
   pdl_trigger();
   pdl_wait();
   int2 rows;
-  const int r0 = blockIdx.y, e = owner(p, r0, &rows, &found);
+  const int r0 = blockIdx.y, e = owner<kForwardThreads>(p, r0, &rows, &found);
   if (e < 0 || (r0 - rows.x) % kTok) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int valid = min(kTok, rows.y - r0);
@@ -120,11 +126,11 @@ stream_forward_kernel(const GroupedLinear p) {
 __global__ void __launch_bounds__(kRowsThreads)
 stream_rows_kernel(const GroupedLinear p) {
   __shared__ __align__(16) float part[kColSplit][kTok][kCols + 4];    // (a quarter warp's stores meet no bank twice)
-  __shared__ int found;
+  __shared__ unsigned long long found;
   pdl_trigger();
   pdl_wait();
   int2 rows;
-  const int r0 = blockIdx.y, e = owner(p, r0, &rows, &found);
+  const int r0 = blockIdx.y, e = owner<kRowsThreads>(p, r0, &rows, &found);
   if (e < 0 || (r0 - rows.x) % kTok) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, g = lane >> 2, t = lane & 3;
   const int valid = min(kTok, rows.y - r0);
