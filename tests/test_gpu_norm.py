@@ -169,7 +169,7 @@ def test_specials_stay_in_their_row(H):
     assert bool(torch.isnan(out[5, H - 1])) and not out[5, :H - 1].any()
 
 
-BACK = [(1, 8), (2, 16), (9, 256), (40, 264), (100, 520), (1300, 1024), (3, 1032), (33, 2048), (700, 2056), (300, 4096), (1, 4104),
+BACK = [(63, 24), (64, 512), (64, 1024), (65, 1024), (17, 768), (1, 1024), (1, 8), (2, 16), (9, 256), (40, 264), (100, 520), (1300, 1024), (3, 1032), (33, 2048), (700, 2056), (300, 4096), (1, 4104),
         (650, 7168), (5, 8192), (40, 8200), (1300, 16384), (5000, 64), (6000, 1024), (70000, 16)]
 
 
