@@ -511,10 +511,16 @@ norm_join_kernel(const float* __restrict__ partial, int parts, int H, float* __r
   const int p0 = run * each, p1 = min(p0 + each, parts);
   float4 v = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
   if (col < H) {
-#pragma unroll 8
-    for (int p = p0; p < p1; ++p) {
-      const float4 a = *reinterpret_cast<const float4*>(partial + (long long)p * H + col);
-      v.x += a.x; v.y += a.y; v.z += a.z; v.w += a.w;
+    for (int p = p0; p < p1; p += 8) {           // eight loads at a time, also of a run that is shorter
+      float4 a[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i)
+        a[i] = p + i < p1 ? *reinterpret_cast<const float4*>(partial + (long long)(p + i) * H + col)
+                          : make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        v.x += a[i].x; v.y += a[i].y; v.z += a[i].z; v.w += a[i].w;
+      }
     }
   }
   sums[run][c] = v;
