@@ -225,8 +225,8 @@ def test_empty_batch():
     assert not dw.any()
 
 
-def test_captured_and_on_another_stream():
-    T, H = 200, 2048
+@pytest.mark.parametrize("T,H", [(200, 2048), (20, 512), (300, 96)])
+def test_captured_and_on_another_stream(T, H):
     h, res, w = batch(T, H, 1)
     dy = bf16(np.random.default_rng(0).standard_normal((T, H)))
     out, dh, dw = torch.empty_like(h), torch.empty_like(h), torch.empty(H, device="cuda")
