@@ -36,7 +36,8 @@
 //   forward       [4096, 7168] x [8192, 7168], one expert: 254 us, tensor pipe (1.89 PFLOP/s)
 //   forward       65536 rows over 128 experts, 1024 x 2048: 178 us with 512 rows each (1.55 PFLOP/s), 190
 //                 with uneven ones: a tile of fewer than 256 rows brings in more bytes per MMA cycle
-//   rows          65536 over 128 experts, 2048 x 512: 107 us (604 MB, 5.6 TB/s; 1.28 PFLOP/s): both
+//   rows          65536 over 128 experts, 2048 x 512: 107 us (604 MB, 5.6 TB/s; 1.28 PFLOP/s) where the tiles
+//                 are eight rounds of the 76 pairs, 117 to 118 where they are nine: both, and the rounds
 //   weights       65536 rows over 128 experts, 1024 x 2048: fp32 265 us, with addend 437 (2.55 GB,
 //                 5.8 TB/s), bf16 211: memory, and the latency of the rows against a ring of six stages
 //                 (with five: 303, 439, 227)
