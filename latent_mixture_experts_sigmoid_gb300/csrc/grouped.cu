@@ -450,6 +450,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             }
             ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kFull + s), ph, abort_flag, p.err, kErrMmaFull));
             if (!ok) break;
+            // (the zeros that both CTAs' warps 2 have written)
+            if (kMode == kWeights && depth - k < kBK) mbar_acquire_cluster(bar_at(kFull + s), ph);
             tc_fence_after();
             const uint64_t da = a0 + (uint64_t)s * (p.stage_bytes >> 4), db = b0 + (uint64_t)s * (p.stage_bytes >> 4);
             const uint32_t d = tmem_base + acc * kTile;
