@@ -15,15 +15,17 @@
 // experts' rows behind the last are not stored.  The major-ness is a bit of the MMA's operand
 // descriptors: nothing is transposed in memory.
 //
-// Where the token rows are the sum's index (weights), the last block of 64 reaches into the next
-// expert's rows.  Its bytes go to a barrier of the CTA's own first; a warp sets the rows behind the
-// last to zero and passes the block on.  (Both operands': 0 times another expert's NaN is NaN.)
+// Where the token rows are the sum's index (weights), an expert's last block of 64 may have fewer rows,
+// and those behind them, the next expert's, have to read as zeros.  (Both operands': 0 times another
+// expert's NaN is NaN.)  The copies fill them in: the tensor maps count a row twice, as j of 64 from row
+// i on, so that a box of 64 from j = -(64 - left) has its first 64 - left rows outside the map.  Zeros
+// that threads write (a barrier of the CTA's own, a warp that clears the rows and passes the block on)
+// have to be released to the other CTA's MMAs in cluster scope: fp32 331 us, bf16 271 at the case below.
 //
 //   warp 0      TMA producer of this CTA's halves; their bytes count on the leader's (rank 0's)
 //               barrier
 //   warp 1      allocates TMEM; in the leader one lane issues the MMAs of both CTAs, and its
 //               commits arrive in both
-//   warp 2      (weights) the zeros in the last blocks
 //   warps 4..11 read a finished tile from TMEM (warp w: the 32 M rows of lane quarter w % 4, half of
 //               the columns) and write it: token rows through shared memory in 256-byte pieces, gradients
 //               of weights through shared memory and bulk tensor stores, an addend added on the way
@@ -38,9 +40,9 @@
 //                 with uneven ones: a tile of fewer than 256 rows brings in more bytes per MMA cycle
 //   rows          65536 over 128 experts, 2048 x 512: 107 us (604 MB, 5.6 TB/s; 1.28 PFLOP/s) where the tiles
 //                 are eight rounds of the 76 pairs, 117 to 118 where they are nine: both, and the rounds
-//   weights       65536 rows over 128 experts, 1024 x 2048: fp32 265 us, with addend 437 (2.55 GB,
-//                 5.8 TB/s), bf16 211: memory, and the latency of the rows against a ring of six stages
-//                 (with five: 303, 439, 227)
+//   weights       65536 rows over 128 experts, 1024 x 2048: fp32 256 us, with addend 437 (2.55 GB,
+//                 5.8 TB/s), bf16 206: memory, and the latency of the rows against a ring of six stages
+//                 (one stage fewer: 16 % more in fp32, 8 % in bf16)
 // Taking tiles over from clusters that have not started (cluster launch control) was no faster than
 // tile u on pair u mod pairs, L2 prefetches of the next tile's rows or addend were slower.
 #include <cuda.h>
@@ -293,8 +295,8 @@ __device__ __forceinline__ void load_addend(const Params& p, const Tile& x, int 
 template <int kMode, int kOut>
 __global__ void __launch_bounds__(kThreads, 1)
 grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-               const __grid_constant__ CUtensorMap tmAp, const __grid_constant__ CUtensorMap tmBp,
-               const __grid_constant__ CUtensorMap tmO, const Params p) {
+               const __grid_constant__ CUtensorMap tmBp, const __grid_constant__ CUtensorMap tmO,
+               const Params p) {
   constexpr bool kAK = kMode == kForward, kBK_ = kMode != kWeights;   // K-major operands
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
@@ -302,7 +304,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   uint8_t* boxes = smem + (size_t)p.stages * p.stage_bytes;
   uint64_t* bars = reinterpret_cast<uint64_t*>(boxes + out_bytes(kMode));
   constexpr int kFull = 0, kEmpty = kMaxStages, kTfull = 2 * kMaxStages, kTempty = kTfull + kAcc,
-                kDone = kTempty + kAcc, kLast = kDone + 1, kBars = kLast + kMaxStages;
+                kDone = kTempty + kAcc, kBars = kDone + 1;
   uint32_t* tmem_holder = reinterpret_cast<uint32_t*>(bars + kBars);
   volatile int* abort_flag = reinterpret_cast<volatile int*>(tmem_holder + 1);
   int* warp_sum = reinterpret_cast<int*>(tmem_holder + 2);
@@ -315,9 +317,8 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
   pdl_trigger();
   if (threadIdx.x == 0) {
     for (int i = 0; i < p.stages; ++i) {
-      mbar_init(bar_at(kFull + i), kMode == kWeights ? 2 : 1);   // (a last block: both CTAs' warps 2)
+      mbar_init(bar_at(kFull + i), 1);
       mbar_init(bar_at(kEmpty + i), 1);
-      mbar_init(bar_at(kLast + i), 1);
     }
     for (int i = 0; i < kAcc; ++i) {
       mbar_init(bar_at(kTfull + i), 1);
@@ -376,44 +377,31 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           if (!ok) break;
           const uint32_t at = smem_u32(smem) + (uint32_t)s * p.stage_bytes, bt = at + kABytes;
           const int k = kb * kBK;
-          const int left = x.rows - k;                 // (weights)
+          const int skip = min(x.rows - k - kBK, 0);   // (weights: minus the zero rows ahead of an expert's last)
           if (elect_one()) {
-            if (kMode == kWeights && left < kBK) {
-              const int n16 = (left + 15) >> 4;
-              const uint32_t bar = bar_at(kLast + s);
-              mbar_arrive_expect_tx(bar, (uint32_t)((2 + nchunk) * n16) * 2048u);
-              for (int c = 0; c < 2; ++c)
-                for (int i = 0; i < n16; ++i)
-                  tma_load_2d(&tmAp, at + c * kChunk + i * 2048u, bar, m + c * 64, x.row0 + k + i * 16);
-              for (int c = 0; c < nchunk; ++c)
-                for (int i = 0; i < n16; ++i)
-                  tma_load_2d(&tmBp, bt + c * kChunk + i * 2048u, bar, n0 + c * 64, x.row0 + k + i * 16);
+            const uint32_t bar = cluster_addr(bar_at(kFull + s), 0);
+            if (rank == 0) {
+              const uint32_t bytes = kMode == kWeights ? (uint32_t)(2 + nchunk) * kChunk
+                                                       : kABytes + (uint32_t)(nbox * brows) * 128u;
+              mbar_arrive_expect_tx(bar_at(kFull + s), 2 * bytes);
+            }
+            if constexpr (kMode == kForward) {
+              tma_load_pair_3d(&tmA, at, bar, k, m, x.group);
+            } else if constexpr (kMode == kRows) {
+              tma_load_pair_3d(&tmA, at, bar, m, k, x.group);
+              tma_load_pair_3d(&tmA, at + kChunk, bar, m + 64, k, x.group);
             } else {
-              const uint32_t bar = cluster_addr(bar_at(kFull + s), 0);
-              if (rank == 0) {
-                const uint32_t bytes = kMode == kWeights ? (uint32_t)(2 + nchunk) * kChunk
-                                                         : kABytes + (uint32_t)(nbox * brows) * 128u;
-                if constexpr (kMode == kWeights) mbar_arrive(bar_at(kFull + s));
-                mbar_arrive_expect_tx(bar_at(kFull + s), 2 * bytes);
-              }
-              if constexpr (kMode == kForward) {
-                tma_load_pair_3d(&tmA, at, bar, k, m, x.group);
-              } else if constexpr (kMode == kRows) {
-                tma_load_pair_3d(&tmA, at, bar, m, k, x.group);
-                tma_load_pair_3d(&tmA, at + kChunk, bar, m + 64, k, x.group);
-              } else {
-                tma_load_pair(&tmA, at, bar, m, x.row0 + k);
-                tma_load_pair(&tmA, at + kChunk, bar, m + 64, x.row0 + k);
-              }
-              if constexpr (kMode == kWeights) {
-                tma_load_pair(&tmB, bt, bar, n0, x.row0 + k);
-                if (nchunk > 1) tma_load_pair(&tmB, bt + kChunk, bar, n0 + 64, x.row0 + k);
-              } else if (whole) {
-                tma_load_pair(&tmB, bt, bar, k, tok);
-              } else {
-                for (int i = 0; i < nbox; ++i)
-                  tma_load_pair(&tmBp, bt + (uint32_t)(i * brows) * 128u, bar, k, tok + i * brows);
-              }
+              tma_load_pair_3d(&tmA, at, bar, m, skip, x.row0 + k);
+              tma_load_pair_3d(&tmA, at + kChunk, bar, m + 64, skip, x.row0 + k);
+            }
+            if constexpr (kMode == kWeights) {
+              tma_load_pair_3d(&tmB, bt, bar, n0, skip, x.row0 + k);
+              if (nchunk > 1) tma_load_pair_3d(&tmB, bt + kChunk, bar, n0 + 64, skip, x.row0 + k);
+            } else if (whole) {
+              tma_load_pair(&tmB, bt, bar, k, tok);
+            } else {
+              for (int i = 0; i < nbox; ++i)
+                tma_load_pair(&tmBp, bt + (uint32_t)(i * brows) * 128u, bar, k, tok + i * brows);
             }
           }
           __syncwarp();
@@ -450,18 +438,17 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             }
             ok = __all_sync(0xFFFFFFFFu, wait_phase(bar_at(kFull + s), ph, abort_flag, p.err, kErrMmaFull));
             if (!ok) break;
-            // (the zeros that both CTAs' warps 2 have written)
-            if (kMode == kWeights && depth - k < kBK) mbar_acquire_cluster(bar_at(kFull + s), ph);
             tc_fence_after();
             const uint64_t da = a0 + (uint64_t)s * (p.stage_bytes >> 4), db = b0 + (uint64_t)s * (p.stage_bytes >> 4);
             const uint32_t d = tmem_base + acc * kTile;
             const bool last = k + kBK >= depth || (kMode == kWeights && (k + kBK) % kFlush == 0);
+            // (weights: not the groups of zeros in front; the others' blocks are whole or end in zeros)
+            const int j0 = kMode == kWeights ? max(kBK - (depth - k), 0) >> 4 : 0;
             if (elect_one()) {
 #pragma unroll
               for (int j = 0; j < kBK / 16; ++j)
-                // (weights: not past the zeros; the others' blocks are whole or filled up with zeros)
-                if (kMode != kWeights || k + 16 * j < depth)
-                  mma_pair(d, da + j * kStep<kAK>, db + j * kStep<kBK_>, id, j ? 1u : (uint32_t)!fresh);
+                if (kMode != kWeights || j >= j0)
+                  mma_pair(d, da + j * kStep<kAK>, db + j * kStep<kBK_>, id, j > j0 ? 1u : (uint32_t)!fresh);
               commit_both(bar_at(kEmpty + s));
               if (last) commit_both(bar_at(kTfull + (int)acc));
             }
@@ -479,30 +466,6 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
         __syncwarp();
         volatile int never = 0;
         wait_phase(bar_at(kDone), 0u, &never, p.err, kErrDone);
-      }
-    } else if (warp == 2) {
-      if constexpr (kMode == kWeights) {
-        // ---------------- zeros behind an expert's last row ----------------
-        uint32_t it = 0, lph = 0;                      // lph: a stage's phase of kLast, a bit each
-        for (int u = u0; u < U; u += ustep) {
-          const Tile x = tile_of<kMode>(p, groups, u);
-          it += (uint32_t)(x.rows + kBK - 1) / kBK;
-          const int left = x.rows & (kBK - 1);
-          if (left == 0) continue;
-          const int s = (int)((it - 1) % (uint32_t)p.stages);
-          if (!__all_sync(0xFFFFFFFFu, wait_phase(bar_at(kLast + s), (lph >> s) & 1u, abort_flag, p.err,
-                                                  kErrProducer)))
-            break;
-          lph ^= 1u << s;
-          const int z = (-left & 15) * 8;              // 16-byte pieces of the rows up to the next 16
-          uint8_t* at = smem + (size_t)s * p.stage_bytes + left * 128;
-          for (int c = 0; c < 2 + (x.n >> 7); ++c)     // 64 columns each
-            for (int i = lane; i < z; i += 32)
-              *reinterpret_cast<uint4*>(at + c * kChunk + i * 16) = make_uint4(0, 0, 0, 0);
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive_cluster_data(cluster_addr(bar_at(kFull + s), 0));
-        }
       }
     }
   } else {
@@ -655,15 +618,15 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   const cuuint32_t*, CUtensorMapInterleave, CUtensorMapSwizzle,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// [groups, rows, cols] in boxes of box_rows rows of 128 bytes, 128-byte swizzle; elements outside
-// read as zeros and are not written
+// [groups, rows, cols], or (groups = 0) [rows, cols], in boxes of box_rows rows of 128 bytes, 128-byte
+// swizzle; elements outside read as zeros and are not written.
 bool make_map(CUtensorMap* m, const void* base, bool fp32, long long groups, long long rows, int cols,
-              int box_rows) {
+              int box_rows, bool runs = false) {
   const EncodeTiledFn enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
   if (!enc) return false;
   const cuuint64_t size = fp32 ? 4 : 2;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)groups};
-  cuuint64_t strides[2] = {(cuuint64_t)cols * size, (cuuint64_t)cols * size * (cuuint64_t)rows};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * size, (cuuint64_t)cols * size * (cuuint64_t)(runs ? 1 : rows)};
   cuuint32_t box[3] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
@@ -672,12 +635,19 @@ bool make_map(CUtensorMap* m, const void* base, bool fp32, long long groups, lon
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// [rows, cols] as runs of kBK rows: row j of the run from row i is row i + j (the two strides are one).  j
+// < 0 and j >= kBK read as zeros.  (A run that goes past the last row is in the map and outside the
+// memory: boxes end with an expert's last row.)
+bool make_runs(CUtensorMap* m, const void* base, long long rows, int cols) {
+  return make_map(m, base, false, rows, kBK, cols, kBK, true);
+}
+
 constexpr size_t kMaxSmem = 227 * 1024;
 
 // shared memory of a launch but for its stages
 constexpr size_t other_smem(int mode, int E) {
   return 1024 + out_bytes(mode) +
-         (3 * kMaxStages + 2 * kAcc + 1) * 8 + 8 + (kThreads / 32) * 4 +
+         (2 * kMaxStages + 2 * kAcc + 1) * 8 + 8 + (kThreads / 32) * 4 +
          (mode == kWeights ? 0 : (size_t)(3 * E + 1) * 4) + 16;
 }
 
@@ -715,7 +685,7 @@ int pairs_resident() {
 }
 
 struct Maps {
-  CUtensorMap a, b, ap, bp, o;
+  CUtensorMap a, b, bp, o;
 };
 
 template <int kMode, int kOut>
@@ -728,8 +698,8 @@ cudaError_t launch(const Maps& m, Params& p, long long units, cudaStream_t s) {
   p.stages = (int)((kMaxSmem - other) / p.stage_bytes);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   return launch_k_cluster(grouped_kernel<kMode, kOut>, dim3(2 * (unsigned)(units < pairs ? units : pairs)),
-                          dim3(kThreads), other + (size_t)p.stages * p.stage_bytes, s, 2, m.a, m.b, m.ap,
-                          m.bp, m.o, p);
+                          dim3(kThreads), other + (size_t)p.stages * p.stage_bytes, s, 2, m.a, m.b, m.bp,
+                          m.o, p);
 }
 
 // Whether few rows stream through registers (grouped_stream.cu), by what both forms take in
@@ -773,7 +743,6 @@ cudaError_t launch_grouped_linear(const GroupedLinear& g, bool backward, cudaStr
       !make_map(&m.b, g.rows_in, false, 0, g.R, p.depth, p.nt / 2) ||
       !make_map(&m.bp, g.rows_in, false, 0, g.R, p.depth, kPartBox))
     return cudaErrorInvalidValue;
-  m.ap = m.a;
   m.o = m.a;
   // token tiles: one a started nt rows and expert at most
   const long long units = (g.R / p.nt + (g.R < g.E ? g.R : g.E)) * p.mtiles;
@@ -793,10 +762,10 @@ cudaError_t launch_grouped_weight_grad(const GroupedWeightGrad& g, cudaStream_t 
   p.add = g.add;
   Maps m;
   const bool fp32 = g.dw != nullptr;
-  if (!make_map(&m.a, g.dy, false, 0, g.R, g.N, kBK) || !make_map(&m.ap, g.dy, false, 0, g.R, g.N, 16) ||
-      !make_map(&m.b, g.x, false, 0, g.R, g.K, kBK) || !make_map(&m.bp, g.x, false, 0, g.R, g.K, 16) ||
+  if (!make_runs(&m.a, g.dy, g.R, g.N) || !make_runs(&m.b, g.x, g.R, g.K) ||
       !make_map(&m.o, fp32 ? (const void*)g.dw : g.dw_bf16, fp32, g.E, g.N, g.K, 32))
     return cudaErrorInvalidValue;
+  m.bp = m.b;
   const long long units = (long long)p.E * p.mtiles * p.ntiles;
   if (!fp32) return launch<kWeights, 1>(m, p, units, s);
   return p.add ? launch<kWeights, 2>(m, p, units, s) : launch<kWeights, 0>(m, p, units, s);

@@ -195,21 +195,6 @@ __device__ __forceinline__ void tma_load_pair_3d(const CUtensorMap* map, uint32_
       : "memory");
 }
 
-// The same where this CTA's threads have written shared memory that the other CTA's MMAs read, behind
-// the writers' fence_proxy_async_smem() and a barrier among them: the release has cluster scope (the
-// default's is the CTA), and the waiting thread acquires with mbar_acquire_cluster.
-__device__ __forceinline__ void mbar_arrive_cluster_data(uint32_t cluster_bar) {
-  asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(cluster_bar) : "memory");
-}
-// behind a wait that has seen the phase's end
-__device__ __forceinline__ void mbar_acquire_cluster(uint32_t bar, uint32_t parity) {
-  asm volatile(
-      "{\n\t.reg .pred p;\n\t"
-      "mbarrier.test_wait.parity.acquire.cluster.shared::cta.b64 p, [%0], %1;\n\t}" ::"r"(bar),
-      "r"(parity)
-      : "memory");
-}
-
 __device__ __forceinline__ void tma_store_3d(const CUtensorMap* map, uint32_t src, int c0, int c1, int c2) {
   asm volatile(
       "cp.async.bulk.tensor.3d.global.shared::cta.bulk_group [%0, {%2, %3, %4}], [%1];" ::"l"(

@@ -21,15 +21,15 @@ def test_arrivals_in_another_cta_name_their_scope():
         for m in re.finditer(r'"(mbarrier\.arrive[^ "]*\.shared::cluster[^ "]*)', open(path).read()):
             found += 1
             assert ".cluster.shared::cluster" in m[1], (path, m[1])
-    assert found >= 2
+    assert found >= 1
 
 
-def test_data_handed_to_the_other_cta_is_released_and_acquired():
-    # (weights' gradient: the zeros behind an expert's last row are read by the leader's MMAs)
-    ptx, grouped = source("tc_ptx.cuh"), source("grouped.cu")
-    body = re.search(r"void mbar_arrive_cluster_data\(.*?\n}", ptx, re.S)[0]
-    assert "mbarrier.arrive.release.cluster.shared::cluster" in body
-    assert "parity.acquire.cluster" in re.search(r"void mbar_acquire_cluster\(.*?\n}", ptx, re.S)[0]
-    mma = grouped[grouped.index("MMA issuer of the pair"):grouped.index("warp == 2")]
-    # behind the wait for the block, ahead of its MMAs
-    assert mma.index("kFull + s), ph, abort_flag") < mma.index("mbar_acquire_cluster(") < mma.index("mma_pair(")
+def test_no_thread_writes_what_the_other_cta_s_tensor_cores_read():
+    # (grouped products: every operand comes by TMA, whose bytes count on the leader's barrier; a CTA's
+    # threads write their epilogue's boxes alone.  Otherwise a release and an acquire of cluster scope
+    # have to stand between the writes and the MMAs.)
+    grouped = source("grouped.cu")
+    roles = grouped[grouped.index("TMA producer ---"):grouped.index("epilogue ---")]
+    assert "mma_pair(" in roles and "reinterpret_cast<uint4*>" not in roles
+    if "mbar_arrive_cluster_data" in grouped:
+        assert "mbarrier.arrive.release.cluster" in source("tc_ptx.cuh") and "acquire.cluster" in source("tc_ptx.cuh")
