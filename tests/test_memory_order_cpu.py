@@ -33,3 +33,17 @@ def test_no_thread_writes_what_the_other_cta_s_tensor_cores_read():
     assert "mma_pair(" in roles and "reinterpret_cast<uint4*>" not in roles
     if "mbar_arrive_cluster_data" in grouped:
         assert "mbarrier.arrive.release.cluster" in source("tc_ptx.cuh") and "acquire.cluster" in source("tc_ptx.cuh")
+
+
+def test_in_place_operands_are_not_read_as_constant():
+    # ld.global.nc and __restrict__ say that nobody writes the memory while the kernel runs; SituGLU's
+    # gradient may be written over its input, the norm's outputs over its inputs
+    situ = source("situ.cu")
+    kernel = re.search(r"situ_backward_kernel\(.*?\n}", situ, re.S)[0]
+    assert re.match(r"situ_backward_kernel\(const uint16_t\* in,", kernel), kernel[:80]
+    loads = re.findall(r"(\w+)\(reinterpret_cast<const uint4\*>\(in \+", kernel)
+    assert len(loads) == 2
+    for name in loads:
+        assert ".nc" not in re.search(r"uint4 " + name + r"\(.*?\n}", situ, re.S)[0], name
+    norm = source("norm.cu")
+    assert ".nc" not in norm and "__ldg" not in norm
