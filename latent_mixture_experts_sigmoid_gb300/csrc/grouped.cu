@@ -41,7 +41,7 @@
 //   rows          65536 over 128 experts, 2048 x 512: 107 us (604 MB, 5.6 TB/s; 1.28 PFLOP/s) where the tiles
 //                 are eight rounds of the 76 pairs, 117 to 118 where they are nine: both, and the rounds
 //   weights       65536 rows over 128 experts, 1024 x 2048: fp32 256 us, with addend 437 (2.55 GB,
-//                 5.8 TB/s), bf16 206: memory, and the latency of the rows against a ring of six stages
+//                 5.8 TB/s), bf16 204: memory, and the latency of the rows against a ring of six stages
 //                 (one stage fewer: 16 % more in fp32, 8 % in bf16)
 // Taking tiles over from clusters that have not started (cluster launch control) was no faster than
 // tile u on pair u mod pairs, L2 prefetches of the next tile's rows or addend were slower.
@@ -67,11 +67,15 @@ constexpr int kBK = 64;                             // a K block: 128 bytes
 constexpr uint32_t kChunk = kBK * 128;              // 64 M or N columns of a block, K rows of 128 bytes
 constexpr uint32_t kABytes = kHalf * kBK * 2;
 constexpr int kAcc = 2;                             // TMEM accumulators of 256 columns
-// weights: rows that the tensor cores add up before registers take over.  Their additions truncate:
-// a sum of n rows comes out low by about n 2^-30 of itself (65536 rows: 8e-5, of numbers of one sign
-// 4e-4).  512 rows are 5e-7 off, the registers' additions round, and a read of TMEM every 4096
-// cycles of MMAs hides behind them (256 rows: the same but with an addend, 473 us for 438).
-constexpr int kFlush = 512;
+// weights: rows that the tensor cores add up before registers take over, whose additions round.  The
+// tensor cores' truncate: of a step of 16 terms each is cut to 2^-25 of the largest magnitude's power of
+// two, their sum to 2^-23 (seen with one term of 1 and others below it).  256 rows are off by 2.3e-7 of
+// their norm (normal ones; 3.1e-7, all of them low, for positive ones), 512 rows by 4.7e-7 (7.1e-7), any
+// number of rows by the same.  A read of TMEM every 2048 cycles of MMAs hides behind them but for the
+// registers that the addend takes: 65536 rows, 128 experts, 1024 x 2048, 256 / 512 rows: fp32 256 / 256 us,
+// bf16 204 / 204, with addend 467 / 437.
+template <int kOut>
+constexpr int kFlushRows = kOut == 2 ? 512 : 256;
 constexpr int kMaxStages = 8;
 constexpr int kPartBox = 32;                        // token rows of a partial box
 constexpr int kMaxGroups = 1024;
@@ -298,6 +302,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
                const __grid_constant__ CUtensorMap tmBp, const __grid_constant__ CUtensorMap tmO,
                const Params p) {
   constexpr bool kAK = kMode == kForward, kBK_ = kMode != kWeights;   // K-major operands
+  constexpr int kFlush = kFlushRows<kOut>;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) &
                                              ~uintptr_t(1023));

@@ -46,3 +46,29 @@ def test_weight_gradients_beside_experts_of_nan(form):
             lm.lmoe_grouped_linear_backward_w(dn, xn, off, got, add=add)
             assert torch.equal(got[1 - parity::2], want[1 - parity::2])
             assert bool(torch.isnan(got[parity::2]).all())
+
+
+@pytest.mark.parametrize("rows", [200, 512, 1100])
+@pytest.mark.parametrize("form", ["fp32", "bf16"])
+def test_small_terms_behind_a_large_one(rows, form):
+    # A first term of 1 and terms p, which the tensor cores cut: a step of 16 loses up to
+    # 16 * 2^-25 and 2^-23 in its own sum (5 units of 2^-23 at the most) of the power of two below
+    # the largest magnitude, here 1.  256 rows are summed so, and joined by additions that round: one
+    # block loses what 16 steps do, the others nothing, as their terms are alike and less than 2^-16
+    # of the sum.  (512 rows at once lose 127 units with p = 0.99 * 2^-25.)
+    p = 0.9921875 * 2.0 ** torch.arange(-22, -30, -1, dtype=torch.float64)
+    x = torch.ones((rows, 8), dtype=torch.bfloat16, device="cuda")
+    dy = p.repeat(rows, 1)
+    dy[0] = 1.0
+    if form == "bf16":
+        dy = dy - (dy == 1.0) * 1.0               # (the large term's own bits would hide them: p alone)
+    dy = dy.to(torch.bfloat16).to("cuda")
+    dw = torch.empty((1, 8, 8), dtype=torch.float32 if form == "fp32" else torch.bfloat16, device="cuda")
+    lm.lmoe_grouped_linear_backward_w(dy, x, offsets([rows]), dw)
+    ref = (dy.double().T @ x.double()).cpu().numpy()[None]
+    joins = 2 + rows / 256
+    if form == "fp32":
+        bound = (16 * 5 + joins / 2) * 2.0 ** -23 * np.ones_like(ref)
+    else:
+        bound = (BF16 + (16 * 5 + joins / 2) * 2.0 ** -23) * np.abs(ref)
+    assert np.all(np.abs(f64(dw) - ref) <= bound), (np.abs(f64(dw) - ref) / bound).max()
