@@ -532,8 +532,8 @@ int lmoe_rms_norm(const lmoe_bf16* x, const lmoe_bf16* residual, const lmoe_bf16
 /* (not computed; no workspace is needed then).  grad_h may be grad_out, h or  */
 /* grad_residual.  Sums are fp32 in a fixed order: repeated calls give the     */
 /* same bits.  Limits of lmoe_rms_norm; H % 8 == 0.  T == 0: grad_norm_w       */
-/* becomes 0 where it is memory of the current device.  The sum of             */
-/* grad_out * norm_w * h over a row is taken in fp32 and must be in its range.  */
+/* becomes 0.  The sum of grad_out * norm_w * h over a row is taken in fp32     */
+/* and must be in its range.                                                  */
 /* The workspace (256-byte aligned, not shared with a call that may overlap)   */
 /* does not fall as T grows.                                                  */
 size_t lmoe_rms_norm_backward_workspace_bytes(int T, int H);

@@ -1425,8 +1425,10 @@ int lmoe_rms_norm_backward(const lmoe_bf16* grad_out, const lmoe_bf16* h, const 
   if (v != LMOE_OK) return v;
   if (T == 0) {
     // an empty batch (a rank without tokens): 0, not what an earlier call left there
-    if (grad_norm_w && on_current_device({grad_norm_w}))
-      LMOE_TRY(cudaMemsetAsync(grad_norm_w, 0, (size_t)H * sizeof(float), (cudaStream_t)stream));
+    if (!grad_norm_w) return LMOE_OK;
+    if (!aligned16(grad_norm_w)) return LMOE_ERR_ALIGN;
+    if (!on_current_device({grad_norm_w})) return LMOE_ERR_DEVICE;
+    LMOE_TRY(cudaMemsetAsync(grad_norm_w, 0, (size_t)H * sizeof(float), (cudaStream_t)stream));
     return LMOE_OK;
   }
   if (!grad_out || !h || !grad_h) return LMOE_ERR_NULL;
