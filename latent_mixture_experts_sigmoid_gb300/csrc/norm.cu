@@ -238,8 +238,9 @@ __device__ __forceinline__ void sums_of(float (&sum)[2], const uint4 (&hv)[kVec]
   sum[1] = f2_lo(gh) + f2_hi(gh);
 }
 
-// n = (h s) r (not h (s r): s r may leave the range where the squares did);
-// grad_h = grad_residual + s r (g - n k), k = mean(g n)
+// n = (h s) r; grad_h = grad_residual + s (r (g - n k)), k = mean(g n).  (Never s r, which may leave the
+// range where the squares did: of rows below 2^-128 it is infinite, and 0 times it NaN.  The multiplication
+// more shows in no time.)
 struct RowFactors {
   float s, r, k;
 };
@@ -273,7 +274,9 @@ __device__ __forceinline__ uint4 grad_of(const uint4& hv, const uint4& dv, const
     if (f.s != 1.0f) h[e] = f2_mul(h[e], f2_splat(f.s));
     const f32x2 n = f2_mul(h[e], f2_splat(f.r));
     acc[e] = f2_fma(d[e], n, acc[e]);
-    q[e] = f2_fma(f2_splat(f.s * f.r), f2_fma(n, f2_splat(-f.k), f2_mul(d[e], w[e])), q[e]);
+    f32x2 v = f2_fma(n, f2_splat(-f.k), f2_mul(d[e], w[e]));
+    v = f2_mul(v, f2_splat(f.r));
+    q[e] = f2_fma(f2_splat(f.s), v, q[e]);
   }
   return narrow(q);
 }
