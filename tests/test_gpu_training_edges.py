@@ -4,6 +4,7 @@ import pytest
 import torch
 
 from oracle import training_oracle as O
+from tests.test_gpu_situ_backward import check
 
 pytestmark = pytest.mark.gpu
 lm = pytest.importorskip("latent_mixture_experts_sigmoid_gb300")
@@ -60,3 +61,15 @@ def test_norm_gradient_far_from_one(T, H):
         # (bounds of test_gpu_norm; bf16 below 2^-126 rounds by 2^-134)
         bound = BF16 * np.abs(ref) * (1 + 2 ** -7) + 160 * 2.0 ** -24 * mag + 2.0 ** -134
         assert np.all(np.abs(f64(dh) - ref) <= bound), (of_h, of_dy)
+
+
+@pytest.mark.parametrize("beta", [4.0, 1.0])
+def test_situ_gradient_of_large_products(beta):
+    # without a bound on up, grad_out * up may leave fp32 where the gate's small derivative brings the
+    # result back: of a saturated gate, and NaN beside a derivative of 0
+    g = np.random.default_rng(2)
+    gate = np.array([40.0, -40.0, 20.0, -60.0, 300.0, 1000.0, -300.0, 6.0])
+    up, dy = 2.0 ** np.array([100.0, 100, 110, 120, 127, 127, 127, 20]), 2.0 ** np.array([30.0, 30, 20, 10, 3, 3, 3, 100])
+    x = np.concatenate([np.tile(gate, (4, 8)), np.tile(up, (4, 8)) * np.sign(g.standard_normal((4, 64)))], 1)
+    dx = check(bf16(x), bf16(np.tile(dy, (4, 8))), beta, 0.0)
+    assert bool(torch.isfinite(dx).all())
