@@ -764,6 +764,13 @@ def moe_router_backward(router_logits, topk_ids, grad_logits, grad_topk_weights=
 # --- residual + RMSNorm ------------------------------------------------------------
 
 
+_INT_MAX = 2 ** 31 - 1
+
+
+def _refuse_sizes(**sizes):
+    raise ValueError(f"sizes past the ABI's 32 bits: {sizes}")    # (ctypes would cut them)
+
+
 def lmoe_rms_norm(x, norm_w, rms_eps: float, out=None, codes=None, scales=None, residual=None,
                   residual_out=None, stream=None, T: int | None = None, H: int | None = None):
     """RMSNorm of h = x (+ residual) [T, H]: out bf16, e4m3 codes [T, H] with scales
@@ -773,6 +780,8 @@ def lmoe_rms_norm(x, norm_w, rms_eps: float, out=None, codes=None, scales=None, 
         H = x.shape[-1]
         T = x.numel() // H
     T, H = int(T), int(H)
+    if T > _INT_MAX or H > _INT_MAX:
+        _refuse_sizes(T=T, H=H)
     here = _current_device()
     st = load_library().lmoe_rms_norm(
         _dev(x, "x", _BF16, T * H, here), _dev(residual, "residual", _BF16, T * H, here),
@@ -784,7 +793,10 @@ def lmoe_rms_norm(x, norm_w, rms_eps: float, out=None, codes=None, scales=None, 
 
 
 def lmoe_rms_norm_backward_workspace_bytes(T: int, H: int) -> int:
-    return int(load_library().lmoe_rms_norm_backward_workspace_bytes(int(T), int(H)))
+    T, H = int(T), int(H)
+    if T > _INT_MAX or H > _INT_MAX:
+        _refuse_sizes(T=T, H=H)
+    return int(load_library().lmoe_rms_norm_backward_workspace_bytes(T, H))
 
 
 def lmoe_rms_norm_backward(grad_out, h, norm_w, rms_eps: float, grad_h, grad_norm_w=None,
@@ -796,6 +808,8 @@ def lmoe_rms_norm_backward(grad_out, h, norm_w, rms_eps: float, grad_h, grad_nor
         H = h.shape[-1]
         T = h.numel() // H
     T, H = int(T), int(H)
+    if T > _INT_MAX or H > _INT_MAX:
+        _refuse_sizes(T=T, H=H)
     wsp, wsn = _workspace(workspace, None)
     here = _current_device()
     st = load_library().lmoe_rms_norm_backward(
@@ -813,6 +827,8 @@ def situ_and_mul_backward(inp, grad_out, grad_in, beta: float, linear_beta: floa
         d = inp.shape[-1] // 2
         N = inp.numel() // (2 * d)
     N, d = int(N), int(d)
+    if d > _INT_MAX:
+        _refuse_sizes(d=d)
     here = _current_device()
     st = load_library().situ_and_mul_backward(
         _dev(inp, "input", _BF16, N * 2 * d, here), _dev(grad_out, "grad_out", _BF16, N * d, here),
@@ -828,7 +844,10 @@ def _grouped_shape(rows, weights, width: int, shape):
     """(rows, E, N, K) of a [rows, N or K] matrix and [E, N, K] weights; width: the index of
     the rows' width in [E, N, K]."""
     if shape is not None:
-        return tuple(int(v) for v in shape)
+        R, E, N, K = (int(v) for v in shape)
+        if E > _INT_MAX or N > _INT_MAX or K > _INT_MAX:
+            _refuse_sizes(E=E, N=N, K=K)
+        return R, E, N, K
     R, wide = rows.shape
     E, N, K = weights.shape
     if wide != weights.shape[width]:
