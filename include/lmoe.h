@@ -629,10 +629,11 @@ int lmoe_linear(const lmoe_bf16* x, const lmoe_bf16* w, const lmoe_bf16* add, lm
 const char* lmoe_status_string(int status);
 
 /* Reads (and with clear != 0 resets) the device error word of the current    */
-/* device: 0 = nothing went wrong; 1-6 = a bounded wait of a kernel gave up   */
-/* (of the tensor-core products, of a ring of copies); 7 = latent_moe_forward_routed met an expert id outside      */
-/* [0, E).  The first code written stays until cleared.  Synchronises the    */
-/* device.                                                                    */
+/* device: 0 = nothing went wrong; 1-6 = a bounded wait of a tensor-core      */
+/* product gave up; 7 = latent_moe_forward_routed met an expert id outside    */
+/* [0, E); 8 = a wait of the MXFP4 product for few tokens gave up; 9 =        */
+/* lmoe_rms_norm_backward's wait for a row gave up.  The first code written   */
+/* stays until cleared.  Synchronises the device.                             */
 /* Returns the word, or LMOE_ERR_CUDA if it cannot be read.                   */
 int lmoe_device_error(int clear);
 

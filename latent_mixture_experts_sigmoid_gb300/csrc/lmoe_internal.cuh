@@ -14,9 +14,10 @@ namespace lmoe {
 constexpr int kNumSmsDefault = 152;
 
 // Codes of the device error word (the first one written stays): 1-6 are the
-// tensor-core GEMM's bounded waits; kErrExpertId is an expert id outside
-// [0, E) handed to the pre-routed forward.
+// tensor-core products' bounded waits; kErrExpertId is an expert id outside
+// [0, E) handed to the pre-routed forward; 8 is the MXFP4 product's wait.
 constexpr int kErrExpertId = 7;
+constexpr int kErrNormRow = 9;   // a row of the norm's gradient did not arrive in its ring
 
 // Device address of the error word of the current device.
 int* device_error_word();

@@ -90,7 +90,6 @@ __device__ __forceinline__ float range_scale(float sum, float H, float eps) {
 }
 
 constexpr int kMaxRing = 16;                     // rows of the gradient's ring
-constexpr int kErrNormRow = 4;                   // device error word: a row did not arrive
 
 // A bounded wait, about two seconds.
 __device__ __forceinline__ bool wait_row(uint32_t bar, uint32_t parity) {
