@@ -535,7 +535,7 @@ norm_join_kernel(const float* __restrict__ partial, int parts, int H, float* __r
   }
 }
 
-int round32(int n) { return (n + 31) / 32 * 32; }
+constexpr int round32(int n) { return (n + 31) / 32 * 32; }
 
 constexpr int kShortThreads = 256;               // a CTA of several short rows
 // lanes that a short row takes, vectors a lane (of H <= 512; the forward's up to 1024)
@@ -549,9 +549,42 @@ ShortRow short_row(int nvec) {
 }
 constexpr int kForwardShort = 128, kBackwardShort = 64;      // vectors
 
-// How the gradient's kernel is launched.  Long rows: as many CTAs of 512 threads together as the
-// registers (128 a thread) leave room for, if their rings have three rows each; together the rings
-// take up to 216 KB.
+// Long rows of the gradient: as many CTAs of 512 threads together as the registers (128 a thread) leave
+// room for, if their rings have three rows each.  The rings take up to 216 KB of an SM's 228, less where
+// many CTAs have 2.3 KB each beside them (their sums and barriers, and 1 KB that the system keeps): the grid
+// is the CTAs that fit, each with an equal share of the rows, and one that did not would run alone
+// behind them ([16384, 768] with grad_residual 26.6 us, 39.6 with seven of eight CTAs resident).
+constexpr int kSmSmem = 228 * 1024, kRingSmem = 216 * 1024, kRingBeside = 1280 + 1024;
+struct RingPlan {
+  int vec, threads, per_sm, stages;
+  size_t smem;
+};
+constexpr RingPlan ring_plan(int H, bool residual) {
+  RingPlan r{};
+  const int nvec = H / 8, slot = H * 2 * (residual ? 3 : 2);
+  r.vec = nvec <= 1024 ? 2 : 4;
+  r.threads = round32((nvec + r.vec - 1) / r.vec);
+  int most = 0;
+  for (r.per_sm = 512 / r.threads;; --r.per_sm) {
+    most = kRingSmem / r.per_sm;
+    if (most > kSmSmem / r.per_sm - kRingBeside) most = kSmSmem / r.per_sm - kRingBeside;
+    if (r.per_sm == 1 || most >= 3 * slot) break;
+  }
+  r.stages = most / slot < kMaxRing ? most / slot : kMaxRing;
+  r.smem = (size_t)r.stages * slot;
+  return r;
+}
+constexpr bool rings_fit() {
+  for (int H = kBackwardShort * 8 + 8; H <= kMaxNormDim; H += 8)
+    for (int residual = 0; residual < 2; ++residual) {
+      const RingPlan r = ring_plan(H, residual != 0);
+      if (r.stages < 2 || r.per_sm * (r.smem + kRingBeside) > kSmSmem) return false;
+    }
+  return true;
+}
+static_assert(rings_fit(), "the grid's CTAs are resident together");
+
+// How the gradient's kernel is launched.
 struct BackwardPlan {
   int lanes, vec;              // lanes 0: long rows
   int threads, blocks, stages;
@@ -568,14 +601,12 @@ BackwardPlan backward_plan(int T, int H, bool residual) {
     b.threads = kShortThreads;
     rows = ceil_div(T, kShortThreads / r.lanes);
   } else {
-    b.vec = nvec <= 1024 ? 2 : 4;
-    b.threads = round32((nvec + b.vec - 1) / b.vec);
-    const size_t slot = (size_t)H * 2 * (residual ? 3 : 2), most = 216 * 1024;
-    per_sm = 512 / b.threads;
-    while (per_sm > 1 && most / per_sm < 3 * slot) --per_sm;
-    b.stages = (int)(most / per_sm / slot);
-    if (b.stages > kMaxRing) b.stages = kMaxRing;
-    b.smem = b.stages * slot;
+    const RingPlan r = ring_plan(H, residual);
+    b.vec = r.vec;
+    b.threads = r.threads;
+    b.stages = r.stages;
+    b.smem = r.smem;
+    per_sm = r.per_sm;
   }
   const long long blocks = per_sm * num_sms();
   b.blocks = (int)(rows < blocks ? rows : blocks);
