@@ -554,8 +554,9 @@ int situ_and_mul_backward(const lmoe_bf16* in, const lmoe_bf16* grad_out, lmoe_b
 /* Expert e owns rows expert_offsets[e] .. expert_offsets[e+1] - 1 of the row  */
 /* matrices; expert_offsets [E+1] int32 on the device, ascending, within       */
 /* [0, rows] (entries outside are clamped on the device).  A row that no       */
-/* expert owns is neither read nor written.  w, grad_w [E, N, K] (lmoe_weights */
-/* w13: N = 2 inter, K = latent; w2: N = latent, K = inter).                   */
+/* expert owns is not written, and its values reach nothing.  w, grad_w        */
+/* [E, N, K] (lmoe_weights w13: N = 2 inter, K = latent; w2: N = latent,       */
+/* K = inter).                                                                */
 /*   lmoe_grouped_linear:            out[r,:]    = bf16( W_e x[r,:] )          */
 /*   lmoe_grouped_linear_backward_x: grad_x[r,:] = bf16( W_e^T grad_out[r,:] ) */
 /*   lmoe_grouped_linear_backward_w: grad_w[e]   = sum over the rows r of e of */
@@ -565,10 +566,14 @@ int situ_and_mul_backward(const lmoe_bf16* in, const lmoe_bf16* grad_out, lmoe_b
 /* fp32 or NULL, with grad_w only (LMOE_ERR_NULL otherwise), may be grad_w     */
 /* itself (a gradient summed over micro-batches).  Every element of grad_w is  */
 /* written, add or 0 for experts without rows (also with rows == 0).           */
-/* Products are summed on the tensor cores in fp32 and rounded once.  Those     */
-/* sums truncate: out and grad_x come out low by up to n/16 * 2^-24 of the sum  */
-/* of n magnitudes (n = K, N), at 65536 a tenth of a bf16 rounding; grad_w's    */
-/* are taken 512 rows at a time and joined by rounded additions.  Repeated      */
+/* Products are summed on the tensor cores in fp32 and rounded once.  Those    */
+/* sums truncate: a step of 16 products loses up to 5 * 2^-23 of the largest   */
+/* magnitude among them and the sum so far.  out and grad_x are off by up to   */
+/* n/16 * 5 * 2^-23 of the sum of n magnitudes (n = K, N), at n = 65536 six    */
+/* tenths of a bf16 rounding; n products of one sign come out about a sixth of */
+/* that low.  grad_w sums 256 rows so (512 with add) and joins them by rounded */
+/* additions: off by up to 1.0e-5 (2.0e-5) of the sum of magnitudes and half a */
+/* unit a join, of normal ones by 2.3e-7 (4.7e-7) of their norm.  Repeated     */
 /* calls give the same bits.  A NaN or infinity in a row reaches that row of   */
 /* out and grad_x, and the gradients of its expert's weights, alone.           */
 /* Requires 1 <= E <= 1024, N % 8 == 0, K % 8 == 0, 8 <= N, K <= 65536,         */

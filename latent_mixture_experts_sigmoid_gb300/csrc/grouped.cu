@@ -70,10 +70,10 @@ constexpr int kAcc = 2;                             // TMEM accumulators of 256 
 // weights: rows that the tensor cores add up before registers take over, whose additions round.  The
 // tensor cores' truncate: of a step of 16 terms each is cut to 2^-25 of the largest magnitude's power of
 // two, their sum to 2^-23 (seen with one term of 1 and others below it).  256 rows are off by 2.3e-7 of
-// their norm (normal ones; 3.1e-7, all of them low, for positive ones), 512 rows by 4.7e-7 (7.1e-7), any
-// number of rows by the same.  A read of TMEM every 2048 cycles of MMAs hides behind them but for the
-// registers that the addend takes: 65536 rows, 128 experts, 1024 x 2048, 256 / 512 rows: fp32 256 / 256 us,
-// bf16 204 / 204, with addend 467 / 437.
+// their norm (normal ones; 3.1e-7, all of them low, for positive ones), 512 rows by 4.7e-7 (7.1e-7), 65536
+// rows in such sums by 3.7e-7 and 5.0e-7.  A read of TMEM every 2048 cycles of MMAs hides behind them but for
+// the registers that the addend takes: 65536 rows, 128 experts, 1024 x 2048, 256 / 512 rows: fp32 256 / 256
+// us, bf16 204 / 204, with addend 467 / 437.
 template <int kOut>
 constexpr int kFlushRows = kOut == 2 ? 512 : 256;
 constexpr int kMaxStages = 8;

@@ -104,8 +104,9 @@ __device__ __forceinline__ bool wait_row(uint32_t bar, uint32_t parity) {
 // A row's loads are one burst, so that CTAs in number hide its latencies; packed fp32 throughout (one
 // by one, at 29 instructions an element, the kernel was bound by their issue).
 // [4096, 7168] with residual and both outputs: 41 us (265 MB, 6.4 TB/s), codes alone without a residual
-// 23 us (their floor is 13: too little per row to load); [1, 7168]: 2.2 us.  Rows walked by few CTAs
-// through a ring of copies as in the gradient: 49 us.
+// 23 us (their floor is 13: 64 registers a thread leave room for four rows an SM, and without a residual each
+// has half the bytes on their way); [1, 7168]: 2.2 us.  Rows walked by few CTAs through a ring of copies as
+// in the gradient: 49 us.
 template <int kVec, int kLanes, bool kRes>
 __global__ void __launch_bounds__(kLanes ? 256 : kVec == 4 ? 512 : 1024, kLanes == 0 && kVec == 4 ? 2 : 1)
 norm_kernel(const NormForward p) {
@@ -409,8 +410,9 @@ norm_backward_few_kernel(const NormBackward p) {
 // ring in shared memory meanwhile, as bulk copies that one thread issues: their bytes in flight do
 // not depend on how many warps the registers leave room for.  The barrier of a row's sums says that
 // the slot of the row before has been read.
-// [16384, 7168] with grad_residual: 144 us with the join (940 MB, 6.5 TB/s); one CTA an SM without the
-// ring took 229.  [16384, 2048]: 64 us for 40 us of bytes, a row's chain of latencies.
+// [16384, 7168] with grad_residual: 147 us with the join (940 MB, 6.4 TB/s); one CTA an SM without the
+// ring took 229.  [16384, 2048]: 66 us for 40 us of bytes, [8192, 16384] 243 for 158: a row's chain of
+// latencies on the 512 threads an SM that the registers leave room for.
 template <int kVec>
 __global__ void __launch_bounds__(512)
 norm_backward_kernel(const NormBackward p, int stages) {
@@ -468,7 +470,7 @@ norm_backward_kernel(const NormBackward p, int stages) {
         dv[i] = slot[nvec + j];
       }
     }
-    if constexpr (kVec == 4) load_weights();     // (kept, they spill)
+    if constexpr (kVec == 4) load_weights();     // (kept, 384 bytes a thread spill; as it is, 248)
     const RowFactors f = factors_of<kVec, 0>(hv, dv, wv, (float)p.H, inv_H, p.eps, slots[flip], slots[2 + flip]);
     if (*(volatile int*)&abort_flag) break;      // (set ahead of the barrier in factors_of: for all)
     const int last = s ? s - 1 : stages - 1;
@@ -585,6 +587,9 @@ constexpr bool rings_fit() {
 static_assert(rings_fit(), "the grid's CTAs are resident together");
 
 // How the gradient's kernel is launched.
+// Short rows: four CTAs an SM, of which the registers let three be resident (two of rows of 264 and more), not fitted yet:
+// times in us with four / three / two, grad_residual too: [65536, 64] 11.3 / 11.0 / 10.8, [65536, 128]
+// 17.3 / 13.1 / 16.6, [65536, 256] 35.7 / 28.0 / 34.7, [65536, 512] 48.8 / 55.0 / 47.4.
 struct BackwardPlan {
   int lanes, vec;              // lanes 0: long rows
   int threads, blocks, stages;
@@ -686,6 +691,11 @@ cudaError_t launch_norm(const NormForward& n, cudaStream_t s) {
                         : launch_norm_as<4, 32>(n, grid, kShortThreads, s);
   }
   const dim3 grid((unsigned)n.T);
+  // Up to two rows an SM: as many threads a row as it has vectors, beyond that a quarter of them with four
+  // each, so that more rows fit (us, many threads / four vectors, both outputs with a residual:
+  // [16, 7168] 2.1 / 2.4, [304, 7168] 3.25 / 3.23, [608, 7168] 5.8 / 4.7, [4096, 7168] 45.5 / 40.7;
+  // [16, 2048] 1.6 / 2.1, [304, 2048] 2.0 / 2.2, [1024, 2048] 3.6 / 4.7, [4096, 2048] 9.8 / 8.1;
+  // [152, 16384] 3.6 / 3.7, [304, 16384] 7.0 / 5.4, [608, 16384] 14.0 / 10.8).
   if (n.T <= 2 * num_sms())
     return nvec <= 1024 ? launch_norm_as<1, 0>(n, grid, round32(nvec), s)
                         : launch_norm_as<2, 0>(n, grid, round32((nvec + 1) / 2), s);

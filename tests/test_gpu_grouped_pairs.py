@@ -244,3 +244,23 @@ def test_each_product_of_a_step_with_many_rows():
         dy, x = f64(dy), f64(x)
         ref, mag = O.grouped_linear_backward_w(dy, x, off), O.grouped_linear_backward_w(np.abs(dy), np.abs(x), off)
         assert np.all(np.abs(f64(got) - ref) <= 2.0 ** -24 * np.abs(ref) + slack_w(counts) * mag)
+
+
+@pytest.mark.parametrize("R", [1, 16384])
+@pytest.mark.parametrize("K", [16, 64, 256, 1024, 4096])
+def test_sums_keep_the_documented_bound(R, K):
+    # Terms 1, p, ..., p, -1: what the sums lose of the p is not hidden by the output's rounding.  Each
+    # of K / 16 steps loses 5 units of 2^-23 of the largest magnitude, here a power of two up to twice
+    # 1 + (K - 2) p; both kernels (few rows, pairs of SMs).
+    p = 0.9921875 * 2.0 ** torch.arange(-16, -32, -1, dtype=torch.float64)
+    w = p[:, None].repeat(1, K)
+    w[:, 0], w[:, -1] = 1.0, -1.0
+    w = w.to(torch.bfloat16).to("cuda")[None]
+    if R > 1:
+        on_pairs(R, 16, K)
+    x = torch.ones((R, K), dtype=torch.bfloat16, device="cuda")
+    y = torch.empty((R, 16), dtype=torch.bfloat16, device="cuda")
+    lm.lmoe_grouped_linear(x, w, offsets([R]), y)
+    ref = f64(w)[0].sum(1)
+    bound = K / 16 * 5 * 2.0 ** -23 * (1 + (K - 2) * p.numpy()) + BF16 * (1 + 2 ** -7) * np.abs(ref)
+    assert np.all(np.abs(f64(y) - ref) <= bound), (np.abs(f64(y) - ref) / bound).max()
