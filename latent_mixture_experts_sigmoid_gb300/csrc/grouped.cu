@@ -16,9 +16,9 @@
 // descriptors: nothing is transposed in memory.
 //
 // Where the token rows are the sum's index (weights), an expert's last block of 64 may have fewer rows,
-// and those behind them, the next expert's, have to read as zeros.  (Both operands': 0 times another
-// expert's NaN is NaN.)  The copies fill them in: the tensor maps count a row twice, as j of 64 from row
-// i on, so that a box of 64 from j = -(64 - left) has its first 64 - left rows outside the map.  Zeros
+// and those behind them up to the next 16, the next expert's, have to read as zeros.  (Both operands': 0
+// times another expert's NaN is NaN.)  The copies bring them, too: boxes of 16, 4 and 1 rows make up the
+// expert's own, boxes of 4 and 1 rows behind the last row of all, outside the tensor map, the zeros.  Zeros
 // that threads write (a barrier of the CTA's own, a warp that clears the rows and passes the block on)
 // have to be released to the other CTA's MMAs in cluster scope: fp32 331 us, bf16 271 at the case below.
 //
@@ -295,12 +295,16 @@ __device__ __forceinline__ void load_addend(const Params& p, const Tile& x, int 
   }
 }
 
+// part: boxes of fewer rows.  forward, rows: kPartBox of b; weights: 16, 4 and 1 of a and of b
+template <int kMode>
+struct Maps {
+  CUtensorMap a, b, o, part[kMode == kWeights ? 6 : 1];
+};
+
 // kOut (weights): 0 fp32, 1 bf16, 2 fp32 with an addend
 template <int kMode, int kOut>
 __global__ void __launch_bounds__(kThreads, 1)
-grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ CUtensorMap tmB,
-               const __grid_constant__ CUtensorMap tmBp, const __grid_constant__ CUtensorMap tmO,
-               const Params p) {
+grouped_kernel(const __grid_constant__ Maps<kMode> maps, const Params p) {
   constexpr bool kAK = kMode == kForward, kBK_ = kMode != kWeights;   // K-major operands
   constexpr int kFlush = kFlushRows<kOut>;
   extern __shared__ uint8_t smem_raw[];
@@ -382,31 +386,48 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           if (!ok) break;
           const uint32_t at = smem_u32(smem) + (uint32_t)s * p.stage_bytes, bt = at + kABytes;
           const int k = kb * kBK;
-          const int skip = min(x.rows - k - kBK, 0);   // (weights: minus the zero rows ahead of an expert's last)
+          const int left = x.rows - k;                 // (weights)
+          const bool part = kMode == kWeights && left < kBK;
+          const int filled = part ? (left + 15) & ~15 : kBK;
           if (elect_one()) {
             const uint32_t bar = cluster_addr(bar_at(kFull + s), 0);
             if (rank == 0) {
-              const uint32_t bytes = kMode == kWeights ? (uint32_t)(2 + nchunk) * kChunk
+              const uint32_t bytes = kMode == kWeights ? (uint32_t)((2 + nchunk) * filled) * 128u
                                                        : kABytes + (uint32_t)(nbox * brows) * 128u;
               mbar_arrive_expect_tx(bar_at(kFull + s), 2 * bytes);
             }
             if constexpr (kMode == kForward) {
-              tma_load_pair_3d(&tmA, at, bar, k, m, x.group);
+              tma_load_pair_3d(&maps.a, at, bar, k, m, x.group);
             } else if constexpr (kMode == kRows) {
-              tma_load_pair_3d(&tmA, at, bar, m, k, x.group);
-              tma_load_pair_3d(&tmA, at + kChunk, bar, m + 64, k, x.group);
-            } else {
-              tma_load_pair_3d(&tmA, at, bar, m, skip, x.row0 + k);
-              tma_load_pair_3d(&tmA, at + kChunk, bar, m + 64, skip, x.row0 + k);
+              tma_load_pair_3d(&maps.a, at, bar, m, k, x.group);
+              tma_load_pair_3d(&maps.a, at + kChunk, bar, m + 64, k, x.group);
             }
-            if constexpr (kMode == kWeights) {
-              tma_load_pair_3d(&tmB, bt, bar, n0, skip, x.row0 + k);
-              if (nchunk > 1) tma_load_pair_3d(&tmB, bt + kChunk, bar, n0 + 64, skip, x.row0 + k);
-            } else if (whole) {
-              tma_load_pair(&tmB, bt, bar, k, tok);
+            if constexpr (kMode != kWeights) {
+              if (whole) {
+                tma_load_pair(&maps.b, bt, bar, k, tok);
+              } else {
+                for (int i = 0; i < nbox; ++i)
+                  tma_load_pair(&maps.part[0], bt + (uint32_t)(i * brows) * 128u, bar, k, tok + i * brows);
+              }
             } else {
-              for (int i = 0; i < nbox; ++i)
-                tma_load_pair(&tmBp, bt + (uint32_t)(i * brows) * 128u, bar, k, tok + i * brows);
+              // a box of both operands: to row r of the block
+              auto box = [&](const CUtensorMap* a, const CUtensorMap* b, int r, int row) {
+                tma_load_pair(a, at + r * 128u, bar, m, row);
+                tma_load_pair(a, at + kChunk + r * 128u, bar, m + 64, row);
+                tma_load_pair(b, bt + r * 128u, bar, n0, row);
+                if (nchunk > 1) tma_load_pair(b, bt + kChunk + r * 128u, bar, n0 + 64, row);
+              };
+              const int row0 = x.row0 + k, beyond = (int)p.R;
+              if (!part) {
+                box(&maps.a, &maps.b, 0, row0);
+              } else {
+                int r = 0;
+                for (; r + 16 <= left; r += 16) box(&maps.part[0], &maps.part[1], r, row0 + r);
+                for (; r + 4 <= left; r += 4) box(&maps.part[2], &maps.part[3], r, row0 + r);
+                for (; r < left; ++r) box(&maps.part[4], &maps.part[5], r, row0 + r);
+                for (; r & 3; ++r) box(&maps.part[4], &maps.part[5], r, beyond);
+                for (; r < filled; r += 4) box(&maps.part[2], &maps.part[3], r, beyond);
+              }
             }
           }
           __syncwarp();
@@ -447,13 +468,12 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
             const uint64_t da = a0 + (uint64_t)s * (p.stage_bytes >> 4), db = b0 + (uint64_t)s * (p.stage_bytes >> 4);
             const uint32_t d = tmem_base + acc * kTile;
             const bool last = k + kBK >= depth || (kMode == kWeights && (k + kBK) % kFlush == 0);
-            // (weights: not the groups of zeros in front; the others' blocks are whole or end in zeros)
-            const int j0 = kMode == kWeights ? max(kBK - (depth - k), 0) >> 4 : 0;
             if (elect_one()) {
 #pragma unroll
               for (int j = 0; j < kBK / 16; ++j)
-                if (kMode != kWeights || j >= j0)
-                  mma_pair(d, da + j * kStep<kAK>, db + j * kStep<kBK_>, id, j > j0 ? 1u : (uint32_t)!fresh);
+                // (weights: not past the zeros; the others' blocks are whole or filled up with zeros)
+                if (kMode != kWeights || k + 16 * j < depth)
+                  mma_pair(d, da + j * kStep<kAK>, db + j * kStep<kBK_>, id, j ? 1u : (uint32_t)!fresh);
               commit_both(bar_at(kEmpty + s));
               if (last) commit_both(bar_at(kTfull + (int)acc));
             }
@@ -597,7 +617,7 @@ grouped_kernel(const __grid_constant__ CUtensorMap tmA, const __grid_constant__ 
           fence_proxy_async_smem();
           __syncwarp();
           if (lane == 0) {
-            if (m < p.mdim && col < p.ncols) tma_store_3d(&tmO, smem_u32(box), col, m, x.group);
+            if (m < p.mdim && col < p.ncols) tma_store_3d(&maps.o, smem_u32(box), col, m, x.group);
             bulk_commit();
           }
         }
@@ -624,27 +644,20 @@ typedef CUresult (*EncodeTiledFn)(CUtensorMap*, CUtensorMapDataType, cuuint32_t,
                                   CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
 // [groups, rows, cols], or (groups = 0) [rows, cols], in boxes of box_rows rows of 128 bytes, 128-byte
-// swizzle; elements outside read as zeros and are not written.
+// swizzle; elements outside read as zeros and are not written
 bool make_map(CUtensorMap* m, const void* base, bool fp32, long long groups, long long rows, int cols,
-              int box_rows, bool runs = false) {
+              int box_rows) {
   const EncodeTiledFn enc = reinterpret_cast<EncodeTiledFn>(tensor_map_encoder());
   if (!enc) return false;
   const cuuint64_t size = fp32 ? 4 : 2;
   cuuint64_t dims[3] = {(cuuint64_t)cols, (cuuint64_t)rows, (cuuint64_t)groups};
-  cuuint64_t strides[2] = {(cuuint64_t)cols * size, (cuuint64_t)cols * size * (cuuint64_t)(runs ? 1 : rows)};
+  cuuint64_t strides[2] = {(cuuint64_t)cols * size, (cuuint64_t)cols * size * (cuuint64_t)rows};
   cuuint32_t box[3] = {(cuuint32_t)(128 / size), (cuuint32_t)box_rows, 1};
   cuuint32_t estr[3] = {1, 1, 1};
   return enc(m, fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16,
              groups ? 3 : 2, const_cast<void*>(base), dims, strides, box, estr,
              CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
-}
-
-// [rows, cols] as runs of kBK rows: row j of the run from row i is row i + j (the two strides are one).  j
-// < 0 and j >= kBK read as zeros.  (A run that goes past the last row is in the map and outside the
-// memory: boxes end with an expert's last row.)
-bool make_runs(CUtensorMap* m, const void* base, long long rows, int cols) {
-  return make_map(m, base, false, rows, kBK, cols, kBK, true);
 }
 
 constexpr size_t kMaxSmem = 227 * 1024;
@@ -689,12 +702,8 @@ int pairs_resident() {
   return cache[dev] = n;
 }
 
-struct Maps {
-  CUtensorMap a, b, bp, o;
-};
-
 template <int kMode, int kOut>
-cudaError_t launch(const Maps& m, Params& p, long long units, cudaStream_t s) {
+cudaError_t launch(const Maps<kMode>& m, Params& p, long long units, cudaStream_t s) {
   const int pairs = pairs_resident<kMode, kOut>();
   if (pairs < 1) return cudaErrorInvalidConfiguration;
   p.err = device_error_word();
@@ -703,8 +712,7 @@ cudaError_t launch(const Maps& m, Params& p, long long units, cudaStream_t s) {
   p.stages = (int)((kMaxSmem - other) / p.stage_bytes);
   if (p.stages > kMaxStages) p.stages = kMaxStages;
   return launch_k_cluster(grouped_kernel<kMode, kOut>, dim3(2 * (unsigned)(units < pairs ? units : pairs)),
-                          dim3(kThreads), other + (size_t)p.stages * p.stage_bytes, s, 2, m.a, m.b, m.bp,
-                          m.o, p);
+                          dim3(kThreads), other + (size_t)p.stages * p.stage_bytes, s, 2, m, p);
 }
 
 // Whether few rows stream through registers (grouped_stream.cu), by what both forms take in
@@ -743,15 +751,15 @@ cudaError_t launch_grouped_linear(const GroupedLinear& g, bool backward, cudaStr
   p.R = g.R;
   p.offsets = g.offsets;
   p.out = g.rows_out;
-  Maps m;
-  if (!make_map(&m.a, g.w, false, g.E, g.N, g.K, backward ? kBK : kHalf) ||
-      !make_map(&m.b, g.rows_in, false, 0, g.R, p.depth, p.nt / 2) ||
-      !make_map(&m.bp, g.rows_in, false, 0, g.R, p.depth, kPartBox))
+  CUtensorMap a, b, part;
+  if (!make_map(&a, g.w, false, g.E, g.N, g.K, backward ? kBK : kHalf) ||
+      !make_map(&b, g.rows_in, false, 0, g.R, p.depth, p.nt / 2) ||
+      !make_map(&part, g.rows_in, false, 0, g.R, p.depth, kPartBox))
     return cudaErrorInvalidValue;
-  m.o = m.a;
   // token tiles: one a started nt rows and expert at most
   const long long units = (g.R / p.nt + (g.R < g.E ? g.R : g.E)) * p.mtiles;
-  return backward ? launch<kRows, 0>(m, p, units, s) : launch<kForward, 0>(m, p, units, s);
+  return backward ? launch<kRows, 0>({a, b, a, {part}}, p, units, s)
+                  : launch<kForward, 0>({a, b, a, {part}}, p, units, s);
 }
 
 cudaError_t launch_grouped_weight_grad(const GroupedWeightGrad& g, cudaStream_t s) {
@@ -765,12 +773,14 @@ cudaError_t launch_grouped_weight_grad(const GroupedWeightGrad& g, cudaStream_t 
   p.R = g.R;
   p.offsets = g.offsets;
   p.add = g.add;
-  Maps m;
+  Maps<kWeights> m;
   const bool fp32 = g.dw != nullptr;
-  if (!make_runs(&m.a, g.dy, g.R, g.N) || !make_runs(&m.b, g.x, g.R, g.K) ||
-      !make_map(&m.o, fp32 ? (const void*)g.dw : g.dw_bf16, fp32, g.E, g.N, g.K, 32))
-    return cudaErrorInvalidValue;
-  m.bp = m.b;
+  bool ok = make_map(&m.a, g.dy, false, 0, g.R, g.N, kBK) && make_map(&m.b, g.x, false, 0, g.R, g.K, kBK) &&
+            make_map(&m.o, fp32 ? (const void*)g.dw : g.dw_bf16, fp32, g.E, g.N, g.K, 32);
+  for (int i = 0; ok && i < 3; ++i)
+    ok = make_map(&m.part[2 * i], g.dy, false, 0, g.R, g.N, 16 >> 2 * i) &&
+         make_map(&m.part[2 * i + 1], g.x, false, 0, g.R, g.K, 16 >> 2 * i);
+  if (!ok) return cudaErrorInvalidValue;
   const long long units = (long long)p.E * p.mtiles * p.ntiles;
   if (!fp32) return launch<kWeights, 1>(m, p, units, s);
   return p.add ? launch<kWeights, 2>(m, p, units, s) : launch<kWeights, 0>(m, p, units, s);

@@ -586,10 +586,10 @@ constexpr bool rings_fit() {
 }
 static_assert(rings_fit(), "the grid's CTAs are resident together");
 
-// How the gradient's kernel is launched.
-// Short rows: four CTAs an SM, of which the registers let three be resident (two of rows of 264 and more), not fitted yet:
-// times in us with four / three / two, grad_residual too: [65536, 64] 11.3 / 11.0 / 10.8, [65536, 128]
-// 17.3 / 13.1 / 16.6, [65536, 256] 35.7 / 28.0 / 34.7, [65536, 512] 48.8 / 55.0 / 47.4.
+// How the gradient's kernel is launched.  Short rows: four CTAs an SM, of which the registers let three be
+// resident (two of rows of 264 and more), not fitted yet: times in us with four / three / two, with
+// grad_residual: [65536, 64] 11.3 / 11.0 / 10.8, [65536, 128] 17.3 / 13.1 / 16.6, [65536, 256]
+// 35.7 / 28.0 / 34.7, [65536, 512] 48.8 / 55.0 / 47.4.
 struct BackwardPlan {
   int lanes, vec;              // lanes 0: long rows
   int threads, blocks, stages;
