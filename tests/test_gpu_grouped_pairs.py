@@ -264,3 +264,43 @@ def test_sums_keep_the_documented_bound(R, K):
     ref = f64(w)[0].sum(1)
     bound = K / 16 * 5 * 2.0 ** -23 * (1 + (K - 2) * p.numpy()) + BF16 * (1 + 2 ** -7) * np.abs(ref)
     assert np.all(np.abs(f64(y) - ref) <= bound), (np.abs(f64(y) - ref) / bound).max()
+
+
+EDGES = """
+import torch, latent_mixture_experts_sigmoid_gb300 as lm
+lm.load_library()
+# matrices that fill their pieces of device memory to the byte (2 MB ones), with short experts at both ends
+R, N, K = 16384, 512, 1024
+x, dy = (torch.empty((R, c), dtype=torch.bfloat16, device="cuda") for c in (K, N))
+for t in (x, dy):
+    t.normal_()
+counts = [3, 5, 1, 17, 40, 0, 63, 64, 65, 1000]
+tail = [90, 64, 31, 1, 0, 16, 7, 2]
+counts += [R - sum(counts) - sum(tail)] + tail
+E = len(counts)
+off = torch.tensor([0] + counts, device="cuda").cumsum(0).to(torch.int32)
+dw = torch.empty((E, N, K), device="cuda")
+half, w, y, dx = torch.empty_like(dw, dtype=torch.bfloat16), torch.randn((E, N, K), device="cuda").bfloat16(), torch.empty_like(dy), torch.empty_like(x)
+lm.lmoe_grouped_linear_backward_w(dy, x, off, dw)
+lm.lmoe_grouped_linear_backward_w(dy, x, off, half)
+lm.lmoe_grouped_linear(x, w, off, y)
+lm.lmoe_grouped_linear_backward_x(dy, w, off, dx)
+torch.cuda.synchronize()
+assert lm.lmoe_device_error() == 0
+a = 0
+for e, n in enumerate(counts):
+    d, v = dy[a:a + n].double(), x[a:a + n].double()
+    a += n
+    ref, mag = d.T @ v, d.abs().T @ v.abs()
+    slack = ((min(n, 512) / 16 + 2) * 2.0 ** -23 + n / 512 * 2.0 ** -24) * mag
+    assert bool(((dw[e].double() - ref).abs() <= 2.0 ** -24 * ref.abs() + slack).all()), e
+    assert bool(((half[e].double() - ref).abs() <= 2.0 ** -8 * ref.abs() + slack).all()), e
+assert bool(torch.isfinite(y.float()).all()) and bool(torch.isfinite(dx.float()).all())
+"""
+
+
+def test_matrices_that_fill_their_memory():
+    # in a process of its own, whose first large allocations they are: what is read or written ahead of
+    # them or behind them is no memory
+    r = subprocess.run([sys.executable, "-c", EDGES], cwd=ROOT, capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stderr[-2000:]

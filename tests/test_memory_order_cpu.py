@@ -47,3 +47,14 @@ def test_in_place_operands_are_not_read_as_constant():
         assert ".nc" not in re.search(r"uint4 " + name + r"\(.*?\n}", situ, re.S)[0], name
     norm = source("norm.cu")
     assert ".nc" not in norm and "__ldg" not in norm
+
+
+def test_tensor_maps_have_the_documented_form():
+    # each stride is the one before times its extent (a map with two equal strides counts rows twice
+    # and covers memory that its matrix does not have), and no copy of token rows begins ahead of them
+    grouped = source("grouped.cu")
+    strides = re.findall(r"cuuint64_t strides\[\d\] = \{(.*?)\};", grouped)
+    assert strides == ["(cuuint64_t)cols * size, (cuuint64_t)cols * size * (cuuint64_t)rows"]
+    producer = grouped[grouped.index("TMA producer ---"):grouped.index("MMA issuer of the pair")]
+    rows = set(re.findall(r"box\(&maps\.\S+, &maps\.\S+, \w+, ([^)]*)\)", producer))
+    assert rows == {"row0", "row0 + r", "beyond"} and "const int row0 = x.row0 + k, beyond = (int)p.R;" in producer
