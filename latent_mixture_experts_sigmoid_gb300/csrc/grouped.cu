@@ -21,6 +21,8 @@
 // expert's own, boxes of 4 and 1 rows behind the last row of all, outside the tensor map, the zeros.  Zeros
 // that threads write (a barrier of the CTA's own, a warp that clears the rows and passes the block on)
 // have to be released to the other CTA's MMAs in cluster scope: fp32 331 us, bf16 271 at the case below.
+// (Boxes of every power of two up to 16 or 32: 264 us and 212 there, but 896 experts 1412 and 758 for 1412
+// and 660, and a small call 1 us more for the maps.)
 //
 //   warp 0      TMA producer of this CTA's halves; their bytes count on the leader's (rank 0's)
 //               barrier
@@ -40,8 +42,8 @@
 //                 with uneven ones: a tile of fewer than 256 rows brings in more bytes per MMA cycle
 //   rows          65536 over 128 experts, 2048 x 512: 107 us (604 MB, 5.6 TB/s; 1.28 PFLOP/s) where the tiles
 //                 are eight rounds of the 76 pairs, 117 to 118 where they are nine: both, and the rounds
-//   weights       65536 rows over 128 experts, 1024 x 2048: fp32 256 us, with addend 437 (2.55 GB,
-//                 5.8 TB/s), bf16 204: memory, and the latency of the rows against a ring of six stages
+//   weights       65536 rows over 128 experts, 1024 x 2048: fp32 269 us, with addend 438 (2.55 GB,
+//                 5.8 TB/s), bf16 215; with 512 rows each 245, 435, 195: memory, and the latency of the rows against a ring of six stages
 //                 (one stage fewer: 16 % more in fp32, 8 % in bf16)
 // Taking tiles over from clusters that have not started (cluster launch control) was no faster than
 // tile u on pair u mod pairs, L2 prefetches of the next tile's rows or addend were slower.
@@ -72,8 +74,8 @@ constexpr int kAcc = 2;                             // TMEM accumulators of 256 
 // two, their sum to 2^-23 (seen with one term of 1 and others below it).  256 rows are off by 2.3e-7 of
 // their norm (normal ones; 3.1e-7, all of them low, for positive ones), 512 rows by 4.7e-7 (7.1e-7), 65536
 // rows in such sums by 3.7e-7 and 5.0e-7.  A read of TMEM every 2048 cycles of MMAs hides behind them but for
-// the registers that the addend takes: 65536 rows, 128 experts, 1024 x 2048, 256 / 512 rows: fp32 256 / 256
-// us, bf16 204 / 204, with addend 467 / 437.
+// the registers that the addend takes: 65536 rows, 128 experts, 1024 x 2048, 256 / 512 rows: fp32 269 / 268
+// us, bf16 215 / 215, with addend 469 / 438.
 template <int kOut>
 constexpr int kFlushRows = kOut == 2 ? 512 : 256;
 constexpr int kMaxStages = 8;
